@@ -56,7 +56,11 @@ typedef enum {
     QG_BF16 = 1,
     QG_INT32 = 2,
     QG_INT8 = 3,
-    QG_UINT8 = 4
+    QG_UINT8 = 4,
+    /* only in qgemm_mx.h */
+    QG_FP16 = 5,
+    QG_MXFP8 = 6,   /* e4m3 elements, a power-of-two scale per 32 */
+    QG_MXFP4 = 7    /* e2m1 elements, a power-of-two scale per 32 */
 } qg_dtype;
 
 /* Operation ids for qgemm_workspace_bytes. */

@@ -24,6 +24,18 @@ this package is its thin Python binding, with the same call names:
 * ``dynamic_quantize_linear(x)``: ONNX DynamicQuantizeLinear to uint8,
   returning (y, scale, zero_point) on the device.
 
+Around the products (``include/qgemm_mx.h``):
+
+* ``rms_norm_quantize(x, weight, eps, residual, format)``: root-mean-square
+  norm with the residual's addition, to int8 with a scale per row (the left
+  operand of ``qgemm_a8w8``) or to MXFP8 / MXFP4 (that of ``mx_matmul``);
+  ``rms_norm`` is the same with a floating output, ``rms_norm_grad`` its
+  gradient.
+* ``mx_quantize(x, format="mxfp4")`` and ``mx_dequantize(codes, scale)``:
+  microscaled formats, a power-of-two scale per 32 values, and back.
+* ``mx_matmul(A, a_scale, W, w_scale, act_scale=None)``: MXFP8 or MXFP4
+  activations times an MXFP4 weight.
+
 ``calib_read``, ``calib_mfma_i8``, ``calib_mfma_f32`` and ``calib_mfma_bf16``
 measure the machine's HBM read and int8, fp32 and bf16 matrix-core ceilings
 for the roofline figures.
@@ -53,4 +65,13 @@ from ._binding import (  # noqa: F401
     status_string,
     version,
     workspace_bytes,
+)
+from ._mx import (  # noqa: F401
+    mx_dequantize,
+    mx_matmul,
+    mx_matmul_workspace_bytes,
+    mx_quantize,
+    rms_norm,
+    rms_norm_grad,
+    rms_norm_quantize,
 )

@@ -38,6 +38,11 @@ SOURCES = [
     "conv_integer.hip",
     "conv_implicit.hip",
     "calibrate.hip",
+    "rms_norm.hip",
+    "rms_norm_grad.hip",
+    "mx_quantize.hip",
+    "mx_matmul_bytes.hip",
+    "mx_api.cpp",
     "api.cpp",
 ]
 

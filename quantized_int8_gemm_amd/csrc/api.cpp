@@ -12,6 +12,7 @@
 
 #include "../../include/qgemm.h"
 #include "kernels.h"
+#include "mx_kernels.h"
 
 namespace {
 
@@ -190,6 +191,10 @@ hipError_t launch_tiled(const qg::Int8GemmArgs& a, int cfg, bool bkm, bool vec, 
 }
 
 }  // namespace
+
+namespace qg {
+void record_kernel(const char* name) { g_last_kernel = name; }
+}  // namespace qg
 
 extern "C" {
 

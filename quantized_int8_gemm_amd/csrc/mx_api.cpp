@@ -1,0 +1,164 @@
+// C entry points of qgemm_mx.h: argument checks (before any HIP call), kernel
+// choice and launch, with the launch-status convention of api.cpp.
+#include <cmath>
+#include <cstdlib>
+#include <cstring>
+
+#include <hip/hip_runtime.h>
+
+#include "mx_kernels.h"
+
+namespace {
+
+constexpr int64_t LIM = (int64_t)1 << 30;
+
+bool is_float(qg_dtype t) { return t == QG_FP32 || t == QG_BF16 || t == QG_FP16; }
+bool is_mx(qg_dtype t) { return t == QG_MXFP8 || t == QG_MXFP4; }
+int64_t blocks_of(int64_t n) { return (n + 31) / 32; }
+int64_t code_bytes(qg_dtype f, int64_t n) { return blocks_of(n) * (f == QG_MXFP8 ? 32 : 16); }
+
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+bool aligned_for(const void* p, qg_dtype t) { return aligned(p, t == QG_FP32 ? 4 : 2); }
+
+qg_status done(hipError_t e, const char* name) {
+    if (e != hipSuccess) return QG_ERR_HIP;
+    qg::record_kernel(name);
+    return QG_OK;
+}
+
+qg_status nothing() {
+    qg::record_kernel("none");
+    return QG_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+qg_status rms_norm(int64_t M, int64_t n, const void* x, qg_dtype type, int64_t ldx, const void* residual,
+                   int64_t ld_residual, const void* weight, qg_dtype weight_type, float eps, void* h, int64_t ldh,
+                   void* out, qg_dtype format, int64_t ldo, uint8_t* block_scale, int64_t ld_block_scale,
+                   float* row_scale, void* stream) {
+    if (M < 0 || M >= LIM || n < 1 || n >= LIM) return QG_ERR_INVALID_ARGUMENT;
+    if (!is_float(type) || (weight_type != type && weight_type != QG_FP32)) return QG_ERR_INVALID_ARGUMENT;
+    if (!(format == QG_INT8 || is_mx(format) || format == QG_FP32 || format == type)) return QG_ERR_INVALID_ARGUMENT;
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return QG_ERR_INVALID_ARGUMENT;
+    if (n > QG_RMS_NORM_MAX_COLUMNS) return QG_ERR_UNSUPPORTED;
+    if (M == 0) return nothing();
+    if (x == nullptr || weight == nullptr || out == nullptr || ldx < n) return QG_ERR_INVALID_ARGUMENT;
+    if (residual != nullptr && (h == nullptr || ld_residual < n || ldh < n)) return QG_ERR_INVALID_ARGUMENT;
+    if (!aligned_for(x, type) || !aligned_for(residual, type) || !aligned_for(weight, weight_type) ||
+        (residual != nullptr && !aligned_for(h, type)))
+        return QG_ERR_INVALID_ARGUMENT;
+    if (is_mx(format)) {
+        if (block_scale == nullptr || ld_block_scale < blocks_of(n) || ldo < code_bytes(format, n))
+            return QG_ERR_INVALID_ARGUMENT;
+    } else {
+        if (ldo < n || (format != QG_INT8 && !aligned_for(out, format))) return QG_ERR_INVALID_ARGUMENT;
+    }
+    if ((format == QG_INT8 || is_mx(format)) && row_scale == nullptr) return QG_ERR_INVALID_ARGUMENT;
+    if (!aligned(row_scale, 4)) return QG_ERR_INVALID_ARGUMENT;
+    (void)hipGetLastError();
+    const qg::RmsNormArgs a{M, (int)n, x, ldx, residual, ld_residual, weight, eps, h, ldh,
+                            out, ldo, block_scale, ld_block_scale, row_scale};
+    const char* name = "";
+    const hipError_t e = qg::launch_rms_norm(a, type, weight_type == QG_FP32, format, (hipStream_t)stream, &name);
+    return done(e, name);
+}
+
+size_t rms_norm_grad_workspace_bytes(int64_t M, int64_t n) {
+    if (M < 1 || M >= LIM || n < 1 || n > QG_RMS_NORM_MAX_COLUMNS) return 0;
+    return (size_t)qg::rms_norm_grad_parts(M, n) * (size_t)n * 4;
+}
+
+qg_status rms_norm_grad(int64_t M, int64_t n, const void* dy, qg_dtype type, int64_t ld_dy, const void* h, int64_t ldh,
+                        const void* weight, qg_dtype weight_type, const float* rstd, const void* dh, int64_t ld_dh,
+                        void* dx, int64_t ld_dx, void* dweight, void* workspace, size_t workspace_bytes, void* stream) {
+    if (M < 0 || M >= LIM || n < 1 || n >= LIM) return QG_ERR_INVALID_ARGUMENT;
+    if (!is_float(type) || (weight_type != type && weight_type != QG_FP32)) return QG_ERR_INVALID_ARGUMENT;
+    if (n > QG_RMS_NORM_MAX_COLUMNS) return QG_ERR_UNSUPPORTED;
+    if (dweight == nullptr || !aligned_for(dweight, weight_type)) return QG_ERR_INVALID_ARGUMENT;
+    if (M > 0) {
+        if (dy == nullptr || h == nullptr || weight == nullptr || rstd == nullptr || dx == nullptr)
+            return QG_ERR_INVALID_ARGUMENT;
+        if (ld_dy < n || ldh < n || ld_dx < n || (dh != nullptr && ld_dh < n)) return QG_ERR_INVALID_ARGUMENT;
+        if (!aligned_for(dy, type) || !aligned_for(h, type) || !aligned_for(dh, type) || !aligned_for(dx, type) ||
+            !aligned_for(weight, weight_type) || !aligned(rstd, 4))
+            return QG_ERR_INVALID_ARGUMENT;
+        if (workspace == nullptr || !aligned(workspace, 16)) return QG_ERR_INVALID_ARGUMENT;
+        if (workspace_bytes < rms_norm_grad_workspace_bytes(M, n)) return QG_ERR_WORKSPACE;
+    }
+    (void)hipGetLastError();
+    const qg::RmsNormGradArgs a{M, (int)n, dy, ld_dy, h, ldh, weight, rstd, dh, ld_dh, dx, ld_dx, dweight,
+                                (float*)workspace, qg::rms_norm_grad_parts(M, n)};
+    const char* name = "";
+    const hipError_t e = qg::launch_rms_norm_grad(a, type, weight_type == QG_FP32, (hipStream_t)stream, &name);
+    return done(e, name);
+}
+
+qg_status mx_quantize(int64_t M, int64_t n, const void* x, qg_dtype type, int64_t ldx, void* codes, qg_dtype format,
+                      int64_t ldc, uint8_t* scale, int64_t lds, void* stream) {
+    if (M < 0 || M >= LIM || n < 1 || n >= LIM || !is_float(type) || !is_mx(format)) return QG_ERR_INVALID_ARGUMENT;
+    if (M == 0) return nothing();
+    if (x == nullptr || codes == nullptr || scale == nullptr || ldx < n || ldc < code_bytes(format, n) ||
+        lds < blocks_of(n) || !aligned_for(x, type))
+        return QG_ERR_INVALID_ARGUMENT;
+    if (M * blocks_of(n) >= (int64_t)1 << 38) return QG_ERR_UNSUPPORTED;   // one grid dimension
+    (void)hipGetLastError();
+    const qg::MxCodecArgs a{M, n, x, ldx, nullptr, 0, (uint8_t*)codes, ldc, scale, lds};
+    const char* name = "";
+    return done(qg::launch_mx_quantize(a, type, format, (hipStream_t)stream, &name), name);
+}
+
+qg_status mx_dequantize(int64_t M, int64_t n, const void* codes, qg_dtype format, int64_t ldc, const uint8_t* scale,
+                        int64_t lds, void* out, qg_dtype out_type, int64_t ldo, void* stream) {
+    if (M < 0 || M >= LIM || n < 1 || n >= LIM || !is_float(out_type) || !is_mx(format)) return QG_ERR_INVALID_ARGUMENT;
+    if (M == 0) return nothing();
+    if (out == nullptr || codes == nullptr || scale == nullptr || ldo < n || ldc < code_bytes(format, n) ||
+        lds < blocks_of(n) || !aligned_for(out, out_type))
+        return QG_ERR_INVALID_ARGUMENT;
+    if (M * blocks_of(n) >= (int64_t)1 << 38) return QG_ERR_UNSUPPORTED;
+    (void)hipGetLastError();
+    const qg::MxCodecArgs a{M, n, nullptr, 0, out, ldo, (uint8_t*)const_cast<void*>(codes), ldc,
+                            const_cast<uint8_t*>(scale), lds};
+    const char* name = "";
+    return done(qg::launch_mx_dequantize(a, out_type, format, (hipStream_t)stream, &name), name);
+}
+
+size_t mx_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
+    (void)M; (void)N; (void)K;
+    return 0;
+}
+
+qg_status mx_matmul(int64_t M, int64_t N, int64_t K, const void* A, qg_dtype a_format, int64_t lda,
+                    const uint8_t* a_scale, int64_t ld_a_scale, const void* W, int64_t ldw, const uint8_t* w_scale,
+                    int64_t ld_w_scale, int scale_rows_padded, const float* act_scale, void* out, qg_dtype out_type,
+                    int64_t ldo, void* workspace, size_t workspace_bytes, void* stream) {
+    if (M < 0 || N < 0 || K < 0 || M >= LIM || N >= LIM || K >= LIM) return QG_ERR_INVALID_ARGUMENT;
+    if (!is_mx(a_format) || !is_float(out_type)) return QG_ERR_INVALID_ARGUMENT;
+    if (M == 0 || N == 0) return nothing();
+    if (K < 32 || K % 32 != 0) return QG_ERR_INVALID_ARGUMENT;
+    if (A == nullptr || a_scale == nullptr || W == nullptr || w_scale == nullptr || out == nullptr)
+        return QG_ERR_INVALID_ARGUMENT;
+    if (lda < code_bytes(a_format, K) || ldw < K / 2 || ld_a_scale < K / 32 || ld_w_scale < K / 32 || ldo < N ||
+        !aligned_for(out, out_type) || !aligned(act_scale, 4))
+        return QG_ERR_INVALID_ARGUMENT;
+    if (workspace != nullptr && !aligned(workspace, 256)) return QG_ERR_INVALID_ARGUMENT;
+    if (workspace != nullptr && workspace_bytes < mx_matmul_workspace_bytes(M, N, K)) return QG_ERR_WORKSPACE;
+    if (lda * 512 >= (int64_t)1 << 31 || ldw * 512 >= (int64_t)1 << 31 || ld_a_scale * 512 >= (int64_t)1 << 31 ||
+        ld_w_scale * 512 >= (int64_t)1 << 31)
+        return QG_ERR_UNSUPPORTED;
+    (void)scale_rows_padded;
+    if ((M + 15) / 16 > 65535) return QG_ERR_UNSUPPORTED;
+    (void)hipGetLastError();
+    qg::MxMatmulArgs a{};
+    a.M = (int)M; a.N = (int)N; a.K = (int)K;
+    a.A = (const uint8_t*)A; a.lda = lda; a.as = a_scale; a.ldas = ld_a_scale;
+    a.W = (const uint8_t*)W; a.ldw = ldw; a.ws = w_scale; a.ldws = ld_w_scale;
+    a.act_scale = act_scale; a.out = out; a.ldo = ldo; a.out_type = out_type;
+    a.splits = 1;
+    const char* name = "";
+    return done(qg::launch_mx_bytes(a, a_format == QG_MXFP8, (hipStream_t)stream, &name), name);
+}
+
+}  // extern "C"

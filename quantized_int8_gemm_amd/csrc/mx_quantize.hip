@@ -1,0 +1,127 @@
+// Values to MX form and back.
+//
+// Bound by HBM: each lane moves eight consecutive values (16 bytes of a 16-bit
+// type), four lanes hold one block of 32, and the block's largest magnitude
+// comes from two quad permutes.  Lanes are numbered over the rows' groups of
+// eight, so short and odd rows fill waves as well as long ones.
+#include "mx_common.h"
+
+namespace qg {
+namespace {
+
+constexpr int NT = 256;
+constexpr int UNROLL = 4;   // groups of eight in flight per lane
+
+template <typename T, bool FP4>
+__global__ __launch_bounds__(NT) void mx_quantize_kernel(MxCodecArgs a, uint32_t gpr, int64_t groups) {
+    const int64_t g0 = (int64_t)blockIdx.x * (NT * UNROLL) + threadIdx.x;
+    Pack8<T> v[UNROLL];
+    int64_t row[UNROLL];
+    int c[UNROLL];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+        const int64_t g = g0 + u * NT;
+        row[u] = g / gpr;
+        c[u] = (int)(g - row[u] * gpr) * 8;
+        const int left = g < groups ? (int)a.n - c[u] : 0;
+        load8(reinterpret_cast<const T*>(a.x) + row[u] * a.ldx + c[u], left, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+        float f[8];
+        uint32_t m = 0u;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            f[e] = (float)v[u].v[e];
+            m = umax(m, abs_bits(f[e]));
+        }
+        m = quad_max(m);
+        const uint32_t b = mx_scale_byte<FP4>(m);
+        uint32_t q[2];
+        mx_encode8<FP4>(f, b, q);
+        if (g0 + u * NT < groups) {
+            uint8_t* dst = a.codes + row[u] * a.ldc;
+            if constexpr (FP4) __builtin_memcpy(dst + c[u] / 2, q, 4);
+            else __builtin_memcpy(dst + c[u], q, 8);
+            if ((threadIdx.x & 3) == 0) a.scale[row[u] * a.lds + c[u] / 32] = (uint8_t)b;
+        }
+    }
+}
+
+template <typename T, bool FP4>
+__global__ __launch_bounds__(NT) void mx_dequantize_kernel(MxCodecArgs a, uint32_t gpr, int64_t groups) {
+    const int64_t g0 = (int64_t)blockIdx.x * (NT * UNROLL) + threadIdx.x;
+    uint32_t q[UNROLL][2];
+    uint32_t b[UNROLL];
+    int64_t row[UNROLL];
+    int c[UNROLL];
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+        const int64_t g = g0 + u * NT;
+        row[u] = g / gpr;
+        c[u] = (int)(g - row[u] * gpr) * 8;
+        q[u][0] = q[u][1] = b[u] = 0u;
+        if (g < groups) {
+            const uint8_t* src = a.codes + row[u] * a.ldc;
+            if constexpr (FP4) __builtin_memcpy(q[u], src + c[u] / 2, 4);
+            else __builtin_memcpy(q[u], src + c[u], 8);
+            b[u] = a.scale[row[u] * a.lds + c[u] / 32];
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < UNROLL; ++u) {
+        if (g0 + u * NT >= groups) continue;
+        const float s = mx_factor(b[u]);
+        v2f p[4];
+        if constexpr (FP4) {
+            p[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u][0], 1.0f, 0);
+            p[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u][0], 1.0f, 1);
+            p[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u][0], 1.0f, 2);
+            p[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(q[u][0], 1.0f, 3);
+        } else {
+            p[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q[u][0], 1.0f, false);
+            p[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q[u][0], 1.0f, true);
+            p[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q[u][1], 1.0f, false);
+            p[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(q[u][1], 1.0f, true);
+        }
+        Pack8<T> o;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) o.v[e] = (T)(p[e / 2][e & 1] * s);
+        store8(reinterpret_cast<T*>(a.out) + row[u] * a.ldo + c[u], (int)a.n - c[u], o);
+    }
+}
+
+template <typename T, bool FP4>
+hipError_t run(const MxCodecArgs& a, bool back, hipStream_t s) {
+    // Quantising covers whole blocks (their padding is written), reading back
+    // the n values.
+    const int64_t gpr = back ? (a.n + 7) / 8 : (a.n + 31) / 32 * 4;
+    const int64_t groups = a.M * gpr, blocks = (groups + NT * UNROLL - 1) / (NT * UNROLL);
+    if (blocks > 0x7fffffff) return hipErrorInvalidValue;
+    if (back)
+        hipLaunchKernelGGL((mx_dequantize_kernel<T, FP4>), dim3((unsigned)blocks), dim3(NT), 0, s, a, (uint32_t)gpr, groups);
+    else
+        hipLaunchKernelGGL((mx_quantize_kernel<T, FP4>), dim3((unsigned)blocks), dim3(NT), 0, s, a, (uint32_t)gpr, groups);
+    return hipGetLastError();
+}
+
+template <bool FP4>
+hipError_t by_type(const MxCodecArgs& a, qg_dtype type, bool back, hipStream_t s) {
+    if (type == QG_FP32) return run<float, FP4>(a, back, s);
+    if (type == QG_BF16) return run<__bf16, FP4>(a, back, s);
+    return run<_Float16, FP4>(a, back, s);
+}
+
+}  // namespace
+
+hipError_t launch_mx_quantize(const MxCodecArgs& a, qg_dtype type, qg_dtype format, hipStream_t s, const char** name) {
+    *name = format == QG_MXFP4 ? "mx_quantize_mxfp4" : "mx_quantize_mxfp8";
+    return format == QG_MXFP4 ? by_type<true>(a, type, false, s) : by_type<false>(a, type, false, s);
+}
+
+hipError_t launch_mx_dequantize(const MxCodecArgs& a, qg_dtype type, qg_dtype format, hipStream_t s, const char** name) {
+    *name = format == QG_MXFP4 ? "mx_dequantize_mxfp4" : "mx_dequantize_mxfp8";
+    return format == QG_MXFP4 ? by_type<true>(a, type, true, s) : by_type<false>(a, type, true, s);
+}
+
+}  // namespace qg

@@ -1,0 +1,201 @@
+// Root-mean-square norm with the residual's addition and an output in fp32,
+// bf16 or fp16, in int8 with a scale per row, or in MX form.
+//
+// Mathematics: h = x + residual (stored in x's type), r = 1 / sqrt(mean h^2 +
+// eps), y = h r w.  r is one factor of the whole row, so a quantised output
+// never needs it: int8 codes are rint(t * 127 / max|t|) with t = h w, and r
+// joins the row's scale; MX blocks hold t and r is handed on as the product's
+// row scale.  The codes are then the same whatever order the sum of squares
+// is added in, and MX blocks leave before the row's sum is known.
+//
+// Bound by HBM: every value is read once and kept in registers (at most 64 a
+// lane), one barrier per row.  A row is shared by G lanes: one wave up to
+// 1024 columns (four rows per workgroup), 256 lanes up to 8192, 1024 beyond.
+#include "mx_common.h"
+
+namespace qg {
+namespace {
+
+enum { OUT_SAME = 0, OUT_F32 = 1, OUT_I8 = 2, OUT_MX8 = 3, OUT_MX4 = 4 };
+
+// Sum of `ss` and maximum of `top` over the G lanes of a row; every lane
+// receives both.
+template <int G>
+__device__ __forceinline__ void row_reduce(float& ss, uint32_t& top) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) {
+        ss += __shfl_xor(ss, off);
+        top = umax(top, (uint32_t)__shfl_xor((int)top, off));
+    }
+    if constexpr (G > 64) {
+        __shared__ float s_ss[G / 64];
+        __shared__ uint32_t s_top[G / 64];
+        const int wave = threadIdx.x >> 6;
+        if ((threadIdx.x & 63) == 0) {
+            s_ss[wave] = ss;
+            s_top[wave] = top;
+        }
+        __syncthreads();
+        ss = s_ss[0];
+        top = s_top[0];
+#pragma unroll
+        for (int w = 1; w < G / 64; ++w) {
+            ss += s_ss[w];
+            top = umax(top, s_top[w]);
+        }
+    }
+}
+
+template <typename T, int G, int ITER, int OUT, bool WF32>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void rms_norm_kernel(RmsNormArgs a) {
+    constexpr int RPW = G < 256 ? 256 / G : 1;   // rows per workgroup
+    const int t = threadIdx.x % G;
+    const int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / G;
+    if (row >= a.M) return;                      // whole waves (G = 64 has no barrier)
+    const int n = a.n;
+    const T* x = reinterpret_cast<const T*>(a.x) + row * a.ldx;
+    const T* res = a.res != nullptr ? reinterpret_cast<const T*>(a.res) + row * a.ldr : nullptr;
+
+    Pack8<T> xv[ITER], rv[ITER];
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+        const int c = (i * G + t) * 8;
+        load8(x + c, n - c, xv[i]);
+    }
+    if (res != nullptr) {
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            const int c = (i * G + t) * 8;
+            load8(res + c, n - c, rv[i]);
+        }
+    }
+    float ss = 0.f;
+    uint32_t top = 0u;
+    float y[ITER][8];
+#pragma unroll
+    for (int i = 0; i < ITER; ++i) {
+        const int c = (i * G + t) * 8;
+        if (res != nullptr) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) xv[i].v[e] = (T)((float)xv[i].v[e] + (float)rv[i].v[e]);
+            store8(reinterpret_cast<T*>(a.h) + row * a.ldh + c, n - c, xv[i]);
+        }
+        float w[8];
+        if constexpr (WF32) {
+            Pack8<float> p;
+            load8(reinterpret_cast<const float*>(a.weight) + c, n - c, p);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = p.v[e];
+        } else {
+            Pack8<T> p;
+            load8(reinterpret_cast<const T*>(a.weight) + c, n - c, p);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) w[e] = (float)p.v[e];
+        }
+        uint32_t m = 0u;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float h = (float)xv[i].v[e];
+            ss = __builtin_fmaf(h, h, ss);
+            y[i][e] = h * w[e];
+            m = umax(m, abs_bits(y[i][e]));
+        }
+        if constexpr (OUT == OUT_MX8 || OUT == OUT_MX4) {
+            // four lanes hold one block of 32; columns past n are zeros
+            m = quad_max(m);
+            const uint32_t b = mx_scale_byte<OUT == OUT_MX4>(m);
+            uint32_t q[2];
+            mx_encode8<OUT == OUT_MX4>(y[i], b, q);
+            if ((c & ~31) < n) {
+                uint8_t* dst = reinterpret_cast<uint8_t*>(a.out) + row * a.ldo;
+                if constexpr (OUT == OUT_MX4) __builtin_memcpy(dst + c / 2, q, 4);
+                else __builtin_memcpy(dst + c, q, 8);
+                if ((t & 3) == 0) a.block_scale[row * a.lds + c / 32] = (uint8_t)b;
+            }
+        }
+        top = umax(top, m);
+    }
+    row_reduce<G>(ss, top);
+    const float r = 1.0f / __builtin_sqrtf(ss / (float)n + a.eps);
+    if constexpr (OUT == OUT_I8) {
+        const bool bad = top >= INF_BITS;
+        float most = __uint_as_float(top);
+        // 127 / most stays finite: tiny rows are multiplied by 2^60, exactly
+        const float up = most < 0x1p-100f ? 0x1p60f : 1.0f;
+        const float inv = bad || top == 0u ? 0.f : 127.0f / (most * up);
+        if (t == 0) a.row_scale[row] = bad ? __uint_as_float(0x7fc00000u) : (top == 0u ? 1.0f : most * r / 127.0f);
+        int8_t* dst = reinterpret_cast<int8_t*>(a.out) + row * a.ldo;
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            const int c = (i * G + t) * 8;
+            Pack8<int8_t> q;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float v = bad ? 0.f : (y[i][e] * up) * inv;
+                q.v[e] = (int8_t)(int)__builtin_rintf(v);
+            }
+            if (c < n) store8(dst + c, n - c, q);
+        }
+    } else {
+        if (t == 0 && a.row_scale != nullptr) a.row_scale[row] = r;
+        if constexpr (OUT == OUT_SAME || OUT == OUT_F32) {
+            typedef typename std::conditional<OUT == OUT_F32, float, T>::type O;
+            O* dst = reinterpret_cast<O*>(a.out) + row * a.ldo;
+#pragma unroll
+            for (int i = 0; i < ITER; ++i) {
+                const int c = (i * G + t) * 8;
+                Pack8<O> q;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) q.v[e] = (O)(y[i][e] * r);
+                if (c < n) store8(dst + c, n - c, q);
+            }
+        }
+    }
+}
+
+template <typename T, int OUT, bool WF32>
+hipError_t by_width(const RmsNormArgs& a, hipStream_t s) {
+#define QG_NORM(G, ITER)                                                                                       \
+    if (a.n <= G * ITER * 8) {                                                                                 \
+        constexpr int RPW = G < 256 ? 256 / G : 1;                                                             \
+        hipLaunchKernelGGL((rms_norm_kernel<T, G, ITER, OUT, WF32>), dim3((unsigned)((a.M + RPW - 1) / RPW)),  \
+                           dim3(G < 256 ? 256 : G), 0, s, a);                                                  \
+        return hipGetLastError();                                                                              \
+    }
+    QG_NORM(64, 1)
+    QG_NORM(64, 2)
+    QG_NORM(256, 1)
+    QG_NORM(256, 2)
+    QG_NORM(256, 4)
+    QG_NORM(1024, 2)
+    QG_NORM(1024, 4)
+    QG_NORM(1024, 8)
+#undef QG_NORM
+    return hipErrorInvalidValue;
+}
+
+template <typename T, bool WF32>
+hipError_t by_format(const RmsNormArgs& a, int out, hipStream_t s) {
+    switch (out) {
+        case OUT_SAME: return by_width<T, OUT_SAME, WF32>(a, s);
+        case OUT_F32: return by_width<T, OUT_F32, WF32>(a, s);
+        case OUT_I8: return by_width<T, OUT_I8, WF32>(a, s);
+        case OUT_MX8: return by_width<T, OUT_MX8, WF32>(a, s);
+        default: return by_width<T, OUT_MX4, WF32>(a, s);
+    }
+}
+
+}  // namespace
+
+hipError_t launch_rms_norm(const RmsNormArgs& a, qg_dtype type, bool weight_f32, qg_dtype format, hipStream_t s,
+                           const char** name) {
+    const int out = format == QG_INT8 ? OUT_I8 : format == QG_MXFP8 ? OUT_MX8 : format == QG_MXFP4 ? OUT_MX4
+                  : format == type ? OUT_SAME : OUT_F32;
+    static const char* names[] = {"rms_norm", "rms_norm", "rms_norm_int8", "rms_norm_mxfp8", "rms_norm_mxfp4"};
+    *name = names[out];
+    if (type == QG_FP32) return by_format<float, false>(a, out, s);
+    if (type == QG_BF16) return weight_f32 ? by_format<__bf16, true>(a, out, s) : by_format<__bf16, false>(a, out, s);
+    return weight_f32 ? by_format<_Float16, true>(a, out, s) : by_format<_Float16, false>(a, out, s);
+}
+
+}  // namespace qg
