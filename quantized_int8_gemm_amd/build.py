@@ -42,6 +42,10 @@ SOURCES = [
     "rms_norm_grad.hip",
     "mx_quantize.hip",
     "mx_matmul_bytes.hip",
+    "mx_tiled_256x256.hip",
+    "mx_tiled_128x128.hip",
+    "mx_tiled_64x128.hip",
+    "mx_decode.hip",
     "mx_api.cpp",
     "api.cpp",
 ]

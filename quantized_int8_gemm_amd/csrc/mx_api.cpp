@@ -1,11 +1,13 @@
 // C entry points of qgemm_mx.h: argument checks (before any HIP call), kernel
 // choice and launch, with the launch-status convention of api.cpp.
+#include <algorithm>
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
 
 #include <hip/hip_runtime.h>
 
+#include "kernels.h"
 #include "mx_kernels.h"
 
 namespace {
@@ -24,6 +26,45 @@ qg_status done(hipError_t e, const char* name) {
     if (e != hipSuccess) return QG_ERR_HIP;
     qg::record_kernel(name);
     return QG_OK;
+}
+
+bool env_is(const char* name, const char* value) {
+    const char* v = std::getenv(name);
+    return v != nullptr && std::strcmp(v, value) == 0;
+}
+
+int env_int(const char* name, int dflt) {
+    const char* v = std::getenv(name);
+    return v != nullptr && *v ? std::atoi(v) : dflt;
+}
+
+// Kernel of an MX product and its split of K.
+enum MxKind { MX_256x256, MX_128x128, MX_64x128, MX_DECODE };
+struct MxPlan { int kind; int64_t tiles; int splits; int split_k; };
+
+MxPlan plan_mx(int64_t M, int64_t N, int64_t K) {
+    MxPlan p{MX_DECODE, 0, 1, (int)K};
+    auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+    const int64_t t256 = tiles(256, 256), t128 = tiles(128, 128);
+    const int forced = env_int("QGEMM_MX_TILE", -1);
+    if (forced >= 0 && forced <= MX_64x128) p.kind = forced;
+    else if (M <= 16) return p;
+    else p.kind = t256 >= 192 ? MX_256x256 : t128 >= 256 ? MX_128x128 : MX_64x128;
+    p.tiles = p.kind == MX_256x256 ? t256 : p.kind == MX_128x128 ? t128 : tiles(64, 128);
+    if (p.kind == MX_256x256 || p.tiles > qg::SKINNY_MAX_TICKETS) return p;
+    // two workgroups per CU, ranges of at least 1024 values
+    int64_t s = std::min<int64_t>({512 / p.tiles, K / 1024, 8});
+    s = env_int("QGEMM_MX_SPLITS", (int)s);
+    if (s < 2) return p;
+    const int64_t units = (K + 255) / 256, per = (units + s - 1) / s;
+    p.split_k = (int)per * 256;
+    p.splits = (int)((units + per - 1) / per);
+    return p;
+}
+
+size_t plan_bytes(const MxPlan& p) {
+    if (p.splits < 2) return 0;
+    return qg::SKINNY_TICKET_BYTES + (size_t)p.tiles * p.splits * (p.kind == MX_128x128 ? 128 * 128 : 64 * 128) * 4;
 }
 
 qg_status nothing() {
@@ -126,8 +167,8 @@ qg_status mx_dequantize(int64_t M, int64_t n, const void* codes, qg_dtype format
 }
 
 size_t mx_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    (void)M; (void)N; (void)K;
-    return 0;
+    if (M < 1 || N < 1 || K < 32 || M >= LIM || N >= LIM || K >= LIM || K % 32 != 0) return 0;
+    return plan_bytes(plan_mx(M, N, K));
 }
 
 qg_status mx_matmul(int64_t M, int64_t N, int64_t K, const void* A, qg_dtype a_format, int64_t lda,
@@ -148,17 +189,32 @@ qg_status mx_matmul(int64_t M, int64_t N, int64_t K, const void* A, qg_dtype a_f
     if (lda * 512 >= (int64_t)1 << 31 || ldw * 512 >= (int64_t)1 << 31 || ld_a_scale * 512 >= (int64_t)1 << 31 ||
         ld_w_scale * 512 >= (int64_t)1 << 31)
         return QG_ERR_UNSUPPORTED;
-    (void)scale_rows_padded;
-    if ((M + 15) / 16 > 65535) return QG_ERR_UNSUPPORTED;
+    const bool fast = lda % 16 == 0 && ldw % 16 == 0 && aligned(A, 16) && aligned(W, 16) && scale_rows_padded != 0 &&
+                      (ld_a_scale % 4 == 0 || M == 1) && (ld_w_scale % 4 == 0 || N == 1) && aligned(a_scale, 4) &&
+                      aligned(w_scale, 4) && !env_is("QGEMM_MX_KERNEL", "bytes");
+    if (!fast && (M + 15) / 16 > 65535) return QG_ERR_UNSUPPORTED;   // the other kernel's second grid dimension
     (void)hipGetLastError();
     qg::MxMatmulArgs a{};
     a.M = (int)M; a.N = (int)N; a.K = (int)K;
     a.A = (const uint8_t*)A; a.lda = lda; a.as = a_scale; a.ldas = ld_a_scale;
     a.W = (const uint8_t*)W; a.ldw = ldw; a.ws = w_scale; a.ldws = ld_w_scale;
     a.act_scale = act_scale; a.out = out; a.ldo = ldo; a.out_type = out_type;
+    a.workspace = workspace;
     a.splits = 1;
+    const bool a8 = a_format == QG_MXFP8;
+    const hipStream_t st = (hipStream_t)stream;
     const char* name = "";
-    return done(qg::launch_mx_bytes(a, a_format == QG_MXFP8, (hipStream_t)stream, &name), name);
+    if (!fast) return done(qg::launch_mx_bytes(a, a8, st, &name), name);
+    MxPlan p = plan_mx(M, N, K);
+    if (p.kind == MX_DECODE) return done(qg::launch_mx_decode(a, a8, st, &name), name);
+    if (workspace == nullptr) p.splits = 1;
+    a.splits = p.splits;
+    a.split_k = p.split_k;
+    switch (p.kind) {
+        case MX_256x256: return done(qg::launch_mx_256x256(a, a8, st), "mx_tiled_256x256");
+        case MX_128x128: return done(qg::launch_mx_128x128(a, a8, st), p.splits > 1 ? "mx_tiled_128x128_splitk" : "mx_tiled_128x128");
+        default: return done(qg::launch_mx_64x128(a, a8, st), p.splits > 1 ? "mx_tiled_64x128_splitk" : "mx_tiled_64x128");
+    }
 }
 
 }  // extern "C"

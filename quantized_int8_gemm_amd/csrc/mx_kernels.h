@@ -56,6 +56,19 @@ struct MxMatmulArgs {
 // Reads bytes: any strides, any alignment, no workspace.
 hipError_t launch_mx_bytes(const MxMatmulArgs& a, bool a8, hipStream_t s, const char** name);
 
+// Tiled kernels: code rows 16-byte aligned, scale rows 4-byte aligned and
+// readable to the end of their last word; K split when a.splits > 1 (split_k a
+// multiple of 256, tickets for at most SKINNY_MAX_TICKETS tiles; not the
+// 256x256 tiles).
+hipError_t launch_mx_256x256(const MxMatmulArgs& a, bool a8, hipStream_t s);
+hipError_t launch_mx_128x128(const MxMatmulArgs& a, bool a8, hipStream_t s);
+hipError_t launch_mx_64x128(const MxMatmulArgs& a, bool a8, hipStream_t s);
+
+// Few rows: W streamed once, 16 columns per workgroup, no workspace; operands
+// laid out as for the tiled kernels.
+constexpr int MX_DECODE_MAX_M = 64;
+hipError_t launch_mx_decode(const MxMatmulArgs& a, bool a8, hipStream_t s, const char** name);
+
 // Names the kernel for qgemm_last_kernel().
 void record_kernel(const char* name);
 

@@ -1,0 +1,11 @@
+// 256 x 256 tiles of the MX product: eight waves of 128 x 64.  MXFP4: stages of
+// 256 values of K, two of them (136 KiB); MXFP8 activations: 128 values, three
+// (150 KiB).
+#include "mx_tiled_impl.h"
+
+namespace qg {
+hipError_t launch_mx_256x256(const MxMatmulArgs& a, bool a8, hipStream_t s) {
+    return a8 ? mx::launch_out<256, 256, 128, 64, 4, 3, true, false>(a, s)
+              : mx::launch_out<256, 256, 128, 64, 8, 2, false, false>(a, s);
+}
+}  // namespace qg

@@ -6,7 +6,7 @@ import torch
 
 import mx_reference as R
 import quantized_int8_gemm_amd as q
-from gpu_util import case, dev
+from gpu_util import case, dev, env
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
@@ -174,3 +174,36 @@ def test_results_repeat_and_workspace_is_left_clean(M):
     for _ in range(3):
         assert torch.equal(q.mx_matmul(a, sa, w, sw, workspace=ws), first)
     assert not ws[:1024].any()
+
+
+TILES = ["mx_tiled_256x256", "mx_tiled_128x128", "mx_tiled_64x128"]
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 1, 32), (40, 300, 96), (257, 129, 512), (300, 700, 1120), (600, 515, 2080)])
+@pytest.mark.parametrize("tile", [0, 1, 2])
+@pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
+def test_every_tile(M, N, K, tile, fmt):
+    """Each tile shape, whatever the plan would choose, whole and split."""
+    case(f"mx_matmul tile {tile} {M}x{N}x{K} {fmt}")
+    with env(QGEMM_MX_TILE=tile, QGEMM_MX_SPLITS=1):
+        check(M, N, K, fmt, torch.float32, True)
+        assert q._binding.last_kernel() == TILES[tile]
+        check(M, N, K, fmt, torch.bfloat16, False)
+    if tile and K > 512:
+        for s in (2, 3, 5):
+            with env(QGEMM_MX_TILE=tile, QGEMM_MX_SPLITS=s):
+                check(M, N, K, fmt, torch.float32, True)
+                assert q._binding.last_kernel() == TILES[tile] + "_splitk"
+                check(M, N, K, fmt, torch.float16, False)
+
+
+@pytest.mark.parametrize("M,N,K,kernel", [
+    (1, 512, 512, "mx_decode"), (16, 512, 544, "mx_decode"), (17, 512, 512, "mx_tiled_64x128"),
+    (64, 4096, 8192, "mx_tiled_64x128_splitk"), (2048, 2048, 512, "mx_tiled_128x128"), (4096, 4096, 256, "mx_tiled_256x256")])
+def test_kernel_choice(M, N, K, kernel):
+    case(f"mx_matmul kernel for {M}x{N}x{K}")
+    check(M, N, K, "mxfp4", torch.bfloat16, True)
+    assert q._binding.last_kernel() == kernel
+    with env(QGEMM_MX_KERNEL="bytes"):
+        check(M, N, K, "mxfp8", torch.bfloat16, True)
+        assert q._binding.last_kernel() == "mx_matmul_bytes"
