@@ -10,7 +10,7 @@ import ctypes
 
 import torch
 
-from ._binding import (QG_BF16, QG_FP32, QG_INT8, _check, _f32, _i64, _int, _need, _on_gpu, _p, _ptr, _stream, _sz, lib)
+from ._binding import (QG_BF16, QG_FP32, QG_INT8, _check, _f32, _i64, _int, _need, _on_gpu, _p, _sz, lib)
 
 QG_FP16, QG_MXFP8, QG_MXFP4 = 5, 6, 7
 MX_BLOCK = 32
@@ -35,17 +35,38 @@ _FORMATS = {"mxfp8": QG_MXFP8, "mxfp4": QG_MXFP4}
 # element types of the codes: e4m3 as torch has it, e2m1 packed in pairs
 _CODES = {torch.float8_e4m3fn: QG_MXFP8, torch.uint8: QG_MXFP4}
 
+# The smallest calls take a few microseconds on the GPU, so what they do here
+# counts: tensors are looked at through few calls, new outputs are not looked
+# at again, and the stream and the current device come from torch's C
+# functions, which cost a tenth of torch.cuda's own.
+_current_device, _raw_stream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
+
+
+def _kind(t, table, name):
+    """The library's number for t's dtype, one of `table`."""
+    try:
+        return table[t.dtype]
+    except (AttributeError, KeyError):
+        _need(t, tuple(table), name)
+        raise
+
 
 def _matrix(t, name):
     """(rows, columns, row stride in elements) of t seen as a matrix of its
     last dimension; more than two dimensions have to lie like one matrix."""
-    if t.dim() == 0:
+    shape = t.shape
+    if len(shape) == 2:
+        rows, n = shape
+        stride, step = t.stride()
+        if (step == 1 or n <= 1) and (rows <= 1 or stride >= n):
+            return rows, n, stride if rows > 1 else n
+    if not shape:
         raise ValueError(f"{name} must have at least one dimension")
-    n = t.shape[-1]
+    n = shape[-1]
     if n > 1 and t.stride(-1) != 1:
         raise ValueError(f"{name} must have unit column stride")
     rows, stride = 1, None
-    for size, st in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for size, st in zip(reversed(shape[:-1]), reversed(t.stride()[:-1])):
         if size == 1:
             continue
         if stride is None:
@@ -60,23 +81,32 @@ def _matrix(t, name):
     return rows, n, stride
 
 
-def _like(t, name, shape, dtype, dev):
-    """`t` checked against what it has to be, or a new tensor of that kind."""
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+def _device(t, *others):
+    """The GPU that all the tensors are on (None: no tensor)."""
+    index = t.get_device()
+    for o in others:
+        if o is not None and o.get_device() != index:
+            index = -1
+    if index < 0:
+        _on_gpu(t, *(o for o in others if o is not None))
+    return t.device
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _like(t, name, shape, dtype):
+    """`t` checked against what it has to be."""
     _need(t, (dtype,), name)
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}; expected {tuple(shape)}")
     return t
 
 
-def _scale_rows(lead, blocks, dev):
-    """[*lead, blocks] scale bytes whose rows start at multiples of 16 bytes."""
-    return torch.empty((*lead, (blocks + 15) // 16 * 16), dtype=torch.uint8, device=dev)[..., :blocks]
-
-
 def _weight(weight, n, dtype):
-    _need(weight, (dtype, torch.float32), "weight")
+    if weight.__class__ is not torch.Tensor or weight.dtype is not dtype:
+        _need(weight, (dtype, torch.float32), "weight")
     if tuple(weight.shape) != (n,):
         raise ValueError(f"weight has shape {tuple(weight.shape)}; expected ({n},)")
     return weight.contiguous()
@@ -84,42 +114,51 @@ def _weight(weight, n, dtype):
 
 def _launch(dev, fn, *args):
     """Calls a C entry point with the tensors' device current."""
-    if torch.cuda.current_device() == dev.index:
-        st = fn(*args, _stream(dev))
+    index = dev.index
+    if _current_device() == index:
+        st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            st = fn(*args, _stream(dev))
-    _check(st, fn.__name__)
-
-
-def _norm(x, weight, eps, residual, residual_out, format, out, out_dtype, block_scale, row_scale):
-    rows, n, ldx = _matrix(x, "x")
-    ts = [x, weight] + ([residual] if residual is not None else [])
-    h, ldr, ldh = None, 0, 0
-    if residual is not None:
-        _need(residual, (x.dtype,), "residual")
-        if residual.shape != x.shape:
-            raise ValueError(f"residual has shape {tuple(residual.shape)}; x has {tuple(x.shape)}")
-        _, _, ldr = _matrix(residual, "residual")
-        h = _like(residual_out, "residual_out", x.shape, x.dtype, x.device)
-        _, _, ldh = _matrix(h, "residual_out")
-        ts.append(h)
-    elif residual_out is not None:
-        raise ValueError("residual_out needs a residual")
-    dev = _on_gpu(*ts, out, row_scale)
-    _, _, ldo = _matrix(out, "out")
-    lds = _matrix(block_scale, "block_scale")[2] if block_scale is not None else 0
-    _launch(dev, lib.rms_norm, rows, n, _ptr(x), _FLOATS[x.dtype], ldx, _ptr(residual), ldr, _ptr(weight),
-            _FLOATS[weight.dtype], float(eps), _ptr(h), ldh, _ptr(out), format, ldo, _ptr(block_scale), lds,
-            _ptr(row_scale))
-    return h
+            st = fn(*args, _raw_stream(index))
+    if st:
+        _check(st, fn.__name__)
 
 
 def _norm_inputs(x, weight):
-    _need(x, tuple(_FLOATS), "x")
-    if x.dim() == 0 or x.shape[-1] == 0:
+    """x's number of its dtype, rows, columns and row stride, and the weight."""
+    kind = _kind(x, _FLOATS, "x")
+    rows, n, ldx = _matrix(x, "x")
+    if n == 0:
         raise ValueError("x must have at least one column")
-    return _weight(weight, x.shape[-1], x.dtype)
+    return kind, rows, n, ldx, _weight(weight, n, x.dtype)
+
+
+def _norm(x, inputs, eps, residual, residual_out, format, out, ldo, block_scale, lds, row_scale, dev):
+    kind, rows, n, ldx, weight = inputs
+    h, ldr, ldh = None, 0, 0
+    if residual is not None:
+        if residual.dtype is not x.dtype or residual.shape != x.shape:
+            raise ValueError(f"residual has shape {tuple(residual.shape)}; x has {tuple(x.shape)}")
+        ldr = _matrix(residual, "residual")[2]
+        if residual_out is None:
+            h, ldh = torch.empty(x.shape, dtype=x.dtype, device=dev), n
+        else:
+            h = _like(residual_out, "residual_out", x.shape, x.dtype)
+            ldh = _matrix(h, "residual_out")[2]
+            _device(x, h)
+    _launch(dev, lib.rms_norm, rows, n, x.data_ptr(), kind, ldx, _at(residual), ldr, weight.data_ptr(),
+            _FLOATS[weight.dtype], float(eps), _at(h), ldh, out.data_ptr(), format, ldo, _at(block_scale), lds,
+            row_scale.data_ptr())
+    return h
+
+
+def _norm_device(x, weight, residual, residual_out):
+    """The device of a norm's inputs, the residual's dtype checked."""
+    if residual is not None:
+        _need(residual, (x.dtype,), "residual")
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    return _device(x, weight, residual)
 
 
 def rms_norm(x, weight, eps=1e-6, residual=None, out_dtype=None, out=None, residual_out=None):
@@ -132,13 +171,20 @@ def rms_norm(x, weight, eps=1e-6, residual=None, out_dtype=None, out=None, resid
     as a third where a residual is given: rstd is fp32 [...], 1 / sqrt(...), as
     rms_norm_grad takes it.  residual_out: the tensor to write h to; it may be
     x or residual itself."""
-    weight = _norm_inputs(x, weight)
-    out_dtype = x.dtype if out_dtype is None else out_dtype
-    if out_dtype not in (x.dtype, torch.float32):
+    inputs = _norm_inputs(x, weight)
+    if out_dtype is None:
+        out_dtype = x.dtype
+    elif out_dtype not in (x.dtype, torch.float32):
         raise TypeError("out_dtype must be x's dtype or torch.float32")
-    y = _like(out, "out", x.shape, out_dtype, x.device)
-    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    h = _norm(x, weight, eps, residual, residual_out, _FLOATS[out_dtype], y, out_dtype, None, rstd)
+    dev = _norm_device(x, inputs[4], residual, residual_out)
+    if out is None:
+        y, ldo = torch.empty(x.shape, dtype=out_dtype, device=dev), inputs[2]
+    else:
+        y = _like(out, "out", x.shape, out_dtype)
+        ldo = _matrix(y, "out")[2]
+        _device(x, y)
+    rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+    h = _norm(x, inputs, eps, residual, residual_out, _FLOATS[out_dtype], y, ldo, None, 0, rstd, dev)
     return (y, rstd) if h is None else (y, rstd, h)
 
 
@@ -151,15 +197,16 @@ def rms_norm_quantize(x, weight, eps=1e-6, residual=None, format="int8", residua
     h * weight in MX form (as mx_quantize returns it) and fp32 act_scale
     [...] = 1 / sqrt(mean(h^2) + eps): the A, a_scale and act_scale of
     mx_matmul.  Other arguments as rms_norm."""
-    weight = _norm_inputs(x, weight)
-    n, lead, dev = x.shape[-1], x.shape[:-1], x.device
+    inputs = _norm_inputs(x, weight)
+    n, lead = inputs[2], x.shape[:-1]
+    dev = _norm_device(x, inputs[4], residual, residual_out)
     row_scale = torch.empty(lead, dtype=torch.float32, device=dev)
     if format == "int8":
         q = torch.empty(x.shape, dtype=torch.int8, device=dev)
-        h = _norm(x, weight, eps, residual, residual_out, QG_INT8, q, torch.int8, None, row_scale)
+        h = _norm(x, inputs, eps, residual, residual_out, QG_INT8, q, n, None, 0, row_scale, dev)
         return (q, row_scale) if h is None else (q, row_scale, h)
-    codes, scale = _mx_outputs(lead, n, format, dev)
-    h = _norm(x, weight, eps, residual, residual_out, _FORMATS[format], codes, codes.dtype, scale, row_scale)
+    kind, codes, ldo, scale, lds = _mx_outputs(lead, n, format, dev)
+    h = _norm(x, inputs, eps, residual, residual_out, kind, codes, ldo, scale, lds, row_scale, dev)
     return (codes, scale, row_scale) if h is None else (codes, scale, row_scale, h)
 
 
@@ -172,46 +219,51 @@ def rms_norm_grad(dy, h, weight, rstd, dh=None):
     rms_norm; dh: the gradient that reaches h from elsewhere, added to dx.
     dx, of h's shape and dtype, is the gradient of x and of the residual alike;
     dweight has weight's dtype.  Results repeat bit for bit."""
-    _need(h, tuple(_FLOATS), "h")
+    kind = _kind(h, _FLOATS, "h")
     _need(dy, (h.dtype,), "dy")
-    if h.dim() == 0 or h.shape[-1] == 0:
+    rows, n, ldh = _matrix(h, "h")
+    if n == 0:
         raise ValueError("h must have at least one column")
     if dy.shape != h.shape:
         raise ValueError(f"dy has shape {tuple(dy.shape)}; h has {tuple(h.shape)}")
-    rows, n, ldh = _matrix(h, "h")
-    _, _, ldy = _matrix(dy, "dy")
+    ldy = _matrix(dy, "dy")[2]
     weight = _weight(weight, n, h.dtype)
     _need(rstd, (torch.float32,), "rstd")
     if rstd.shape != h.shape[:-1]:
         raise ValueError(f"rstd has shape {tuple(rstd.shape)}; expected {tuple(h.shape[:-1])}")
     rstd = rstd.contiguous()
-    ts, lddh = [dy, h, weight, rstd], 0
+    lddh = 0
     if dh is not None:
         _need(dh, (h.dtype,), "dh")
         if dh.shape != h.shape:
             raise ValueError(f"dh has shape {tuple(dh.shape)}; h has {tuple(h.shape)}")
-        _, _, lddh = _matrix(dh, "dh")
-        ts.append(dh)
-    dev = _on_gpu(*ts)
+        lddh = _matrix(dh, "dh")[2]
+    dev = _device(h, dy, weight, rstd, dh)
     dx = torch.empty(h.shape, dtype=h.dtype, device=dev)
     dweight = torch.empty(n, dtype=weight.dtype, device=dev)
     need = lib.rms_norm_grad_workspace_bytes(rows, n)
-    ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _launch(dev, lib.rms_norm_grad, rows, n, _ptr(dy), _FLOATS[h.dtype], ldy, _ptr(h), ldh, _ptr(weight),
-            _FLOATS[weight.dtype], _ptr(rstd), _ptr(dh), lddh, _ptr(dx), n, _ptr(dweight), _ptr(ws) if need else None,
-            need)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev) if need else None
+    _launch(dev, lib.rms_norm_grad, rows, n, dy.data_ptr(), kind, ldy, h.data_ptr(), ldh, weight.data_ptr(),
+            _FLOATS[weight.dtype], rstd.data_ptr(), _at(dh), lddh, dx.data_ptr(), n, dweight.data_ptr(), _at(ws), need)
     return dx, dweight
 
 
 def _mx_outputs(lead, n, format, dev):
-    if format not in _FORMATS:
+    """The library's number for the format, codes, their row stride in bytes,
+    scale bytes whose rows start at multiples of 16 bytes, and their stride."""
+    kind = _FORMATS.get(format)
+    if kind is None:
         raise ValueError(f"unknown format {format!r}; expected one of {sorted(_FORMATS)}")
     blocks = -(-n // MX_BLOCK)
-    if format == "mxfp8":
-        codes = torch.empty((*lead, blocks * 32), dtype=torch.float8_e4m3fn, device=dev)
+    lds = (blocks + 15) // 16 * 16
+    if kind == QG_MXFP8:
+        width = blocks * 32
+        codes = torch.empty((*lead, width), dtype=torch.float8_e4m3fn, device=dev)
     else:
-        codes = torch.empty((*lead, blocks * 16), dtype=torch.uint8, device=dev)
-    return codes, _scale_rows(lead, blocks, dev)
+        width = blocks * 16
+        codes = torch.empty((*lead, width), dtype=torch.uint8, device=dev)
+    scale = torch.empty((*lead, lds), dtype=torch.uint8, device=dev)
+    return kind, codes, width, scale if lds == blocks else scale.narrow(-1, 0, blocks), lds
 
 
 def mx_quantize(x, format="mxfp4"):
@@ -223,46 +275,50 @@ def mx_quantize(x, format="mxfp4"):
     column in the low half ("mxfp4").  scale: uint8 [..., B], 2^(scale - 127),
     255 for a block that holds a NaN or an infinity; its rows start at
     multiples of 16 bytes."""
-    _need(x, tuple(_FLOATS), "x")
+    dtype = _kind(x, _FLOATS, "x")
     rows, n, ldx = _matrix(x, "x")
     if n == 0:
         raise ValueError("x must have at least one column")
-    dev = _on_gpu(x)
-    codes, scale = _mx_outputs(x.shape[:-1], n, format, dev)
-    _launch(dev, lib.mx_quantize, rows, n, _ptr(x), _FLOATS[x.dtype], ldx, _ptr(codes), _FORMATS[format],
-            codes.shape[-1], _ptr(scale), _matrix(scale, "scale")[2])
+    dev = _device(x)
+    kind, codes, ldc, scale, lds = _mx_outputs(x.shape[:-1], n, format, dev)
+    _launch(dev, lib.mx_quantize, rows, n, x.data_ptr(), dtype, ldx, codes.data_ptr(), kind, ldc, scale.data_ptr(), lds)
     return codes, scale
 
 
 def _mx_operand(codes, scale, name):
-    """(rows, K, code stride in bytes, scale stride) of one MX operand."""
-    _need(codes, tuple(_CODES), name)
-    _need(scale, (torch.uint8,), name + " scale")
+    """(format, rows, K, code stride in bytes, scale stride) of one MX operand."""
+    kind = _kind(codes, _CODES, name)
+    if scale.__class__ is not torch.Tensor or scale.dtype is not torch.uint8:
+        _need(scale, (torch.uint8,), name + " scale")
     rows, width, ldc = _matrix(codes, name)
     srows, blocks, lds = _matrix(scale, name + " scale")
-    per = 32 if codes.dtype == torch.float8_e4m3fn else 16
+    per = 32 if kind == QG_MXFP8 else 16
     if width == 0 or width % per:
         raise ValueError(f"{name} has {width} code columns; expected whole blocks of {per}")
-    if codes.shape[:-1] != scale.shape[:-1] or blocks != width // per:
+    if blocks * per != width or codes.shape[:-1] != scale.shape[:-1]:
         raise ValueError(f"the scale of {name} has shape {tuple(scale.shape)}; "
                          f"expected {(*codes.shape[:-1], width // per)}")
-    return rows, blocks * MX_BLOCK, ldc, lds
+    return kind, rows, blocks * MX_BLOCK, ldc, lds
 
 
 def mx_dequantize(codes, scale, out_dtype=torch.bfloat16, columns=None, out=None):
     """The values an MX tensor stands for: fp32, bf16 or fp16 [..., columns]
     (default: all 32 B of them).  codes, scale: as mx_quantize returns them."""
-    rows, K, ldc, lds = _mx_operand(codes, scale, "codes")
-    if out_dtype not in _FLOATS:
+    kind, rows, K, ldc, lds = _mx_operand(codes, scale, "codes")
+    dtype = _FLOATS.get(out_dtype)
+    if dtype is None:
         raise TypeError(f"out_dtype must be one of {tuple(_FLOATS)}")
     n = K if columns is None else int(columns)
     if not K - MX_BLOCK < n <= K:
         raise ValueError(f"columns = {n} does not fill {K // MX_BLOCK} blocks")
-    dev = _on_gpu(codes, scale)
-    out = _like(out, "out", (*codes.shape[:-1], n), out_dtype, dev)
-    _on_gpu(codes, out)
-    _launch(dev, lib.mx_dequantize, rows, n, _ptr(codes), _CODES[codes.dtype], ldc, _ptr(scale), lds, _ptr(out),
-            _FLOATS[out_dtype], _matrix(out, "out")[2])
+    dev = _device(codes, scale)
+    shape = (*codes.shape[:-1], n)
+    if out is None:
+        out, ldo = torch.empty(shape, dtype=out_dtype, device=dev), n
+    else:
+        ldo = _matrix(_like(out, "out", shape, out_dtype), "out")[2]
+        _device(codes, out)
+    _launch(dev, lib.mx_dequantize, rows, n, codes.data_ptr(), kind, ldc, scale.data_ptr(), lds, out.data_ptr(), dtype, ldo)
     return out
 
 
@@ -276,7 +332,7 @@ def _workspace(dev, nbytes):
     would run with the graph's replays only."""
     if nbytes == 0:
         return None
-    key = (dev, torch.cuda.current_stream(dev).cuda_stream)
+    key = (dev, _raw_stream(dev.index))
     ws = _workspaces.get(key)
     if ws is not None and ws.numel() >= nbytes:
         return ws
@@ -296,8 +352,11 @@ def mx_matmul_workspace_bytes(M, N, K):
 
 def _rows_readable(scale, rows, lds):
     """Whether every scale row can be read to the end of its last 4-byte word."""
+    blocks = scale.shape[-1]
+    if blocks % 4 == 0:
+        return True
     last = scale.storage_offset() + (rows - 1) * lds
-    return scale.untyped_storage().nbytes() - last >= (scale.shape[-1] + 3) // 4 * 4
+    return scale.untyped_storage().nbytes() - last >= (blocks + 3) // 4 * 4
 
 
 def mx_matmul(A, a_scale, W, w_scale, act_scale=None, out_dtype=torch.float32, out=None, workspace=None):
@@ -313,36 +372,43 @@ def mx_matmul(A, a_scale, W, w_scale, act_scale=None, out_dtype=torch.float32, o
     stream) or a zero-filled uint8 tensor of at least
     mx_matmul_workspace_bytes(M, N, K) bytes."""
     for t, name in ((A, "A"), (W, "W")):
-        _need(t, tuple(_CODES) if name == "A" else (torch.uint8,), name)
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
         if t.dim() != 2:
             raise ValueError(f"{name} must be 2-D")
-    if out_dtype not in _FLOATS:
+    if W.dtype is not torch.uint8:
+        _need(W, (torch.uint8,), "W")
+    dtype = _FLOATS.get(out_dtype)
+    if dtype is None:
         raise TypeError(f"out_dtype must be one of {tuple(_FLOATS)}")
-    M, K, lda, ldas = _mx_operand(A, a_scale, "A")
-    N, K2, ldw, ldws = _mx_operand(W, w_scale, "W")
+    kind, M, K, lda, ldas = _mx_operand(A, a_scale, "A")
+    _, N, K2, ldw, ldws = _mx_operand(W, w_scale, "W")
     if K != K2:
         raise ValueError(f"inner dimensions differ: A has {K} columns, W has {K2}")
-    ts = [A, a_scale, W, w_scale]
     if act_scale is not None:
         _need(act_scale, (torch.float32,), "act_scale")
-        if act_scale.dim() == 0 or tuple(act_scale.shape) in ((1,), (1, 1)):
+        shape = tuple(act_scale.shape)
+        if shape in ((), (1,), (1, 1)) and M != 1:
             act_scale = act_scale.reshape(1).expand(M)
-        elif tuple(act_scale.shape) not in ((M,), (M, 1)):
-            raise ValueError(f"act_scale of shape {tuple(act_scale.shape)} is not [M], [M,1] or scalar (M={M})")
-        act_scale = act_scale.reshape(-1).contiguous()
-        ts.append(act_scale)
-    dev = _on_gpu(*ts)
-    out = _like(out, "out", (M, N), out_dtype, dev)
-    _on_gpu(A, out)
+        elif shape not in ((), (1,), (M,), (M, 1)):
+            raise ValueError(f"act_scale of shape {shape} is not [M], [M,1] or scalar (M={M})")
+        if not act_scale.is_contiguous():
+            act_scale = act_scale.contiguous()
+    dev = _device(A, a_scale, W, w_scale, act_scale)
+    if out is None:
+        out, ldo = torch.empty((M, N), dtype=out_dtype, device=dev), N
+    else:
+        ldo = _matrix(_like(out, "out", (M, N), out_dtype), "out")[2]
+        _device(A, out)
     if M == 0 or N == 0:
         return out
     if workspace is None:
-        workspace = _workspace(dev, mx_matmul_workspace_bytes(M, N, K))
+        workspace = _workspace(dev, lib.mx_matmul_workspace_bytes(M, N, K))
     else:
         _need(workspace, (torch.uint8, torch.int8), "workspace")
-        _on_gpu(A, workspace)
+        _device(A, workspace)
     padded = _rows_readable(a_scale, M, ldas) and _rows_readable(w_scale, N, ldws)
-    _launch(dev, lib.mx_matmul, M, N, K, _ptr(A), _CODES[A.dtype], lda, _ptr(a_scale), ldas, _ptr(W), ldw,
-            _ptr(w_scale), ldws, int(padded), _ptr(act_scale), _ptr(out), _FLOATS[out_dtype],
-            _matrix(out, "out")[2], _ptr(workspace), 0 if workspace is None else workspace.numel())
+    _launch(dev, lib.mx_matmul, M, N, K, A.data_ptr(), kind, lda, a_scale.data_ptr(), ldas, W.data_ptr(), ldw,
+            w_scale.data_ptr(), ldws, padded, _at(act_scale), out.data_ptr(), dtype, ldo, _at(workspace),
+            0 if workspace is None else workspace.numel())
     return out
