@@ -1,6 +1,6 @@
 // 128 x 128 tiles of the MX product: four waves of 64 x 64.  MXFP4: stages of
-// 256 values of K, two of them (68 KiB, two workgroups per CU); MXFP8
-// activations: 128 values, three (75 KiB).
+// 256 values of K, two of them (72 KiB, two workgroups per CU); MXFP8
+// activations: 128 values, three (80 KiB).
 #include "mx_tiled_impl.h"
 
 namespace qg {

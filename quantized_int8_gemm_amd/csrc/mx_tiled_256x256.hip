@@ -1,6 +1,6 @@
 // 256 x 256 tiles of the MX product: eight waves of 128 x 64.  MXFP4: stages of
-// 256 values of K, two of them (136 KiB); MXFP8 activations: 128 values, three
-// (150 KiB).
+// 256 values of K, two of them (144 KiB with the scales); MXFP8 activations: 128
+// values, three (160 KiB).
 #include "mx_tiled_impl.h"
 
 namespace qg {

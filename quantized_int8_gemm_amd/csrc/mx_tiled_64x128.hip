@@ -1,5 +1,5 @@
 // 64 x 128 tiles of the MX product: four waves of 32 x 64, stages of 256 values
-// of K, two of them (MXFP4 51 KiB, MXFP8 activations 67 KiB).
+// of K, two of them (MXFP4 56 KiB, MXFP8 activations 72 KiB).
 #include "mx_tiled_impl.h"
 
 namespace qg {

@@ -3,16 +3,34 @@
 //
 // A workgroup computes a BM x BN tile of the output, K in stages of NB blocks
 // (32 NB values) held in a ring of STAGES LDS stages:
-//  * Code rows of A and W go global -> LDS in 16-byte segments, scale bytes in
-//    4-byte words, STAGES - 1 stages ahead of the one being multiplied.  Each
-//    lane's bytes land at consecutive LDS addresses, so the lane picks the
-//    global segment whose swizzled home is that address.  Rows past M or N, and
+//  * Code rows of A and W go global -> LDS in 16-byte segments.  Each lane's
+//    bytes land at consecutive LDS addresses, so the lane picks the global
+//    segment whose swizzled home is that address.  Rows past M or N, and
 //    segments past K, lie outside the buffer windows and read as zero.
+//  * Scale bytes come in groups of 16 a row (2 or 4 stages' worth) into two
+//    places beside the ring, a part of the next group with every stage.  Fetched
+//    a stage's 8 bytes at a time they asked L2 for as many cache lines as the
+//    codes did: 8192^3 MXFP4 292 us so, 276 us in groups.
 //  * The contraction may visit blocks in any order, so that a lane's scales lie
 //    side by side: the two lane groups of a 32x32x64 instruction take blocks s
 //    and NB/2 + s of the stage in step s.  One NB/2-byte read per fragment row
 //    then brings the scales of the whole stage, and the instruction picks the
 //    byte.
+//  * While a step's products run, the next step's fragments are read, across the
+//    stages' border too: the barrier stands before the stage's last step, when
+//    every wave holds the last fragments of the old stage, so its ring place is
+//    free for the chunk STAGES on, whose loads are spread over that step and the
+//    next (all at once they hold the matrix instructions up: 287 us).  Against
+//    reading after the barrier: 8192^3 303 -> 292 us, 4096^3 with MXFP8
+//    activations 62.8 -> 58.3 us.
+// What bounds it (8192^3 MXFP4, 276 us, 4.0 PFLOP/s): the instruction alone on
+// register operands runs at 7.1 PFLOP/s on random data, the clock falling from
+// 2.4 to 1.7 GHz (9.7 PFLOP/s on zeros); here the matrix cores are busy 53 % of
+// the cycles at 1.8 GHz.  The same kernel without its loads takes 223 us, without
+// its fragment reads 265, without its products 226, with neither reads nor
+// products 172: the loads' path (64 B a cycle and CU) is busy half of the time and
+// what is left is that these streams do not overlap fully.  Four waves of 128 x
+// 128 (a third fewer fragment reads, one wave per SIMD) measured 284 us.
 //  * The finished wave tile goes through LDS, 32 rows at a time, and leaves in
 //    whole rows of 64 columns.
 // SK: blockIdx.y divides K into ranges of split_k values; each range leaves its
@@ -84,6 +102,14 @@ __device__ __forceinline__ v16f mfma_step(int s, v8i w, uint32_t ws, v8i a, uint
 
 constexpr uint32_t OUTSIDE = 0xffffff00u;   // past every window
 
+// A wave-uniform value that the compiler takes as it is: address sums stay one
+// vector addition next to their use instead of a register each across the loop.
+__device__ __forceinline__ uint32_t scalar(uint32_t v) {
+    v = __builtin_amdgcn_readfirstlane(v);
+    asm volatile("" : "+s"(v));
+    return v;
+}
+
 template <int BM, int BN, int WM, int WN, int NB, int STAGES, bool A8, typename T, bool SK>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(MxMatmulArgs p) {
     constexpr bool EXACT = A8 && sizeof(T) == 4;
@@ -91,19 +117,22 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(Mx
     constexpr int FM = WM / 32, FN = WN / 32, NS = NB / 2;
     constexpr int AW = NB * (A8 ? 32 : 16), WW = NB * 16;         // bytes of a stage's code rows
     constexpr int A_BYTES = BM * AW, W_BYTES = BN * WW;
-    constexpr int S_BYTES = ((BM + BN) * NB + NT * 4 - 1) / (NT * 4) * (NT * 4);   // whole load rounds, the excess unused
-    constexpr int STAGE = A_BYTES + W_BYTES + S_BYTES;
-    constexpr int A_ROUNDS = A_BYTES / (NT * 16), W_ROUNDS = W_BYTES / (NT * 16), S_ROUNDS = S_BYTES / (NT * 4);
-    constexpr int LOADS = A_ROUNDS + W_ROUNDS + S_ROUNDS;
-    constexpr int OB = sizeof(T);
-    static_assert(WN == 64, "output staging");
+    constexpr int STAGE = A_BYTES + W_BYTES;
+    constexpr int A_ROUNDS = A_BYTES / (NT * 16), W_ROUNDS = W_BYTES / (NT * 16), LOADS = A_ROUNDS + W_ROUNDS;
+    // Scales: groups of 16 bytes a row, Q stages' worth, in two places of their
+    // own; a stage loads one Qth of the group after its own.
+    constexpr int Q = 16 / NB;
+    constexpr int S_ROUNDS = ((BM + BN) * 4 + NT * Q - 1) / (NT * Q);   // per stage; rows past BM + BN are unused
+    constexpr int GROUP = S_ROUNDS * Q * NT * 4, SCALES = STAGES * STAGE;
+    constexpr int OB = sizeof(T), AV = A8 ? 2 : 1;
+    static_assert(WN % 64 == 0, "output staging");
     static_assert(A_BYTES % (NT * 16) == 0 && W_BYTES % (NT * 16) == 0, "whole load rounds");
-    static_assert((BM * NB) % 256 == 0, "a wave's scale words are of one operand");
-    static_assert(LOADS * (STAGES - 2) < 64, "vmcnt range");
-    static_assert(STAGES * STAGE >= NW * 32 * WN * OB, "output staging fits the stage ring");
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * STAGE];
+    static_assert(BM % 16 == 0, "a wave's scale words are of one operand");
+    static_assert(LOADS * (STAGES - 1) < 64, "vmcnt range");
+    static_assert(STAGES * STAGE >= NW * 32 * 64 * OB, "output staging fits the stage ring");
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * STAGE + 2 * GROUP];
 
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WAVES_N, wn = wave % WAVES_N;
     const int g = lane >> 5, r32 = lane & 31;
 
@@ -126,46 +155,44 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(Mx
     const v4i ws_rsrc = rsrc_words(p.ws + (int64_t)n0 * p.ldws + kb0, (uint32_t)((rows_w - 1) * ldws) + s_span);
     const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
-    // Global offset (stage 0) and block of each load round's segment.
-    uint32_t a_off[A_ROUNDS], w_off[W_ROUNDS], s_off[S_ROUNDS];
-    int a_blk[A_ROUNDS], w_blk[W_ROUNDS], s_blk[S_ROUNDS];
-#pragma unroll
-    for (int q = 0; q < A_ROUNDS; ++q) {
-        const int o = (q * NT + tid) * 16, r = o / AW, s = slot<AW>(r, (o % AW) / 16);
-        a_off[q] = (uint32_t)(r * lda + 16 * s);
-        a_blk[q] = 16 * s / ABLK;
-    }
-#pragma unroll
-    for (int q = 0; q < W_ROUNDS; ++q) {
-        const int o = (q * NT + tid) * 16, r = o / WW, s = slot<WW>(r, (o % WW) / 16);
-        w_off[q] = (uint32_t)(r * ldw + 16 * s);
-        w_blk[q] = s;
-    }
-#pragma unroll
-    for (int q = 0; q < S_ROUNDS; ++q) {
-        const int o = (q * NT + tid) * 4, r = o / NB;
-        s_blk[q] = o % NB;
-        s_off[q] = (uint32_t)((r < BM ? r * ldas : (r - BM) * ldws) + s_blk[q]);
-    }
+    // Global offset (stage 0) and block of this lane's segment in a load round.
+    // A round covers a multiple of 16 rows, so all rounds of an operand take the
+    // same segment, a fixed number of rows apart.
+    constexpr int A_ROWS = NT * 16 / AW, W_ROWS = NT * 16 / WW;
+    static_assert(A_ROWS % 16 == 0 && W_ROWS % 16 == 0, "one swizzle for all rounds");
+    const int a_seg = slot<AW>(tid * 16 / AW, tid * 16 % AW / 16), w_seg = slot<WW>(tid * 16 / WW, tid * 16 % WW / 16);
+    const uint32_t a_off = (uint32_t)(tid * 16 / AW * lda + 16 * a_seg), w_off = (uint32_t)(tid * 16 / WW * ldw + 16 * w_seg);
     const int nk = (nblk + NB - 1) / NB;
-    const bool ragged = nblk % NB != 0;
 
-    auto issue = [&](int kt, int stage) {
-        const uint32_t base = lds0 + stage * STAGE, codes = base + wave * 1024;
-        const bool tail = ragged && kt == nk - 1;
-        const int rest = nblk - kt * NB;
+    // Part `part` of PARTS of the loads of chunk kt.  Blocks past K, whole chunks
+    // too, are read from outside the windows: every chunk issues the same loads,
+    // so the loop has no branches and its waits are constants.
+    constexpr int PARTS = 2 * FM;
+    auto issue = [&](int kt, int stage, int part) {
+        const uint32_t base = lds0 + (uint32_t)stage * STAGE, codes = base + wave * 1024;
+        const uint32_t ka = scalar(kt * AW), kw = scalar(kt * WW);
+        const int rest = nblk - kt * NB;   // blocks from this chunk on
 #pragma unroll
-        for (int q = 0; q < A_ROUNDS; ++q)
-            dma16(a_rsrc, tail && a_blk[q] >= rest ? OUTSIDE : a_off[q] + (uint32_t)(kt * AW), codes + q * NT * 16);
+        for (int i = part * LOADS / PARTS; i < (part + 1) * LOADS / PARTS; ++i) {
+            if (i < A_ROUNDS) {
+                dma16(a_rsrc, 16 * a_seg / ABLK >= rest ? OUTSIDE : a_off + ((uint32_t)(i * A_ROWS * lda) + ka), codes + i * NT * 16);
+            } else {
+                const int q = i - A_ROUNDS;
+                dma16(w_rsrc, w_seg >= rest ? OUTSIDE : w_off + ((uint32_t)(q * W_ROWS * ldw) + kw), codes + A_BYTES + q * NT * 16);
+            }
+        }
+    };
+    // Rounds q0 .. of the 4-byte words of scale group j, four lanes to a row.
+    auto issue_scales = [&](int j, int q0) {
+        const uint32_t base = lds0 + SCALES + (uint32_t)(j & 1) * GROUP + wave * 256;
+        const uint32_t blk = (uint32_t)(j * 16 + tid % 4 * 4);
 #pragma unroll
-        for (int q = 0; q < W_ROUNDS; ++q)
-            dma16(w_rsrc, tail && w_blk[q] >= rest ? OUTSIDE : w_off[q] + (uint32_t)(kt * WW), codes + A_BYTES + q * NT * 16);
-#pragma unroll
-        for (int q = 0; q < S_ROUNDS; ++q) {
-            const bool of_a = __builtin_amdgcn_readfirstlane((q * NT + wave * 64) * 4 < BM * NB ? 1 : 0);
-            const bool none = ((q * NT + tid) * 4 >= (BM + BN) * NB) || (tail && s_blk[q] >= rest);
-            dma4(of_a ? as_rsrc : ws_rsrc, none ? OUTSIDE : s_off[q] + (uint32_t)(kt * NB),
-                 base + A_BYTES + W_BYTES + wave * 256 + q * NT * 4);
+        for (int i = 0; i < S_ROUNDS; ++i) {
+            const int q = q0 + i, first = q * (NT / 4) + wave * 16, r = first + lane / 4;
+            const bool of_a = first < BM;
+            const bool none = first >= BM + BN || (int)blk >= nblk;
+            const uint32_t at = (uint32_t)(of_a ? r * ldas : (r - BM) * ldws) + blk;
+            dma4(of_a ? as_rsrc : ws_rsrc, none ? OUTSIDE : at, base + q * NT * 4);
         }
     };
 
@@ -184,73 +211,122 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(Mx
         row_scale[a] = p.act_scale != nullptr && m < p.M ? p.act_scale[m] : 1.0f;
     }
 
-    auto read16 = [&](const uint8_t* at) { return *reinterpret_cast<const u32x4*>(at); };
-    auto read_a = [&](const uint8_t* S, int a, int s) -> v8i {
-        const uint8_t* row = S + (wm * WM + a * 32 + r32) * AW;
-        if constexpr (A8)
-            return words8(read16(row + 16 * slot<AW>(r32, 2 * s + g)), read16(row + 16 * slot<AW>(r32, 2 * (NS + s) + g)));
-        else
-            return words4(read16(row + 16 * slot<AW>(r32, g * NS + s)));
+    auto read16 = [&](const uint8_t* at) {   // as a vector type, which is 16-byte aligned
+        const v4i v = *reinterpret_cast<const v4i*>(at);
+        return u32x4{(uint32_t)v.x, (uint32_t)v.y, (uint32_t)v.z, (uint32_t)v.w};
     };
-    auto read_w = [&](const uint8_t* S, int b, int s) -> v8i {
-        return words4(read16(S + A_BYTES + (wn * WN + b * 32 + r32) * WW + 16 * slot<WW>(r32, g * NS + s)));
-    };
-    auto read_scale = [&](const uint8_t* S, int row) -> uint32_t {
-        const uint8_t* at = S + A_BYTES + W_BYTES + row * NB + g * NS;
-        if constexpr (NS == 4) return *reinterpret_cast<const uint32_t*>(at);
-        else return *reinterpret_cast<const uint16_t*>(at);
+    // Where in a stage this lane's fragment of step s and row block 0 lies, and
+    // its scales; e2m1 fragments are held in four registers and widened at the
+    // instruction.
+    uint32_t a_at[NS][AV], w_at[NS], as_at = SCALES + (wm * WM + r32) * 16 + g * NS;
+    uint32_t ws_at = SCALES + (BM + wn * WN + r32) * 16 + g * NS;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+        const uint32_t row = (wm * WM + r32) * AW;
+        if constexpr (A8) {
+            a_at[s][0] = row + 16 * slot<AW>(r32, 2 * s + g);
+            a_at[s][AV - 1] = row + 16 * slot<AW>(r32, 2 * (NS + s) + g);
+        } else {
+            a_at[s][0] = row + 16 * slot<AW>(r32, g * NS + s);
+        }
+        w_at[s] = A_BYTES + (wn * WN + r32) * WW + 16 * slot<WW>(r32, g * NS + s);
+    }
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+#pragma unroll
+        for (int v = 0; v < AV; ++v) asm volatile("" : "+v"(a_at[s][v]));
+        asm volatile("" : "+v"(w_at[s]));
+    }
+    asm volatile("" : "+v"(as_at), "+v"(ws_at));
+    auto read_scale = [&](const uint8_t* at) -> uint32_t {
+        if constexpr (NS == 4) return *reinterpret_cast<const uint32_t*>(__builtin_assume_aligned(at, 4));
+        else return *reinterpret_cast<const uint16_t*>(__builtin_assume_aligned(at, 2));
     };
 
-    auto compute = [&](int stage, int next_kt, int kt) {
-        const uint8_t* S = smem + stage * STAGE;
-        uint32_t as[FM], ws[FN];
+    // Fragments of the current step and the next; scales of the chunk, and of
+    // the next one as read.
+    u32x4 af[2][FM][AV], wf[2][FN];
+    uint32_t as[FM], ws[FN], as_read[FM], ws_read[FN];
+    auto read_scales = [&](int kt) {
+        const uint8_t* S = smem + scalar((uint32_t)(kt / Q & 1) * GROUP + (uint32_t)(kt % Q) * NB);
 #pragma unroll
-        for (int b = 0; b < FN; ++b) ws[b] = read_scale(S, BM + wn * WN + b * 32 + r32);
+        for (int b = 0; b < FN; ++b) ws_read[b] = read_scale(S + ws_at + b * 512);
 #pragma unroll
-        for (int a = 0; a < FM; ++a) as[a] = read_scale(S, wm * WM + a * 32 + r32);
-        v8i wf[NS][FN];
+        for (int a = 0; a < FM; ++a) as_read[a] = read_scale(S + as_at + a * 512);
+    };
+    auto read_w = [&](const uint8_t* S, int s, int buf) {
 #pragma unroll
-        for (int b = 0; b < FN; ++b) wf[0][b] = read_w(S, b, 0);
-        v8i a_next = read_a(S, 0, 0);
+        for (int b = 0; b < FN; ++b) wf[buf][b] = read16(S + w_at[s] + b * 32 * WW);
+    };
+    auto read_a = [&](const uint8_t* S, int a, int s, int buf) {
 #pragma unroll
-        for (int s = 1; s < NS; ++s)
-#pragma unroll
-            for (int b = 0; b < FN; ++b) wf[s][b] = read_w(S, b, s);
-        __builtin_amdgcn_sched_barrier(0);
-        if (next_kt >= 0) issue(next_kt, next_kt % STAGES);
-        __builtin_amdgcn_sched_barrier(0);
-        if (ragged && kt == nk - 1) {
+        for (int v = 0; v < AV; ++v) af[buf][a][v] = read16(S + a_at[s][v] + a * 32 * AW);
+    };
+    // Step s of chunk kt in ring place `stage`: the products of the fragments at
+    // hand, while those of the next step (at the stage's end, of the next chunk)
+    // are read.
+    auto step = [&](int kt, int stage, int s) {
+        const bool last = s == NS - 1;
+        const int ns = last ? 0 : s + 1, cur = s & 1, nxt = cur ^ 1, after = stage + 1 == STAGES ? 0 : stage + 1;
+        const uint8_t* S = smem + scalar((uint32_t)(last ? after : stage) * STAGE);
+        if (s == 0) {
             // scale bytes past K may be anything: 0 (2^-127) times the zero codes there
             const int rest = nblk - kt * NB - g * NS;
             const uint32_t mask = rest >= 4 ? ~0u : (rest <= 0 ? 0u : (1u << (8 * rest)) - 1u);
 #pragma unroll
-            for (int b = 0; b < FN; ++b) ws[b] &= mask;
+            for (int b = 0; b < FN; ++b) ws[b] = ws_read[b] & mask;
 #pragma unroll
-            for (int a = 0; a < FM; ++a) as[a] &= mask;
+            for (int a = 0; a < FM; ++a) as[a] = as_read[a] & mask;
         }
 #pragma unroll
-        for (int s = 0; s < NS; ++s) {
-#pragma unroll
-            for (int a = 0; a < FM; ++a) {
-                const v8i af = a_next;
-                if (a + 1 < FM) a_next = read_a(S, a + 1, s);
-                else if (s + 1 < NS) a_next = read_a(S, 0, s + 1);
-                __builtin_amdgcn_sched_barrier(0);   // the next read goes ahead of these products
-#pragma unroll
-                for (int b = 0; b < FN; ++b) acc[a][b] = mfma_step<A8, EXACT>(s, wf[s][b], ws[b], af, as[a], acc[a][b]);
+        for (int a = 0; a < FM; ++a) {
+            // W's fragments go first: every product of the next step needs one
+            if (a == 0) read_w(S, ns, nxt);
+            read_a(S, a, ns, nxt);
+            if (last && a == 0) {
+                read_scales(kt + 1);
+                issue_scales((kt + 1) / Q + 1, (kt + 1) % Q * S_ROUNDS);
             }
+            if (last) issue(kt + STAGES, stage, a);
+            if (s == 0) issue(kt + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1, FM + a);
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int b = 0; b < FN; ++b)
+                acc[a][b] = mfma_step<A8, EXACT>(s, words4(wf[cur][b]), ws[b], A8 ? words8(af[cur][a][0], af[cur][a][AV - 1]) : words4(af[cur][a][0]),
+                                                 as[a], acc[a][b]);
+            __builtin_amdgcn_sched_barrier(0);
         }
     };
+    static_assert(NS % 2 == 0, "a stage ends on the buffers it began with");
 
 #pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s)
-        if (s < nk) issue(s, s);
+    for (int q = 0; q < Q; ++q) issue_scales(0, q * S_ROUNDS);
+#pragma unroll
+    for (int part = 0; part < PARTS; ++part) issue(0, 0, part);
+    issue_scales(1, 0);
+#pragma unroll
+    for (int c = 1; c < STAGES; ++c)
+#pragma unroll
+        for (int part = 0; part < (c < STAGES - 1 ? PARTS : FM); ++part) issue(c, c, part);
+    // chunk 0 and its scales have landed once at most the loads after them are outstanding
+    wait_vmcnt<S_ROUNDS + LOADS * (STAGES - 2) + FM * LOADS / PARTS>();
+    __syncthreads();
+    read_w(smem, 0, 0);
+#pragma unroll
+    for (int a = 0; a < FM; ++a) read_a(smem, a, 0, 0);
+    read_scales(0);
+    int stage = 0;
     for (int kt = 0; kt < nk; ++kt) {
-        if (kt + STAGES - 2 < nk) wait_vmcnt<LOADS * (STAGES - 2)>();
-        else wait_vmcnt<0>();
+#pragma unroll
+        for (int s = 0; s < NS - 1; ++s) step(kt, stage, s);
+        // the next chunk is there, with the scale words issued ahead of the loads
+        // that may be outstanding, and every wave has read this chunk's last fragments
+        wait_vmcnt<LOADS * (STAGES - 2)>();
         __syncthreads();
-        compute(kt % STAGES, kt + STAGES - 1 < nk ? kt + STAGES - 1 : -1, kt);
+        step(kt, stage, NS - 1);
+        stage = stage + 1 == STAGES ? 0 : stage + 1;
     }
+    wait_vmcnt<0>();   // loads past K write zeros
     __syncthreads();   // every wave is done with the stage ring
 
     if constexpr (SK) {
@@ -307,47 +383,49 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(Mx
         }
     }
 
-    // 32 rows of the wave's tile at a time through the wave's own piece of LDS:
+    // 32 rows and 64 columns of the wave's tile at a time through the wave's own piece of LDS:
     // register 4 q + i of a lane is row r32, column 8 q + 4 g + i.  Chunk c (16
     // bytes) of a staged row lies at c ^ swizzle, so neither side collides.
-    constexpr int PITCH = WN * OB, CPR = PITCH / 16, PER = 16 / OB, RPI = 64 / CPR;   // rows per store instruction
-    uint8_t* stage = smem + wave * 32 * PITCH;
+    constexpr int PITCH = 64 * OB, CPR = PITCH / 16, PER = 16 / OB, RPI = 64 / CPR;   // rows per store instruction
+    uint8_t* own = smem + wave * 32 * PITCH;
     T* out = reinterpret_cast<T*>(p.out);
     const bool vec = (p.ldo * OB) % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
     auto swiz = [](int row, int c) { return OB == 2 ? c ^ ((row >> 1) & 7) : c ^ (row & 15); };
 #pragma unroll
-    for (int a = 0; a < FM; ++a) {
+    for (int a = 0; a < FM; ++a)
 #pragma unroll
-        for (int b = 0; b < FN; ++b)
+        for (int h = 0; h < FN; h += 2) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                T t[4];
+            for (int b = 0; b < 2; ++b)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) t[i] = (T)(acc[a][b][4 * q + i] * row_scale[a]);
-                const int byte = (b * 32 + 8 * q + 4 * g) * OB;
-                __builtin_memcpy(__builtin_assume_aligned(stage + r32 * PITCH + 16 * swiz(r32, byte / 16) + byte % 16, 4 * OB), t, 4 * OB);
-            }
-        __builtin_amdgcn_wave_barrier();
+                for (int q = 0; q < 4; ++q) {
+                    T t[4];
 #pragma unroll
-        for (int k = 0; k < 32 / RPI; ++k) {
-            const int row = k * RPI + lane / CPR, c = lane % CPR;
-            const u32x4 v = read16(stage + row * PITCH + 16 * swiz(row, c));
-            const int m = m0 + wm * WM + a * 32 + row, n = n0 + wn * WN + c * PER;
-            if (m < p.M && n < p.N) {
-                T* dst = out + (int64_t)m * p.ldo + n;
-                if (vec && n + PER <= p.N) {
-                    *reinterpret_cast<u32x4*>(dst) = v;
-                } else {
-                    T e[PER];
-                    __builtin_memcpy(e, &v, 16);
+                    for (int i = 0; i < 4; ++i) t[i] = (T)(acc[a][h + b][4 * q + i] * row_scale[a]);
+                    const int byte = (b * 32 + 8 * q + 4 * g) * OB;
+                    __builtin_memcpy(__builtin_assume_aligned(own + r32 * PITCH + 16 * swiz(r32, byte / 16) + byte % 16, 4 * OB), t, 4 * OB);
+                }
+            __builtin_amdgcn_wave_barrier();
 #pragma unroll
-                    for (int i = 0; i < PER; ++i)
-                        if (n + i < p.N) dst[i] = e[i];
+            for (int k = 0; k < 32 / RPI; ++k) {
+                const int row = k * RPI + lane / CPR, c = lane % CPR;
+                const u32x4 v = read16(own + row * PITCH + 16 * swiz(row, c));
+                const int m = m0 + wm * WM + a * 32 + row, n = n0 + wn * WN + h * 32 + c * PER;
+                if (m < p.M && n < p.N) {
+                    T* dst = out + (int64_t)m * p.ldo + n;
+                    if (vec && n + PER <= p.N) {
+                        *reinterpret_cast<u32x4*>(dst) = v;
+                    } else {
+                        T e[PER];
+                        __builtin_memcpy(e, &v, 16);
+#pragma unroll
+                        for (int i = 0; i < PER; ++i)
+                            if (n + i < p.N) dst[i] = e[i];
+                    }
                 }
             }
+            __builtin_amdgcn_wave_barrier();
         }
-        __builtin_amdgcn_wave_barrier();
-    }
 }
 
 template <int BM, int BN, int WM, int WN, int NB, int STAGES, bool A8, bool SK>
