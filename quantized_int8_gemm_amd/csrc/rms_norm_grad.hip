@@ -5,6 +5,9 @@
 // workgroup walks rows with a fixed set of columns per lane, so dw is added up
 // in registers and leaves once, as one row of partial sums per workgroup; a
 // second kernel adds those.  No atomics: the order of every sum is fixed.
+// 8192 x 4096 bf16 with dh: 49.7 us both kernels, 5.4 TB/s (a copy of 2 GiB runs at
+// 4.85); 86.9 us with one row at a time in the registers as single values, which
+// left two waves per SIMD nothing in flight between the barrier and the stores.
 #include "mx_common.h"
 
 namespace qg {
@@ -26,74 +29,114 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 }
 
 // The lane's columns are (i * G + t) * 8 .. + 7.  Row groups of G < 256 lanes
-// share a workgroup; their partial sums of dw are added through LDS.
-template <typename T, int G, int ITER, bool WF32>
-__global__ __launch_bounds__(G < 256 ? 256 : G) void rms_norm_grad_kernel(RmsNormGradArgs a) {
+// share a workgroup; their partial sums of dw are added through LDS.  How a row
+// passes through the registers:
+//  * AHEAD, up to 256 lanes: the next row's loads are in flight while this one's
+//    sum is completed and its results are stored;
+//  * HOLD, 512 and 1024 lanes: one row at a time, in at most 128 registers, so
+//    that two workgroups share a CU and one's loads cover the other's barrier
+//    (5000 x 6144 bf16 54.7 us, AHEAD 59.3; 2000 x 16384 55.6, AHEAD 63.9);
+//  * AGAIN, past 16384 columns, where dw alone takes 32 or 64 registers: a row is
+//    read once for its sum and again, from the caches, for its results.
+enum { AHEAD, HOLD, AGAIN };
+
+template <typename T, int G, int ITER, bool WF32, bool TINY, bool NT>
+__global__ __launch_bounds__(G < 256 ? 256 : G, G < 512 ? 1 : 4) void rms_norm_grad_kernel(RmsNormGradArgs a) {
+    typedef typename std::conditional<WF32, float, T>::type W;
     constexpr int RPW = G < 256 ? 256 / G : 1;
+    constexpr int MODE = G < 512 ? AHEAD : ITER <= 2 ? HOLD : AGAIN;
+    constexpr int WI = MODE == AGAIN ? 1 : ITER, BUFS = MODE == AHEAD ? 2 : 1;
     __shared__ float red[2][G / 64];
     __shared__ float part[RPW > 1 ? (RPW - 1) * G * ITER * 8 : 1];
-    const int t = threadIdx.x % G, sub = threadIdx.x / G;
+    const int t = threadIdx.x % G, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / G);
     const int n = a.n;
-    float w[ITER][8], dw[ITER][8];
+    float w[WI][8], dw[ITER][8];
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
-        const int c = (i * G + t) * 8;
-        if constexpr (WF32) {
-            Pack8<float> p;
-            load8(reinterpret_cast<const float*>(a.weight) + c, n - c, p);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[i][e] = p.v[e];
-        } else {
-            Pack8<T> p;
-            load8(reinterpret_cast<const T*>(a.weight) + c, n - c, p);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) w[i][e] = (float)p.v[e];
-        }
+        if constexpr (MODE != AGAIN) load_weights<W, TINY>(a.weight, (i * G + t) * 8, n, w[i]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
     }
-    int turn = 0;
-    for (int64_t row = (int64_t)blockIdx.x * RPW + sub; row < a.M; row += (int64_t)gridDim.x * RPW, turn ^= 1) {
-        const T* dy = reinterpret_cast<const T*>(a.dy) + row * a.ldy;
-        const T* h = reinterpret_cast<const T*>(a.h) + row * a.ldh;
-        Pack8<T> yv[ITER], hv[ITER], sv[ITER];
+    Pack8<T> yv[BUFS][WI], hv[BUFS][WI], sv[BUFS][WI] = {};
+    float rv[BUFS];
+    const int step = (int)gridDim.x * RPW, M = (int)a.M;   // M + step < 2^31
+    auto fetch = [&](int row, int i, int buf, int at, bool also) {
+        const int c = (i * G + t) * 8;
+        load8<TINY, NT && MODE != AGAIN>(reinterpret_cast<const T*>(a.dy) + (int64_t)row * a.ldy, c, n, yv[buf][at]);
+        load8<TINY, NT && MODE != AGAIN>(reinterpret_cast<const T*>(a.h) + (int64_t)row * a.ldh, c, n, hv[buf][at]);
+        if (also && a.dh != nullptr) load8<TINY, NT>(reinterpret_cast<const T*>(a.dh) + (int64_t)row * a.lddh, c, n, sv[buf][at]);
+    };
+    auto fetch_row = [&](int row, int buf) {
+        if constexpr (MODE != AGAIN) {
+#pragma unroll
+            for (int i = 0; i < ITER; ++i) fetch(row, i, buf, i, true);
+        }
+        rv[buf] = a.rstd[row];
+    };
+    auto hold_packed = [&](int buf) {
+#pragma unroll
+        for (int i = 0; i < WI; ++i) {
+            stay_packed(yv[buf][i]);
+            stay_packed(hv[buf][i]);
+            stay_packed(sv[buf][i]);
+        }
+    };
+    // slot: two in turn, since a wave may be one row ahead of the others' reads
+    auto finish_row = [&](int row, int buf, int slot) {
+        const float r = rv[buf];
+        float dot = 0.f;
+        if constexpr (MODE != AGAIN) hold_packed(buf);
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
-            const int c = (i * G + t) * 8;
-            load8(dy + c, n - c, yv[i]);
-            load8(h + c, n - c, hv[i]);
-        }
-        if (a.dh != nullptr) {
-#pragma unroll
-            for (int i = 0; i < ITER; ++i) {
-                const int c = (i * G + t) * 8;
-                load8(reinterpret_cast<const T*>(a.dh) + row * a.lddh + c, n - c, sv[i]);
+            const int at = MODE == AGAIN ? 0 : i;
+            if constexpr (MODE == AGAIN) {
+                load_weights<W, TINY>(a.weight, (i * G + t) * 8, n, w[0]);
+                fetch(row, i, buf, 0, false);
             }
-        }
-        const float r = a.rstd[row];
-        float dot = 0.f;
-#pragma unroll
-        for (int i = 0; i < ITER; ++i)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float yh = (float)yv[i].v[e] * (float)hv[i].v[e];
-                dot = __builtin_fmaf(yh, w[i][e], dot);
+                const float yh = value(yv[buf][at], e) * value(hv[buf][at], e);
+                dot = __builtin_fmaf(yh, w[at][e], dot);
                 dw[i][e] = __builtin_fmaf(yh, r, dw[i][e]);
             }
-        // two slots taken in turn: a wave may be one row ahead of the others' reads
-        dot = row_sum<G>(dot, red[turn]);
+            __builtin_amdgcn_sched_barrier(0);   // one group unpacked at a time
+        }
+        dot = row_sum<G>(dot, red[slot]);
         const float k = r * r * r * (dot / (float)n);
+        if constexpr (MODE != AGAIN) hold_packed(buf);
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
-            const int c = (i * G + t) * 8;
-            Pack8<T> o;
+            const int c = (i * G + t) * 8, at = MODE == AGAIN ? 0 : i;
+            if constexpr (MODE == AGAIN) {
+                load_weights<W, TINY>(a.weight, c, n, w[0]);
+                fetch(row, i, buf, 0, true);
+            }
+            float o[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                float v = r * ((float)yv[i].v[e] * w[i][e]) - k * (float)hv[i].v[e];
-                if (a.dh != nullptr) v += (float)sv[i].v[e];
-                o.v[e] = (T)v;
+                o[e] = r * (value(yv[buf][at], e) * w[at][e]) - k * value(hv[buf][at], e);
+                if (a.dh != nullptr) o[e] += value(sv[buf][at], e);
             }
-            if (c < n) store8(reinterpret_cast<T*>(a.dx) + row * a.ldx + c, n - c, o);
+            if (c < n) store8(reinterpret_cast<T*>(a.dx) + (int64_t)row * a.ldx, c, n, pack<T>(o));
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    int row = (int)blockIdx.x * RPW + sub;
+    if constexpr (MODE == AHEAD) {
+        if (row < M) fetch_row(row, 0);
+        while (row < M) {
+            if (row + step < M) fetch_row(row + step, 1);
+            finish_row(row, 0, 0);
+            row += step;
+            if (row >= M) break;
+            if (row + step < M) fetch_row(row + step, 0);
+            finish_row(row, 1, 1);
+            row += step;
+        }
+    } else {
+        for (int turn = 0; row < M; row += step, turn ^= 1) {
+            fetch_row(row, 0);
+            finish_row(row, 0, turn);
         }
     }
     if constexpr (RPW > 1) {
@@ -116,32 +159,32 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void rms_norm_grad_kernel(RmsNor
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
         const int c = (i * G + t) * 8;
-        Pack8<float> o;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) o.v[e] = dw[i][e];
-        if (c < n) store8(out + c, n - c, o);
+        if (c < n) store8(out, c, n, pack<float>(dw[i]));
     }
 }
 
 // dw[j] = sum of the partial rows: 32 columns a workgroup (one 128-byte line
-// of each row), eight lanes a column, joined through LDS.
+// of each row), 32 lanes a column, joined through LDS.
+constexpr int SUM_ROWS = 32;
 template <typename W>
-__global__ __launch_bounds__(256) void rms_norm_grad_sum(const float* __restrict__ part, int parts, int n,
-                                                         W* __restrict__ dw) {
-    __shared__ float red[8][33];
+__global__ __launch_bounds__(32 * SUM_ROWS) void rms_norm_grad_sum(const float* __restrict__ part, int parts, int n,
+                                                                   W* __restrict__ dw) {
+    __shared__ float red[SUM_ROWS][33];
     const int cl = threadIdx.x & 31, q = threadIdx.x >> 5, c = blockIdx.x * 32 + cl;
     float s = 0.f;
     if (c < n) {
 #pragma unroll 8
-        for (int p = q; p < parts; p += 8) s += part[(int64_t)p * n + c];
+        for (int p = q; p < parts; p += SUM_ROWS) s += part[(int64_t)p * n + c];
     }
     red[q][cl] = s;
     __syncthreads();
-    if (q == 0 && c < n) {
+    if (q < 4) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += red[i][cl];
-        dw[c] = (W)s;
+        for (int i = 4; i < SUM_ROWS; i += 4) s += red[q + i][cl];
+        red[q][cl] = s;
     }
+    __syncthreads();
+    if (q == 0 && c < n) dw[c] = (W)(s + red[1][cl] + red[2][cl] + red[3][cl]);
 }
 
 // Lanes per row for n columns: as the kernel table below.
@@ -151,34 +194,42 @@ template <typename T, bool WF32>
 hipError_t by_width(const RmsNormGradArgs& a, hipStream_t s) {
     typedef typename std::conditional<WF32, float, T>::type W;
     bool done = a.M == 0;
-#define QG_GRAD(G, ITER)                                                                                       \
-    if (!done && a.n <= G * ITER * 8) {                                                                        \
-        hipLaunchKernelGGL((rms_norm_grad_kernel<T, G, ITER, WF32>), dim3((unsigned)a.parts),                  \
+#define QG_GRAD(G, ITER, LIMIT, TINY, NT)                                                                      \
+    if (!done && a.n <= LIMIT) {                                                                               \
+        hipLaunchKernelGGL((rms_norm_grad_kernel<T, G, ITER, WF32, TINY, NT>), dim3((unsigned)a.parts),        \
                            dim3(G < 256 ? 256 : G), 0, s, a);                                                  \
         done = true;                                                                                           \
     }
-    QG_GRAD(64, 1)
-    QG_GRAD(64, 2)
-    QG_GRAD(256, 1)
-    QG_GRAD(256, 2)
-    QG_GRAD(512, 2)
-    QG_GRAD(1024, 2)
-    QG_GRAD(1024, 4)
-    QG_GRAD(1024, 8)
+    QG_GRAD(64, 1, 7, true, false)
+    QG_GRAD(64, 1, 512, false, false)
+    QG_GRAD(64, 2, 1024, false, false)
+    QG_GRAD(256, 1, 2048, false, false)
+    if (whole_lines(a.dy, a.ldy * sizeof(T)) && whole_lines(a.h, a.ldh * sizeof(T)) &&
+        (a.dh == nullptr || whole_lines(a.dh, a.lddh * sizeof(T)))) {
+        QG_GRAD(256, 2, 4096, false, true)
+        QG_GRAD(512, 2, 8192, false, true)
+        QG_GRAD(1024, 2, 16384, false, true)
+    }
+    QG_GRAD(256, 2, 4096, false, false)
+    QG_GRAD(512, 2, 8192, false, false)
+    QG_GRAD(1024, 2, 16384, false, false)
+    QG_GRAD(1024, 4, 32768, false, false)
+    QG_GRAD(1024, 8, 65536, false, false)
 #undef QG_GRAD
     if (!done) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((rms_norm_grad_sum<W>), dim3((unsigned)((a.n + 31) / 32)), dim3(256), 0, s, a.part, a.parts, a.n,
+    hipLaunchKernelGGL((rms_norm_grad_sum<W>), dim3((unsigned)((a.n + 31) / 32)), dim3(32 * SUM_ROWS), 0, s, a.part, a.parts, a.n,
                        reinterpret_cast<W*>(a.dweight));
     return hipGetLastError();
 }
 
 }  // namespace
 
-// Workgroups of the row kernel, each with one partial row of dw: two per
-// compute unit, none without rows.
+// Workgroups of the row kernel, each with one partial row of dw, none without
+// rows: two per compute unit, or one for wide rows (2000 x 16384: the
+// partial rows of 512 workgroups are a quarter of what the gradient itself moves).
 int rms_norm_grad_parts(int64_t M, int64_t n) {
-    const int64_t groups = (M + rows_per_group(n) - 1) / rows_per_group(n);
-    return (int)(groups < 512 ? groups : 512);
+    const int64_t groups = (M + rows_per_group(n) - 1) / rows_per_group(n), most = n > 8192 ? 256 : 512;
+    return (int)(groups < most ? groups : most);
 }
 
 hipError_t launch_rms_norm_grad(const RmsNormGradArgs& a, qg_dtype type, bool weight_f32, hipStream_t s,
