@@ -52,8 +52,8 @@ MxPlan plan_mx(int64_t M, int64_t N, int64_t K) {
     else p.kind = t256 >= 192 ? MX_256x256 : t128 >= 256 ? MX_128x128 : MX_64x128;
     p.tiles = p.kind == MX_256x256 ? t256 : p.kind == MX_128x128 ? t128 : tiles(64, 128);
     if (p.kind == MX_256x256 || p.tiles > qg::SKINNY_MAX_TICKETS) return p;
-    // two workgroups per CU, ranges of at least 1024 values
-    int64_t s = std::min<int64_t>({512 / p.tiles, K / 1024, 8});
+    // one workgroup per CU, ranges of at least 1024 values
+    int64_t s = std::min<int64_t>({256 / p.tiles, K / 1024, 8});
     s = env_int("QGEMM_MX_SPLITS", (int)s);
     if (s < 2) return p;
     const int64_t units = (K + 255) / 256, per = (units + s - 1) / s;

@@ -119,18 +119,24 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(Mx
     constexpr int A_BYTES = BM * AW, W_BYTES = BN * WW;
     constexpr int STAGE = A_BYTES + W_BYTES;
     constexpr int A_ROUNDS = A_BYTES / (NT * 16), W_ROUNDS = W_BYTES / (NT * 16), LOADS = A_ROUNDS + W_ROUNDS;
-    // Scales: groups of 16 bytes a row, Q stages' worth, in two places of their
-    // own; a stage loads one Qth of the group after its own.
+    // Scales: groups of 16 bytes a row, Q stages' worth, in places of their own.
+    // With the loads of a chunk goes one Qth of a group: with those that start in
+    // stage kt's last step the part of the group after that of stage kt + 1 + D.
+    // D is what the wait at a stage's end leaves time for, so the last part of a
+    // group has landed when its first stage begins.
     constexpr int Q = 16 / NB;
     constexpr int S_ROUNDS = ((BM + BN) * 4 + NT * Q - 1) / (NT * Q);   // per stage; rows past BM + BN are unused
+    constexpr int D = STAGES > 3 ? STAGES - 3 : 0, PLACES = (D + Q - 1) / Q + 2;
     constexpr int GROUP = S_ROUNDS * Q * NT * 4, SCALES = STAGES * STAGE;
+    // loads newer than the next chunk's and than the last part of its scale group
+    constexpr int AFTER = STAGES == 2 ? 0 : LOADS + D * (LOADS + S_ROUNDS);
     constexpr int OB = sizeof(T), AV = A8 ? 2 : 1;
     static_assert(WN % 64 == 0, "output staging");
     static_assert(A_BYTES % (NT * 16) == 0 && W_BYTES % (NT * 16) == 0, "whole load rounds");
     static_assert(BM % 16 == 0, "a wave's scale words are of one operand");
-    static_assert(LOADS * (STAGES - 1) < 64, "vmcnt range");
+    static_assert((LOADS + S_ROUNDS) * (STAGES - 1) < 64, "vmcnt range");
     static_assert(STAGES * STAGE >= NW * 32 * 64 * OB, "output staging fits the stage ring");
-    __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * STAGE + 2 * GROUP];
+    __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * STAGE + PLACES * GROUP];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wm = wave / WAVES_N, wn = wave % WAVES_N;
@@ -182,9 +188,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(Mx
             }
         }
     };
-    // Rounds q0 .. of the 4-byte words of scale group j, four lanes to a row.
-    auto issue_scales = [&](int j, int q0) {
-        const uint32_t base = lds0 + SCALES + (uint32_t)(j & 1) * GROUP + wave * 256;
+    // Part t % Q of scale group t / Q + ahead, in 4-byte words, four lanes to a row.
+    auto issue_scales = [&](int t, int ahead) {
+        const int j = t / Q + ahead, q0 = t % Q * S_ROUNDS;
+        const uint32_t base = lds0 + SCALES + (uint32_t)(j % PLACES) * GROUP + wave * 256;
         const uint32_t blk = (uint32_t)(j * 16 + tid % 4 * 4);
 #pragma unroll
         for (int i = 0; i < S_ROUNDS; ++i) {
@@ -248,7 +255,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(Mx
     u32x4 af[2][FM][AV], wf[2][FN];
     uint32_t as[FM], ws[FN], as_read[FM], ws_read[FN];
     auto read_scales = [&](int kt) {
-        const uint8_t* S = smem + scalar((uint32_t)(kt / Q & 1) * GROUP + (uint32_t)(kt % Q) * NB);
+        const uint8_t* S = smem + scalar((uint32_t)(kt / Q % PLACES) * GROUP + (uint32_t)(kt % Q) * NB);
 #pragma unroll
         for (int b = 0; b < FN; ++b) ws_read[b] = read_scale(S + ws_at + b * 512);
 #pragma unroll
@@ -285,7 +292,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(Mx
             read_a(S, a, ns, nxt);
             if (last && a == 0) {
                 read_scales(kt + 1);
-                issue_scales((kt + 1) / Q + 1, (kt + 1) % Q * S_ROUNDS);
+                issue_scales(kt + 1 + D, 1);
             }
             if (last) issue(kt + STAGES, stage, a);
             if (s == 0) issue(kt + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1, FM + a);
@@ -300,16 +307,15 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(Mx
     static_assert(NS % 2 == 0, "a stage ends on the buffers it began with");
 
 #pragma unroll
-    for (int q = 0; q < Q; ++q) issue_scales(0, q * S_ROUNDS);
+    for (int t = 0; t < Q; ++t) issue_scales(t, 0);
 #pragma unroll
-    for (int part = 0; part < PARTS; ++part) issue(0, 0, part);
-    issue_scales(1, 0);
-#pragma unroll
-    for (int c = 1; c < STAGES; ++c)
+    for (int c = 0; c < STAGES; ++c) {
+        if (c >= STAGES - 1 - D) issue_scales(c - (STAGES - 1 - D), 1);
 #pragma unroll
         for (int part = 0; part < (c < STAGES - 1 ? PARTS : FM); ++part) issue(c, c, part);
+    }
     // chunk 0 and its scales have landed once at most the loads after them are outstanding
-    wait_vmcnt<S_ROUNDS + LOADS * (STAGES - 2) + FM * LOADS / PARTS>();
+    wait_vmcnt<S_ROUNDS * (D + 1) + LOADS * (STAGES - 2) + FM * LOADS / PARTS>();
     __syncthreads();
     read_w(smem, 0, 0);
 #pragma unroll
@@ -319,9 +325,9 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(Mx
     for (int kt = 0; kt < nk; ++kt) {
 #pragma unroll
         for (int s = 0; s < NS - 1; ++s) step(kt, stage, s);
-        // the next chunk is there, with the scale words issued ahead of the loads
-        // that may be outstanding, and every wave has read this chunk's last fragments
-        wait_vmcnt<LOADS * (STAGES - 2)>();
+        // the next chunk and its scales are there, and every wave has read this
+        // chunk's last fragments
+        wait_vmcnt<AFTER>();
         __syncthreads();
         step(kt, stage, NS - 1);
         stage = stage + 1 == STAGES ? 0 : stage + 1;
@@ -439,6 +445,12 @@ hipError_t launch_out(const MxMatmulArgs& a, hipStream_t s) {
     else
         hipLaunchKernelGGL((mx_tiled_kernel<BM, BN, WM, WN, NB, STAGES, A8, _Float16, SK>), grid, block, 0, s, a);
     return hipGetLastError();
+}
+
+// At most one workgroup a CU: the whole of its LDS may go to a deep ring.
+template <int BM, int BN>
+bool one_round(const MxMatmulArgs& a) {
+    return (int64_t)((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN) * a.splits <= 256;
 }
 
 }  // namespace mx
