@@ -139,12 +139,6 @@ qg_status mx_dequantize(int64_t M, int64_t n,
  *   [N,K/32], strides in bytes.  K: a multiple of 32, K >= 32.
  *   act_scale: fp32 [M], or NULL for 1.
  *   out: QG_FP32, QG_BF16 or QG_FP16, [M,N], rounded once.
- *   workspace: NULL, or mx_matmul_workspace_bytes(M, N, K) bytes, 256-byte
- *     aligned, zero-filled before its first use; outputs of few tiles then
- *     divide K among workgroups.  Its first bytes are tickets that every call
- *     leaves at zero, so calls on one stream may share it, whatever their
- *     shapes; calls that overlap in time must not.  (It may be the workspace
- *     of the calls of qgemm.h, whose tickets lie in the same place.)
  * Operands with 16-byte aligned rows, scale rows at multiples of 4 bytes and
  * readable to the end of the 4-byte word that holds their last byte take the
  * fast kernels (few rows: one that streams W once); `scale_rows_padded` says
@@ -155,11 +149,10 @@ qg_status mx_dequantize(int64_t M, int64_t n,
  * 2^-14 below the largest of them cut off, an error of about 1e-5 of the
  * result's size on usual data, far below a 16-bit output's rounding; for an
  * fp32 output the activations are split in two by magnitude so that nothing
- * is cut off.  Sums over split K are added in a fixed order: results repeat
- * bit for bit.  An element whose block scale is 255 gives NaN.
+ * is cut off.  Sums are added in a fixed order: results repeat bit for bit.
+ * An element whose block scale is 255 gives NaN.
  * QG_ERR_UNSUPPORTED if 512 rows of an operand span 2^31 bytes.
  */
-size_t mx_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K);
 qg_status mx_matmul(int64_t M, int64_t N, int64_t K,
                     const void* A, qg_dtype a_format, int64_t lda,
                     const uint8_t* a_scale, int64_t ld_a_scale,
@@ -168,7 +161,6 @@ qg_status mx_matmul(int64_t M, int64_t N, int64_t K,
                     int scale_rows_padded,
                     const float* act_scale,
                     void* out, qg_dtype out_type, int64_t ldo,
-                    void* workspace, size_t workspace_bytes,
                     void* stream);
 
 #ifdef __cplusplus

@@ -69,7 +69,6 @@ from ._binding import (  # noqa: F401
 from ._mx import (  # noqa: F401
     mx_dequantize,
     mx_matmul,
-    mx_matmul_workspace_bytes,
     mx_quantize,
     rms_norm,
     rms_norm_grad,

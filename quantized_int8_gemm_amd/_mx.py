@@ -22,9 +22,7 @@ PROTOTYPES = {
     "rms_norm_grad": ([_i64, _i64, _p, _int, _i64, _p, _i64, _p, _int, _p, _p, _i64, _p, _i64, _p, _p, _sz, _p], _int),
     "mx_quantize": ([_i64, _i64, _p, _int, _i64, _p, _int, _i64, _p, _i64, _p], _int),
     "mx_dequantize": ([_i64, _i64, _p, _int, _i64, _p, _i64, _p, _int, _i64, _p], _int),
-    "mx_matmul_workspace_bytes": ([_i64, _i64, _i64], _sz),
-    "mx_matmul": ([_i64, _i64, _i64, _p, _int, _i64, _p, _i64, _p, _i64, _p, _i64, _int, _p, _p, _int, _i64, _p, _sz,
-                   _p], _int),
+    "mx_matmul": ([_i64, _i64, _i64, _p, _int, _i64, _p, _i64, _p, _i64, _p, _i64, _int, _p, _p, _int, _i64, _p], _int),
 }
 for _name, (_args, _res) in PROTOTYPES.items():
     _fn = getattr(lib, _name)
@@ -322,34 +320,6 @@ def mx_dequantize(codes, scale, out_dtype=torch.bfloat16, columns=None, out=None
     return out
 
 
-_workspaces = {}
-_outgrown = []   # a captured graph may still use these
-
-
-def _workspace(dev, nbytes):
-    """A zero-filled workspace per (device, stream); the library leaves its
-    tickets at zero.  While a graph is captured nothing new is kept: the fill
-    would run with the graph's replays only."""
-    if nbytes == 0:
-        return None
-    key = (dev, _raw_stream(dev.index))
-    ws = _workspaces.get(key)
-    if ws is not None and ws.numel() >= nbytes:
-        return ws
-    if torch.cuda.is_current_stream_capturing():
-        return torch.zeros(nbytes, dtype=torch.uint8, device=dev)
-    if ws is not None:
-        _outgrown.append(ws)
-        nbytes = max(nbytes, 2 * ws.numel())
-    _workspaces[key] = torch.zeros(nbytes, dtype=torch.uint8, device=dev)
-    return _workspaces[key]
-
-
-def mx_matmul_workspace_bytes(M, N, K):
-    """Bytes of workspace with which mx_matmul divides K among workgroups."""
-    return int(lib.mx_matmul_workspace_bytes(M, N, K))
-
-
 def _rows_readable(scale, rows, lds):
     """Whether every scale row can be read to the end of its last 4-byte word."""
     blocks = scale.shape[-1]
@@ -359,7 +329,7 @@ def _rows_readable(scale, rows, lds):
     return scale.untyped_storage().nbytes() - last >= (blocks + 3) // 4 * 4
 
 
-def mx_matmul(A, a_scale, W, w_scale, act_scale=None, out_dtype=torch.float32, out=None, workspace=None):
+def mx_matmul(A, a_scale, W, w_scale, act_scale=None, out_dtype=torch.float32, out=None):
     """out[m, n] = act_scale[m] * sum_k A[m, k] * W[n, k] over MX operands.
 
     A: float8_e4m3fn [M, K] or packed e2m1 uint8 [M, K/2] with a_scale uint8
@@ -368,9 +338,7 @@ def mx_matmul(A, a_scale, W, w_scale, act_scale=None, out_dtype=torch.float32, o
     None for 1.  out_dtype: torch.float32, bfloat16 or float16.  Fast kernels
     need code rows at multiples of 16 bytes and scale rows at multiples of 4,
     as mx_quantize and rms_norm_quantize lay them out; other layouts run a
-    slower one.  workspace: None (a cached, zeroed buffer per device and
-    stream) or a zero-filled uint8 tensor of at least
-    mx_matmul_workspace_bytes(M, N, K) bytes."""
+    slower one."""
     for t, name in ((A, "A"), (W, "W")):
         if not isinstance(t, torch.Tensor):
             raise TypeError(f"{name} must be a torch.Tensor")
@@ -402,13 +370,7 @@ def mx_matmul(A, a_scale, W, w_scale, act_scale=None, out_dtype=torch.float32, o
         _device(A, out)
     if M == 0 or N == 0:
         return out
-    if workspace is None:
-        workspace = _workspace(dev, lib.mx_matmul_workspace_bytes(M, N, K))
-    else:
-        _need(workspace, (torch.uint8, torch.int8), "workspace")
-        _device(A, workspace)
     padded = _rows_readable(a_scale, M, ldas) and _rows_readable(w_scale, N, ldws)
     _launch(dev, lib.mx_matmul, M, N, K, A.data_ptr(), kind, lda, a_scale.data_ptr(), ldas, W.data_ptr(), ldw,
-            w_scale.data_ptr(), ldws, padded, _at(act_scale), out.data_ptr(), dtype, ldo, _at(workspace),
-            0 if workspace is None else workspace.numel())
+            w_scale.data_ptr(), ldws, padded, _at(act_scale), out.data_ptr(), dtype, ldo)
     return out

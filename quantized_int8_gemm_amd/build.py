@@ -45,6 +45,7 @@ SOURCES = [
     "mx_tiled_256x256.hip",
     "mx_tiled_128x128.hip",
     "mx_tiled_64x128.hip",
+    "mx_tiled_small.hip",
     "mx_decode.hip",
     "mx_api.cpp",
     "api.cpp",

@@ -7,7 +7,6 @@
 
 #include <hip/hip_runtime.h>
 
-#include "kernels.h"
 #include "mx_kernels.h"
 
 namespace {
@@ -38,33 +37,20 @@ int env_int(const char* name, int dflt) {
     return v != nullptr && *v ? std::atoi(v) : dflt;
 }
 
-// Kernel of an MX product and its split of K.
-enum MxKind { MX_256x256, MX_128x128, MX_64x128, MX_DECODE };
-struct MxPlan { int kind; int64_t tiles; int splits; int split_k; };
+// Kernels of the MX product.
+enum MxKind { MX_256x256, MX_128x128, MX_64x128, MX_64x64, MX_64x32, MX_32x32, MX_DECODE };
 
-MxPlan plan_mx(int64_t M, int64_t N, int64_t K) {
-    MxPlan p{MX_DECODE, 0, 1, (int)K};
-    auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-    const int64_t t256 = tiles(256, 256), t128 = tiles(128, 128);
+MxKind mx_kind(int64_t M, int64_t N) {
     const int forced = env_int("QGEMM_MX_TILE", -1);
-    if (forced >= 0 && forced <= MX_64x128) p.kind = forced;
-    else if (M <= 16) return p;
-    else p.kind = t256 >= 192 ? MX_256x256 : t128 >= 256 ? MX_128x128 : MX_64x128;
-    p.tiles = p.kind == MX_256x256 ? t256 : p.kind == MX_128x128 ? t128 : tiles(64, 128);
-    if (p.kind == MX_256x256 || p.tiles > qg::SKINNY_MAX_TICKETS) return p;
-    // one workgroup per CU, ranges of at least 1024 values
-    int64_t s = std::min<int64_t>({256 / p.tiles, K / 1024, 8});
-    s = env_int("QGEMM_MX_SPLITS", (int)s);
-    if (s < 2) return p;
-    const int64_t units = (K + 255) / 256, per = (units + s - 1) / s;
-    p.split_k = (int)per * 256;
-    p.splits = (int)((units + per - 1) / per);
-    return p;
-}
-
-size_t plan_bytes(const MxPlan& p) {
-    if (p.splits < 2) return 0;
-    return qg::SKINNY_TICKET_BYTES + (size_t)p.tiles * p.splits * (p.kind == MX_128x128 ? 128 * 128 : 64 * 128) * 4;
+    if (forced >= 0 && forced <= MX_DECODE && (forced != MX_DECODE || M <= qg::MX_DECODE_MAX_M)) return (MxKind)forced;
+    auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
+    if (M <= 8 && tiles(32, 32) <= 112) return MX_DECODE;
+    // the smallest tile of which every CU gets at most one
+    if (tiles(32, 32) <= qg::MX_ROUND) return MX_32x32;
+    if (tiles(64, 32) <= qg::MX_ROUND) return MX_64x32;
+    if (tiles(64, 64) <= qg::MX_ROUND) return MX_64x64;
+    if (tiles(64, 128) <= qg::MX_ROUND) return MX_64x128;
+    return tiles(256, 256) >= 160 ? MX_256x256 : MX_128x128;
 }
 
 qg_status nothing() {
@@ -166,15 +152,10 @@ qg_status mx_dequantize(int64_t M, int64_t n, const void* codes, qg_dtype format
     return done(qg::launch_mx_dequantize(a, out_type, format, (hipStream_t)stream, &name), name);
 }
 
-size_t mx_matmul_workspace_bytes(int64_t M, int64_t N, int64_t K) {
-    if (M < 1 || N < 1 || K < 32 || M >= LIM || N >= LIM || K >= LIM || K % 32 != 0) return 0;
-    return plan_bytes(plan_mx(M, N, K));
-}
-
 qg_status mx_matmul(int64_t M, int64_t N, int64_t K, const void* A, qg_dtype a_format, int64_t lda,
                     const uint8_t* a_scale, int64_t ld_a_scale, const void* W, int64_t ldw, const uint8_t* w_scale,
                     int64_t ld_w_scale, int scale_rows_padded, const float* act_scale, void* out, qg_dtype out_type,
-                    int64_t ldo, void* workspace, size_t workspace_bytes, void* stream) {
+                    int64_t ldo, void* stream) {
     if (M < 0 || N < 0 || K < 0 || M >= LIM || N >= LIM || K >= LIM) return QG_ERR_INVALID_ARGUMENT;
     if (!is_mx(a_format) || !is_float(out_type)) return QG_ERR_INVALID_ARGUMENT;
     if (M == 0 || N == 0) return nothing();
@@ -184,8 +165,6 @@ qg_status mx_matmul(int64_t M, int64_t N, int64_t K, const void* A, qg_dtype a_f
     if (lda < code_bytes(a_format, K) || ldw < K / 2 || ld_a_scale < K / 32 || ld_w_scale < K / 32 || ldo < N ||
         !aligned_for(out, out_type) || !aligned(act_scale, 4))
         return QG_ERR_INVALID_ARGUMENT;
-    if (workspace != nullptr && !aligned(workspace, 256)) return QG_ERR_INVALID_ARGUMENT;
-    if (workspace != nullptr && workspace_bytes < mx_matmul_workspace_bytes(M, N, K)) return QG_ERR_WORKSPACE;
     if (lda * 512 >= (int64_t)1 << 31 || ldw * 512 >= (int64_t)1 << 31 || ld_a_scale * 512 >= (int64_t)1 << 31 ||
         ld_w_scale * 512 >= (int64_t)1 << 31)
         return QG_ERR_UNSUPPORTED;
@@ -199,21 +178,18 @@ qg_status mx_matmul(int64_t M, int64_t N, int64_t K, const void* A, qg_dtype a_f
     a.A = (const uint8_t*)A; a.lda = lda; a.as = a_scale; a.ldas = ld_a_scale;
     a.W = (const uint8_t*)W; a.ldw = ldw; a.ws = w_scale; a.ldws = ld_w_scale;
     a.act_scale = act_scale; a.out = out; a.ldo = ldo; a.out_type = out_type;
-    a.workspace = workspace;
-    a.splits = 1;
     const bool a8 = a_format == QG_MXFP8;
     const hipStream_t st = (hipStream_t)stream;
     const char* name = "";
     if (!fast) return done(qg::launch_mx_bytes(a, a8, st, &name), name);
-    MxPlan p = plan_mx(M, N, K);
-    if (p.kind == MX_DECODE) return done(qg::launch_mx_decode(a, a8, st, &name), name);
-    if (workspace == nullptr) p.splits = 1;
-    a.splits = p.splits;
-    a.split_k = p.split_k;
-    switch (p.kind) {
+    switch (mx_kind(M, N)) {
         case MX_256x256: return done(qg::launch_mx_256x256(a, a8, st), "mx_tiled_256x256");
-        case MX_128x128: return done(qg::launch_mx_128x128(a, a8, st), p.splits > 1 ? "mx_tiled_128x128_splitk" : "mx_tiled_128x128");
-        default: return done(qg::launch_mx_64x128(a, a8, st), p.splits > 1 ? "mx_tiled_64x128_splitk" : "mx_tiled_64x128");
+        case MX_128x128: return done(qg::launch_mx_128x128(a, a8, st), "mx_tiled_128x128");
+        case MX_64x128: return done(qg::launch_mx_64x128(a, a8, st), "mx_tiled_64x128");
+        case MX_64x64: return done(qg::launch_mx_64x64(a, a8, st), "mx_tiled_64x64");
+        case MX_64x32: return done(qg::launch_mx_64x32(a, a8, st), "mx_tiled_64x32");
+        case MX_32x32: return done(qg::launch_mx_32x32(a, a8, st), "mx_tiled_32x32");
+        default: return done(qg::launch_mx_decode(a, a8, st), "mx_decode");
     }
 }
 

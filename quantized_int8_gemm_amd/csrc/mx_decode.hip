@@ -1,29 +1,30 @@
-// MX product for few rows (decoding): W is streamed once.
+// MX product for very few rows and columns too few to give every CU a tile of the
+// tiled kernels: W is streamed once.
 //
 // A workgroup of eight waves owns 16 output columns over all of K.  The waves
 // take chunks of 512 values of K in turn, straight from memory to registers:
 // per 128 values one 16-byte load of W and one (e2m1) or two (e4m3) of A per
-// lane, and one 16x16x128 matrix instruction for each block of 16 rows; two
-// chunks' loads are in flight at once.  Scale bytes come four words at a time,
-// and a lane shifts the byte of its block into place.  The waves' partial
-// tiles are added through LDS in a fixed order.  Bound by reading W; A stays
-// in the caches (rows past M read nothing).
+// lane, and one 16x16x128 matrix instruction; two chunks' loads are in flight at
+// once.  Scale bytes come four words at a time, and a lane shifts the byte of its
+// block into place.  The waves' partial tiles are added through LDS in a fixed
+// order.  Bound by latency: 1 x 2048 x 8192 7.1 us, where 32 x 32 tiles take 8.5 (64
+// workgroups instead of 128).  Its loads of A, which fill 16 rows whatever there are,
+// let the tiles win from 4096 columns on, or with more than eight rows.
 #include "mx_mfma.h"
-#include "kernels.h"
 
 namespace qg {
 namespace {
 
-constexpr int NW = 8;
+constexpr int NW = 8, UNROLL = 2;
 constexpr uint32_t OUTSIDE = 0xffffff00u;   // past every window
 
-// MB blocks of 16 rows.  S16: scale rows are whole 16-byte groups (K a
-// multiple of 512), so four steps' scale words come in one load.
-template <int MB, int UNROLL, bool A8, bool S16, typename T>
+// S16: scale rows are whole 16-byte groups (K a multiple of 512), so four steps'
+// scale words come in one load.
+template <bool A8, bool S16, typename T>
 __global__ __launch_bounds__(NW * 64) void mx_decode_kernel(MxMatmulArgs p) {
     constexpr bool EXACT = A8 && sizeof(T) == 4;
     constexpr int AV = A8 ? 2 : 1, ABLK = A8 ? 32 : 16;
-    __shared__ float part[NW][MB][4][64];
+    __shared__ float part[NW][4][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
     const int r = lane & 15, g = lane >> 4;
     const int n0 = blockIdx.x * 16;
@@ -48,13 +49,11 @@ __global__ __launch_bounds__(NW * 64) void mx_decode_kernel(MxMatmulArgs p) {
         }
     };
 
-    v4f acc[MB];
-#pragma unroll
-    for (int i = 0; i < MB; ++i) acc[i] = v4f{0.f, 0.f, 0.f, 0.f};
+    v4f acc = {0.f, 0.f, 0.f, 0.f};
     const int chunks = (nblk + 15) / 16;
     for (int c0 = wave; c0 < chunks; c0 += NW * UNROLL) {
-        u32x4 w[UNROLL][4], a[UNROLL][4][MB][AV];
-        uint32_t ws[UNROLL][4], as[UNROLL][MB][4];
+        u32x4 w[UNROLL][4], a[UNROLL][4][AV];
+        uint32_t ws[UNROLL][4], as[UNROLL][4];
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
             const int chunk = c0 + u * NW;
@@ -68,20 +67,17 @@ __global__ __launch_bounds__(NW * 64) void mx_decode_kernel(MxMatmulArgs p) {
 #pragma unroll
         for (int u = 0; u < UNROLL; ++u) {
             const int chunk = c0 + u * NW;
+            scales(as_rsrc, (uint32_t)(r * ldas), chunk, chunk < chunks, as[u]);
 #pragma unroll
-            for (int i = 0; i < MB; ++i) {
-                scales(as_rsrc, (uint32_t)((16 * i + r) * ldas), chunk, chunk < chunks, as[u][i]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int b0 = chunk * 16 + 4 * q;
-                    const uint32_t row = (uint32_t)((16 * i + r) * lda);
-                    if constexpr (A8) {
-                        // k = 16 g .. + 15 of the step's first two blocks, then of its last two
-                        a[u][q][i][0] = buffer_load16(a_rsrc, b0 + g / 2 < nblk ? row + (uint32_t)(b0 * 32 + 16 * g) : OUTSIDE, 0);
-                        a[u][q][i][1] = buffer_load16(a_rsrc, b0 + 2 + g / 2 < nblk ? row + (uint32_t)(b0 * 32 + 64 + 16 * g) : OUTSIDE, 0);
-                    } else {
-                        a[u][q][i][0] = buffer_load16(a_rsrc, b0 + g < nblk ? row + (uint32_t)((b0 + g) * 16) : OUTSIDE, 0);
-                    }
+            for (int q = 0; q < 4; ++q) {
+                const int b0 = chunk * 16 + 4 * q;
+                const uint32_t row = (uint32_t)(r * lda);
+                if constexpr (A8) {
+                    // k = 16 g .. + 15 of the step's first two blocks, then of its last two
+                    a[u][q][0] = buffer_load16(a_rsrc, b0 + g / 2 < nblk ? row + (uint32_t)(b0 * 32 + 16 * g) : OUTSIDE, 0);
+                    a[u][q][1] = buffer_load16(a_rsrc, b0 + 2 + g / 2 < nblk ? row + (uint32_t)(b0 * 32 + 64 + 16 * g) : OUTSIDE, 0);
+                } else {
+                    a[u][q][0] = buffer_load16(a_rsrc, b0 + g < nblk ? row + (uint32_t)((b0 + g) * 16) : OUTSIDE, 0);
                 }
             }
         }
@@ -92,42 +88,31 @@ __global__ __launch_bounds__(NW * 64) void mx_decode_kernel(MxMatmulArgs p) {
             for (int q = 0; q < 4; ++q) {
                 // scale bytes past K may be anything: 0 times the zero codes there
                 const bool live = S16 || chunk * 16 + 4 * q + g < nblk;
-                const uint32_t sw = live ? ws[u][q] >> (8 * g) : 0u;
-                const v8i wv = words4(w[u][q]);
-#pragma unroll
-                for (int i = 0; i < MB; ++i) {
-                    const uint32_t sa = live ? as[u][i][q] >> (8 * g) : 0u;
-                    v8i av;
-                    if constexpr (A8) av = words8(a[u][q][i][0], a[u][q][i][1]);
-                    else av = words4(a[u][q][i][0]);
-                    acc[i] = mfma_mx16<A8, EXACT>(wv, sw, av, sa, acc[i]);
-                }
+                const uint32_t sw = live ? ws[u][q] >> (8 * g) : 0u, sa = live ? as[u][q] >> (8 * g) : 0u;
+                acc = mfma_mx16<A8, EXACT>(words4(w[u][q]), sw, A8 ? words8(a[u][q][0], a[u][q][AV - 1]) : words4(a[u][q][0]), sa, acc);
             }
         }
     }
 #pragma unroll
-    for (int i = 0; i < MB; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) part[wave][i][e][lane] = acc[i][e];
+    for (int e = 0; e < 4; ++e) part[wave][e][lane] = acc[e];
     __syncthreads();
-    // 64 MB columns-by-four of results: one thread per element
-    for (int t = tid; t < MB * 256; t += NW * 64) {
-        const int i = t >> 8, e = (t >> 6) & 3, l = t & 63;
+    if (tid < 256) {   // one thread per element
+        const int e = tid >> 6, l = tid & 63;
         float s = 0.f;
 #pragma unroll
-        for (int k = 0; k < NW; ++k) s += part[k][i][e][l];
-        const int m = 16 * i + (l & 15), n = n0 + 4 * (l >> 4) + e;
+        for (int k = 0; k < NW; ++k) s += part[k][e][l];
+        const int m = l & 15, n = n0 + 4 * (l >> 4) + e;
         if (m < p.M && n < p.N) put<T>(p.out, (int64_t)m * p.ldo + n, p.act_scale != nullptr ? s * p.act_scale[m] : s);
     }
 }
 
-template <int MB, int UNROLL, bool A8>
+template <bool A8>
 hipError_t by_out(const MxMatmulArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)((a.N + 15) / 16)), block(NW * 64);
-#define QG_DECODE(T)                                                                                              \
-    do {                                                                                                          \
-        if (a.K % 512 == 0) hipLaunchKernelGGL((mx_decode_kernel<MB, UNROLL, A8, true, T>), grid, block, 0, s, a);  \
-        else hipLaunchKernelGGL((mx_decode_kernel<MB, UNROLL, A8, false, T>), grid, block, 0, s, a);               \
+#define QG_DECODE(T)                                                                                       \
+    do {                                                                                                   \
+        if (a.K % 512 == 0) hipLaunchKernelGGL((mx_decode_kernel<A8, true, T>), grid, block, 0, s, a);     \
+        else hipLaunchKernelGGL((mx_decode_kernel<A8, false, T>), grid, block, 0, s, a);                   \
     } while (0)
     if (a.out_type == QG_FP32) QG_DECODE(float);
     else if (a.out_type == QG_BF16) QG_DECODE(__bf16);
@@ -136,18 +121,10 @@ hipError_t by_out(const MxMatmulArgs& a, hipStream_t s) {
     return hipGetLastError();
 }
 
-template <bool A8>
-hipError_t by_rows(const MxMatmulArgs& a, hipStream_t s) {
-    if (a.M <= 16) return by_out<1, 2, A8>(a, s);
-    if (a.M <= 32) return by_out<2, 1, A8>(a, s);
-    return by_out<4, 1, A8>(a, s);
-}
-
 }  // namespace
 
-hipError_t launch_mx_decode(const MxMatmulArgs& a, bool a8, hipStream_t s, const char** name) {
-    *name = "mx_decode";
-    return a8 ? by_rows<true>(a, s) : by_rows<false>(a, s);
+hipError_t launch_mx_decode(const MxMatmulArgs& a, bool a8, hipStream_t s) {
+    return a8 ? by_out<true>(a, s) : by_out<false>(a, s);
 }
 
 }  // namespace qg

@@ -51,23 +51,24 @@ struct MxMatmulArgs {
     const uint8_t* ws; int64_t ldws;
     const float* act_scale;                  // NULL: 1
     void* out; int64_t ldo; int out_type;    // qg_dtype
-    void* workspace; int splits; int split_k;  // splits > 1: K in ranges of split_k
 };
-// Reads bytes: any strides, any alignment, no workspace.
+// Reads bytes: any strides, any alignment.
 hipError_t launch_mx_bytes(const MxMatmulArgs& a, bool a8, hipStream_t s, const char** name);
 
 // Tiled kernels: code rows 16-byte aligned, scale rows 4-byte aligned and
-// readable to the end of their last word; K split when a.splits > 1 (split_k a
-// multiple of 256, tickets for at most SKINNY_MAX_TICKETS tiles; not the
-// 256x256 tiles).
+// readable to the end of their last word.
+constexpr int MX_ROUND = 256;   // compute units: workgroups that run at once if each fills one
 hipError_t launch_mx_256x256(const MxMatmulArgs& a, bool a8, hipStream_t s);
 hipError_t launch_mx_128x128(const MxMatmulArgs& a, bool a8, hipStream_t s);
 hipError_t launch_mx_64x128(const MxMatmulArgs& a, bool a8, hipStream_t s);
+hipError_t launch_mx_64x64(const MxMatmulArgs& a, bool a8, hipStream_t s);
+hipError_t launch_mx_64x32(const MxMatmulArgs& a, bool a8, hipStream_t s);
+hipError_t launch_mx_32x32(const MxMatmulArgs& a, bool a8, hipStream_t s);
 
-// Few rows: W streamed once, 16 columns per workgroup, no workspace; operands
-// laid out as for the tiled kernels.
-constexpr int MX_DECODE_MAX_M = 64;
-hipError_t launch_mx_decode(const MxMatmulArgs& a, bool a8, hipStream_t s, const char** name);
+// At most 16 rows: W streamed once, 16 columns per workgroup; operands laid out as
+// for the tiled kernels.
+constexpr int MX_DECODE_MAX_M = 16;
+hipError_t launch_mx_decode(const MxMatmulArgs& a, bool a8, hipStream_t s);
 
 // Names the kernel for qgemm_last_kernel().
 void record_kernel(const char* name);

@@ -5,7 +5,7 @@
 
 namespace qg {
 hipError_t launch_mx_256x256(const MxMatmulArgs& a, bool a8, hipStream_t s) {
-    return a8 ? mx::launch_out<256, 256, 128, 64, 4, 3, true, false>(a, s)
-              : mx::launch_out<256, 256, 128, 64, 8, 2, false, false>(a, s);
+    return a8 ? mx::launch_out<256, 256, 128, 64, 1, 4, 3, true>(a, s)
+              : mx::launch_out<256, 256, 128, 64, 1, 8, 2, false>(a, s);
 }
 }  // namespace qg

@@ -31,14 +31,13 @@
 // products 172: the loads' path (64 B a cycle and CU) is busy half of the time and
 // what is left is that these streams do not overlap fully.  Four waves of 128 x
 // 128 (a third fewer fragment reads, one wave per SIMD) measured 284 us.
+//  * KW waves share a wave tile, each with its part of every stage's steps; their
+//    sums are added through LDS, in order, so results repeat bit for bit.  Small
+//    tiles need it: with one wave a SIMD every step waits for its fragments.
 //  * The finished wave tile goes through LDS, 32 rows at a time, and leaves in
 //    whole rows of 64 columns.
-// SK: blockIdx.y divides K into ranges of split_k values; each range leaves its
-// fp32 tile in the workspace and the one that takes the tile's last ticket adds
-// them all in order (so results repeat bit for bit) and writes the output.
 #pragma once
 #include "mx_mfma.h"
-#include "kernels.h"
 
 namespace qg {
 namespace mx {
@@ -110,11 +109,11 @@ __device__ __forceinline__ uint32_t scalar(uint32_t v) {
     return v;
 }
 
-template <int BM, int BN, int WM, int WN, int NB, int STAGES, bool A8, typename T, bool SK>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(MxMatmulArgs p) {
+template <int BM, int BN, int WM, int WN, int KW, int NB, int STAGES, bool A8, typename T>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * KW * 64) void mx_tiled_kernel(MxMatmulArgs p) {
     constexpr bool EXACT = A8 && sizeof(T) == 4;
-    constexpr int NT = (BM / WM) * (BN / WN) * 64, NW = NT / 64, WAVES_N = BN / WN;
-    constexpr int FM = WM / 32, FN = WN / 32, NS = NB / 2;
+    constexpr int NT = (BM / WM) * (BN / WN) * KW * 64, NW = NT / 64 / KW, WAVES_N = BN / WN;
+    constexpr int FM = WM / 32, FN = WN / 32, NS = NB / 2, SPW = NS / KW;   // steps of a stage, of a wave
     constexpr int AW = NB * (A8 ? 32 : 16), WW = NB * 16;         // bytes of a stage's code rows
     constexpr int A_BYTES = BM * AW, W_BYTES = BN * WW;
     constexpr int STAGE = A_BYTES + W_BYTES;
@@ -131,15 +130,16 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(Mx
     // loads newer than the next chunk's and than the last part of its scale group
     constexpr int AFTER = STAGES == 2 ? 0 : LOADS + D * (LOADS + S_ROUNDS);
     constexpr int OB = sizeof(T), AV = A8 ? 2 : 1;
-    static_assert(WN % 64 == 0, "output staging");
+    static_assert(WN == 32 || WN % 64 == 0, "output staging");
     static_assert(A_BYTES % (NT * 16) == 0 && W_BYTES % (NT * 16) == 0, "whole load rounds");
     static_assert(BM % 16 == 0, "a wave's scale words are of one operand");
     static_assert((LOADS + S_ROUNDS) * (STAGES - 1) < 64, "vmcnt range");
-    static_assert(STAGES * STAGE >= NW * 32 * 64 * OB, "output staging fits the stage ring");
+    constexpr int SW = WN < 64 ? WN : 64;   // columns staged at a time
+    static_assert(STAGES * STAGE >= NW * 32 * SW * OB, "output staging fits the stage ring");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * STAGE + PLACES * GROUP];
 
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wm = wave / WAVES_N, wn = wave % WAVES_N;
+    const int kw = wave / NW, wm = wave % NW / WAVES_N, wn = wave % WAVES_N;
     const int g = lane >> 5, r32 = lane & 31;
 
     const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
@@ -148,40 +148,40 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(Mx
     const int m0 = tm * BM, n0 = tn * BN;
     const int rows_a = p.M - m0 < BM ? p.M - m0 : BM, rows_w = p.N - n0 < BN ? p.N - n0 : BN;
     const int lda = (int)p.lda, ldw = (int)p.ldw, ldas = (int)p.ldas, ldws = (int)p.ldws;
-    // this workgroup's blocks of K: kb0 .. kb0 + nblk
-    const int kb0 = SK ? (int)blockIdx.y * (p.split_k / 32) : 0;
-    const int left = p.K / 32 - kb0;
-    const int nblk = SK && left > p.split_k / 32 ? p.split_k / 32 : left;
+    const int nblk = p.K / 32;
     constexpr int ABLK = A8 ? 32 : 16;
-    const v4i a_rsrc = rsrc_words(p.A + (int64_t)m0 * p.lda + kb0 * ABLK, (uint32_t)((rows_a - 1) * lda + nblk * ABLK));
-    const v4i w_rsrc = rsrc_words(p.W + (int64_t)n0 * p.ldw + kb0 * 16, (uint32_t)((rows_w - 1) * ldw + nblk * 16));
+    const v4i a_rsrc = rsrc_words(p.A + (int64_t)m0 * p.lda, (uint32_t)((rows_a - 1) * lda + nblk * ABLK));
+    const v4i w_rsrc = rsrc_words(p.W + (int64_t)n0 * p.ldw, (uint32_t)((rows_w - 1) * ldw + nblk * 16));
     // scale rows are readable to the end of their last 4-byte word
     const uint32_t s_span = (uint32_t)((nblk + 3) & ~3);
-    const v4i as_rsrc = rsrc_words(p.as + (int64_t)m0 * p.ldas + kb0, (uint32_t)((rows_a - 1) * ldas) + s_span);
-    const v4i ws_rsrc = rsrc_words(p.ws + (int64_t)n0 * p.ldws + kb0, (uint32_t)((rows_w - 1) * ldws) + s_span);
+    const v4i as_rsrc = rsrc_words(p.as + (int64_t)m0 * p.ldas, (uint32_t)((rows_a - 1) * ldas) + s_span);
+    const v4i ws_rsrc = rsrc_words(p.ws + (int64_t)n0 * p.ldws, (uint32_t)((rows_w - 1) * ldws) + s_span);
     const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
     // Global offset (stage 0) and block of this lane's segment in a load round.
     // A round covers a multiple of 16 rows, so all rounds of an operand take the
-    // same segment, a fixed number of rows apart.
+    // same segment, a fixed number of rows apart (or of 8: odd rounds of A take
+    // the segment with bit 3 flipped).
     constexpr int A_ROWS = NT * 16 / AW, W_ROWS = NT * 16 / WW;
-    static_assert(A_ROWS % 16 == 0 && W_ROWS % 16 == 0, "one swizzle for all rounds");
+    static_assert(A_ROWS % 8 == 0 && W_ROWS % 16 == 0, "one swizzle for all rounds, or two in turn");
     const int a_seg = slot<AW>(tid * 16 / AW, tid * 16 % AW / 16), w_seg = slot<WW>(tid * 16 / WW, tid * 16 % WW / 16);
     const uint32_t a_off = (uint32_t)(tid * 16 / AW * lda + 16 * a_seg), w_off = (uint32_t)(tid * 16 / WW * ldw + 16 * w_seg);
+    const uint32_t a_odd = (uint32_t)(tid * 16 / AW * lda + 16 * (a_seg ^ 8));
     const int nk = (nblk + NB - 1) / NB;
 
     // Part `part` of PARTS of the loads of chunk kt.  Blocks past K, whole chunks
     // too, are read from outside the windows: every chunk issues the same loads,
     // so the loop has no branches and its waits are constants.
-    constexpr int PARTS = 2 * FM;
-    auto issue = [&](int kt, int stage, int part) {
+    constexpr int PARTS = SPW > 1 ? 2 * FM : FM;
+    auto issue = [&](int kt, int stage, int part) __attribute__((always_inline)) {
         const uint32_t base = lds0 + (uint32_t)stage * STAGE, codes = base + wave * 1024;
         const uint32_t ka = scalar(kt * AW), kw = scalar(kt * WW);
         const int rest = nblk - kt * NB;   // blocks from this chunk on
 #pragma unroll
         for (int i = part * LOADS / PARTS; i < (part + 1) * LOADS / PARTS; ++i) {
             if (i < A_ROUNDS) {
-                dma16(a_rsrc, 16 * a_seg / ABLK >= rest ? OUTSIDE : a_off + ((uint32_t)(i * A_ROWS * lda) + ka), codes + i * NT * 16);
+                const int flip = i * A_ROWS & 8, seg = a_seg ^ flip;
+                dma16(a_rsrc, 16 * seg / ABLK >= rest ? OUTSIDE : (flip ? a_odd : a_off) + ((uint32_t)(i * A_ROWS * lda) + ka), codes + i * NT * 16);
             } else {
                 const int q = i - A_ROUNDS;
                 dma16(w_rsrc, w_seg >= rest ? OUTSIDE : w_off + ((uint32_t)(q * W_ROWS * ldw) + kw), codes + A_BYTES + q * NT * 16);
@@ -189,7 +189,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(Mx
         }
     };
     // Part t % Q of scale group t / Q + ahead, in 4-byte words, four lanes to a row.
-    auto issue_scales = [&](int t, int ahead) {
+    auto issue_scales = [&](int t, int ahead) __attribute__((always_inline)) {
         const int j = t / Q + ahead, q0 = t % Q * S_ROUNDS;
         const uint32_t base = lds0 + SCALES + (uint32_t)(j % PLACES) * GROUP + wave * 256;
         const uint32_t blk = (uint32_t)(j * 16 + tid % 4 * 4);
@@ -225,29 +225,31 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(Mx
     // Where in a stage this lane's fragment of step s and row block 0 lies, and
     // its scales; e2m1 fragments are held in four registers and widened at the
     // instruction.
-    uint32_t a_at[NS][AV], w_at[NS], as_at = SCALES + (wm * WM + r32) * 16 + g * NS;
-    uint32_t ws_at = SCALES + (BM + wn * WN + r32) * 16 + g * NS;
+    uint32_t a_at[SPW][AV], w_at[SPW], as_at = SCALES + (wm * WM + r32) * 16 + g * NS + kw * SPW;
+    uint32_t ws_at = SCALES + (BM + wn * WN + r32) * 16 + g * NS + kw * SPW;
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
+    for (int s = 0; s < SPW; ++s) {
+        const int q = kw * SPW + s;   // this wave's steps are q of the stage
         const uint32_t row = (wm * WM + r32) * AW;
         if constexpr (A8) {
-            a_at[s][0] = row + 16 * slot<AW>(r32, 2 * s + g);
-            a_at[s][AV - 1] = row + 16 * slot<AW>(r32, 2 * (NS + s) + g);
+            a_at[s][0] = row + 16 * slot<AW>(r32, 2 * q + g);
+            a_at[s][AV - 1] = row + 16 * slot<AW>(r32, 2 * (NS + q) + g);
         } else {
-            a_at[s][0] = row + 16 * slot<AW>(r32, g * NS + s);
+            a_at[s][0] = row + 16 * slot<AW>(r32, g * NS + q);
         }
-        w_at[s] = A_BYTES + (wn * WN + r32) * WW + 16 * slot<WW>(r32, g * NS + s);
+        w_at[s] = A_BYTES + (wn * WN + r32) * WW + 16 * slot<WW>(r32, g * NS + q);
     }
 #pragma unroll
-    for (int s = 0; s < NS; ++s) {
+    for (int s = 0; s < SPW; ++s) {
 #pragma unroll
         for (int v = 0; v < AV; ++v) asm volatile("" : "+v"(a_at[s][v]));
         asm volatile("" : "+v"(w_at[s]));
     }
     asm volatile("" : "+v"(as_at), "+v"(ws_at));
     auto read_scale = [&](const uint8_t* at) -> uint32_t {
-        if constexpr (NS == 4) return *reinterpret_cast<const uint32_t*>(__builtin_assume_aligned(at, 4));
-        else return *reinterpret_cast<const uint16_t*>(__builtin_assume_aligned(at, 2));
+        if constexpr (SPW == 4) return *reinterpret_cast<const uint32_t*>(at);
+        else if constexpr (SPW == 2) return *reinterpret_cast<const uint16_t*>(at);
+        else return *at;
     };
 
     // Fragments of the current step and the next; scales of the chunk, and of
@@ -269,16 +271,16 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(Mx
 #pragma unroll
         for (int v = 0; v < AV; ++v) af[buf][a][v] = read16(S + a_at[s][v] + a * 32 * AW);
     };
-    // Step s of chunk kt in ring place `stage`: the products of the fragments at
-    // hand, while those of the next step (at the stage's end, of the next chunk)
-    // are read.
-    auto step = [&](int kt, int stage, int s) {
-        const bool last = s == NS - 1;
-        const int ns = last ? 0 : s + 1, cur = s & 1, nxt = cur ^ 1, after = stage + 1 == STAGES ? 0 : stage + 1;
+    // Step s of this wave's in chunk kt, which lies in ring place `stage`: the
+    // products of the fragments at hand, in buffers cur, while those of the next
+    // step (at the stage's end, of the next chunk) are read.
+    auto step = [&](int kt, int stage, int s, int cur) __attribute__((always_inline)) {
+        const bool last = s == SPW - 1;
+        const int ns = last ? 0 : s + 1, nxt = cur ^ 1, after = stage + 1 == STAGES ? 0 : stage + 1;
         const uint8_t* S = smem + scalar((uint32_t)(last ? after : stage) * STAGE);
         if (s == 0) {
             // scale bytes past K may be anything: 0 (2^-127) times the zero codes there
-            const int rest = nblk - kt * NB - g * NS;
+            const int rest = nblk - kt * NB - g * NS - kw * SPW;
             const uint32_t mask = rest >= 4 ? ~0u : (rest <= 0 ? 0u : (1u << (8 * rest)) - 1u);
 #pragma unroll
             for (int b = 0; b < FN; ++b) ws[b] = ws_read[b] & mask;
@@ -295,7 +297,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(Mx
                 issue_scales(kt + 1 + D, 1);
             }
             if (last) issue(kt + STAGES, stage, a);
-            if (s == 0) issue(kt + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1, FM + a);
+            if (s == 0 && SPW > 1) issue(kt + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1, FM + a);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int b = 0; b < FN; ++b)
@@ -304,8 +306,6 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(Mx
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    static_assert(NS % 2 == 0, "a stage ends on the buffers it began with");
-
 #pragma unroll
     for (int t = 0; t < Q; ++t) issue_scales(t, 0);
 #pragma unroll
@@ -322,87 +322,74 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(Mx
     for (int a = 0; a < FM; ++a) read_a(smem, a, 0, 0);
     read_scales(0);
     int stage = 0;
-    for (int kt = 0; kt < nk; ++kt) {
+    auto chunk = [&](int kt, int cur) __attribute__((always_inline)) {
 #pragma unroll
-        for (int s = 0; s < NS - 1; ++s) step(kt, stage, s);
+        for (int s = 0; s < SPW - 1; ++s) step(kt, stage, s, (cur + s) & 1);
         // the next chunk and its scales are there, and every wave has read this
         // chunk's last fragments
         wait_vmcnt<AFTER>();
         __syncthreads();
-        step(kt, stage, NS - 1);
+        step(kt, stage, SPW - 1, (cur + SPW - 1) & 1);
         stage = stage + 1 == STAGES ? 0 : stage + 1;
+    };
+    if constexpr (SPW % 2 == 0) {
+        for (int kt = 0; kt < nk; ++kt) chunk(kt, 0);
+    } else {
+        for (int kt = 0; kt < nk; kt += 2) {
+            chunk(kt, 0);
+            if (kt + 1 < nk) chunk(kt + 1, 1);
+        }
     }
     wait_vmcnt<0>();   // loads past K write zeros
     __syncthreads();   // every wave is done with the stage ring
 
-    if constexpr (SK) {
-        const int S = (int)gridDim.y, sk = (int)blockIdx.y;
-        if (S > 1) {
-            constexpr int COHERENT = 16;   // sc1: device scope
-            constexpr int TILE_BYTES = BM * BN * 4;
-            const int tile = tm * tiles_n + tn;   // < SKINNY_MAX_TICKETS (host plan)
-            int* tickets = reinterpret_cast<int*>(p.workspace);
-            char* part = reinterpret_cast<char*>(p.workspace) + SKINNY_TICKET_BYTES + (size_t)tile * S * TILE_BYTES;
-            const __amdgpu_buffer_rsrc_t rs = make_rsrc(part, (uint32_t)(S * TILE_BYTES));
-            auto at = [&](int s2, int a, int b, int q) {
-                return (int)(s2 * TILE_BYTES + (((wave * FM + a) * FN + b) * 4 + q) * 1024 + 16 * lane);
-            };
+    const bool mine = KW == 1 || kw == 0;   // the waves that leave the results
+    if constexpr (KW > 1) {
+        // the other waves' sums over their steps join in order
+        constexpr int WAVE = FM * FN * 4096;
+        static_assert((KW - 1) * NW * WAVE <= STAGES * STAGE + PLACES * GROUP, "sums fit the ring");
+        auto at = [&](int k, int a, int b, int q) {
+            return reinterpret_cast<v4f*>(smem + ((k - 1) * NW + wave % NW) * WAVE + ((a * FN + b) * 4 + q) * 1024 + 16 * lane);
+        };
 #pragma unroll
-            for (int a = 0; a < FM; ++a)
+        for (int a = 0; a < FM; ++a)
 #pragma unroll
-                for (int b = 0; b < FN; ++b)
+            for (int b = 0; b < FN; ++b)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const v4f v = {acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
-                        __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(v4i, v), rs, at(sk, a, b, q), 0, COHERENT);
-                    }
-            __builtin_amdgcn_s_waitcnt(0);
-            __shared__ int ticket;
-            __syncthreads();
-            if (tid == 0) ticket = __hip_atomic_fetch_add(&tickets[tile], 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            __syncthreads();
-            if (ticket != S - 1) return;
-            // every range's tile, the own one too, in order
+                for (int q = 0; q < 4; ++q)
+                    if (!mine) *at(kw, a, b, q) = v4f{acc[a][b][4 * q], acc[a][b][4 * q + 1], acc[a][b][4 * q + 2], acc[a][b][4 * q + 3]};
+        __syncthreads();
+        if (mine) {
 #pragma unroll
-            for (int a = 0; a < FM; ++a)
-#pragma unroll
-                for (int b = 0; b < FN; ++b)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) acc[a][b][i] = 0.f;
-            for (int s2 = 0; s2 < S; ++s2) {
-                v4f v[FM][FN][4];
+            for (int k = 1; k < KW; ++k)
 #pragma unroll
                 for (int a = 0; a < FM; ++a)
 #pragma unroll
                     for (int b = 0; b < FN; ++b)
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)
-                            v[a][b][q] = __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rs, at(s2, a, b, q), 0, COHERENT));
+                        for (int q = 0; q < 4; ++q) {
+                            const v4f v = *at(k, a, b, q);
 #pragma unroll
-                for (int a = 0; a < FM; ++a)
-#pragma unroll
-                    for (int b = 0; b < FN; ++b)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) acc[a][b][i] += v[a][b][i / 4][i % 4];
-            }
-            if (tid == 0) __hip_atomic_store(&tickets[tile], 0, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                            for (int i = 0; i < 4; ++i) acc[a][b][4 * q + i] += v[i];
+                        }
         }
+        __syncthreads();
     }
 
-    // 32 rows and 64 columns of the wave's tile at a time through the wave's own piece of LDS:
+    // 32 rows and SW columns of the wave's tile at a time through the wave's own piece of LDS:
     // register 4 q + i of a lane is row r32, column 8 q + 4 g + i.  Chunk c (16
     // bytes) of a staged row lies at c ^ swizzle, so neither side collides.
-    constexpr int PITCH = 64 * OB, CPR = PITCH / 16, PER = 16 / OB, RPI = 64 / CPR;   // rows per store instruction
+    constexpr int PITCH = SW * OB, CPR = PITCH / 16, PER = 16 / OB, RPI = 64 / CPR;   // rows per store instruction
+    if (!mine) return;
     uint8_t* own = smem + wave * 32 * PITCH;
     T* out = reinterpret_cast<T*>(p.out);
-    const bool vec = (p.ldo * OB) % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 15) == 0;
-    auto swiz = [](int row, int c) { return OB == 2 ? c ^ ((row >> 1) & 7) : c ^ (row & 15); };
+    auto swiz = [](int row, int c) { return CPR == 16 ? c ^ (row & 15) : CPR == 8 ? c ^ ((row >> 1) & 7) : c ^ ((row >> 2) & 3); };
 #pragma unroll
     for (int a = 0; a < FM; ++a)
 #pragma unroll
-        for (int h = 0; h < FN; h += 2) {
+        for (int h = 0; h < FN; h += SW / 32) {
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
+            for (int b = 0; b < SW / 32; ++b)
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     T t[4];
@@ -419,8 +406,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(Mx
                 const int m = m0 + wm * WM + a * 32 + row, n = n0 + wn * WN + h * 32 + c * PER;
                 if (m < p.M && n < p.N) {
                     T* dst = out + (int64_t)m * p.ldo + n;
-                    if (vec && n + PER <= p.N) {
-                        *reinterpret_cast<u32x4*>(dst) = v;
+                    if (n + PER <= p.N) {   // at any alignment
+                        *reinterpret_cast<v4i_any*>(dst) = v4i_any{(int)v.x, (int)v.y, (int)v.z, (int)v.w};
                     } else {
                         T e[PER];
                         __builtin_memcpy(e, &v, 16);
@@ -434,23 +421,17 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void mx_tiled_kernel(Mx
         }
 }
 
-template <int BM, int BN, int WM, int WN, int NB, int STAGES, bool A8, bool SK>
+template <int BM, int BN, int WM, int WN, int KW, int NB, int STAGES, bool A8>
 hipError_t launch_out(const MxMatmulArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)(((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN)), SK ? (unsigned)a.splits : 1);
-    const dim3 block((BM / WM) * (BN / WN) * 64);
+    const dim3 grid((unsigned)(((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN)));
+    const dim3 block((BM / WM) * (BN / WN) * KW * 64);
     if (a.out_type == QG_FP32)
-        hipLaunchKernelGGL((mx_tiled_kernel<BM, BN, WM, WN, NB, STAGES, A8, float, SK>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((mx_tiled_kernel<BM, BN, WM, WN, KW, NB, STAGES, A8, float>), grid, block, 0, s, a);
     else if (a.out_type == QG_BF16)
-        hipLaunchKernelGGL((mx_tiled_kernel<BM, BN, WM, WN, NB, STAGES, A8, __bf16, SK>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((mx_tiled_kernel<BM, BN, WM, WN, KW, NB, STAGES, A8, __bf16>), grid, block, 0, s, a);
     else
-        hipLaunchKernelGGL((mx_tiled_kernel<BM, BN, WM, WN, NB, STAGES, A8, _Float16, SK>), grid, block, 0, s, a);
+        hipLaunchKernelGGL((mx_tiled_kernel<BM, BN, WM, WN, KW, NB, STAGES, A8, _Float16>), grid, block, 0, s, a);
     return hipGetLastError();
-}
-
-// At most one workgroup a CU: the whole of its LDS may go to a deep ring.
-template <int BM, int BN>
-bool one_round(const MxMatmulArgs& a) {
-    return (int64_t)((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN) * a.splits <= 256;
 }
 
 }  // namespace mx

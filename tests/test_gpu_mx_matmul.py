@@ -62,7 +62,7 @@ def check(M, N, K, fmt, out, scaled, seed=0, spread=0.0, **kw):
     return got
 
 
-SHAPES = [(1, 16, 32), (1, 1, 32), (2, 33, 96), (1, 4096, 4096), (5, 100, 160), (16, 1000, 2048), (16, 17, 8192), (17, 64, 512),
+SHAPES = [(1, 16, 32), (1, 1, 32), (2, 33, 96), (1, 4096, 4096), (5, 100, 160), (16, 1000, 2048), (16, 17, 8192), (8, 100, 4096), (5, 3000, 1056), (17, 64, 512),
           (33, 129, 320), (64, 256, 256), (100, 300, 1120), (128, 128, 128), (130, 257, 544), (200, 520, 64), (256, 256, 2048),
           (300, 513, 4096), (513, 700, 992), (1000, 1111, 288)]
 
@@ -164,42 +164,37 @@ def test_empty_and_scalar_scale():
 
 
 @pytest.mark.parametrize("M", [1, 16, 64, 200])
-def test_results_repeat_and_workspace_is_left_clean(M):
+def test_results_repeat(M):
     case(f"mx_matmul repeats M={M}")
     N, K = 1500, 4096
     a, sa, _ = operand(M, K, "mxfp8", 3)
     w, sw, _ = operand(N, K, "mxfp4", 4)
-    ws = torch.zeros(max(1024, q.mx_matmul_workspace_bytes(M, N, K)), dtype=torch.uint8, device=dev())
-    first = q.mx_matmul(a, sa, w, sw, workspace=ws)
+    first = q.mx_matmul(a, sa, w, sw)
     for _ in range(3):
-        assert torch.equal(q.mx_matmul(a, sa, w, sw, workspace=ws), first)
-    assert not ws[:1024].any()
+        assert torch.equal(q.mx_matmul(a, sa, w, sw), first)
 
 
-TILES = ["mx_tiled_256x256", "mx_tiled_128x128", "mx_tiled_64x128"]
+TILES = ["mx_tiled_256x256", "mx_tiled_128x128", "mx_tiled_64x128", "mx_tiled_64x64", "mx_tiled_64x32", "mx_tiled_32x32"]
 
 
-@pytest.mark.parametrize("M,N,K", [(1, 1, 32), (40, 300, 96), (257, 129, 512), (300, 700, 1120), (600, 515, 2080)])
-@pytest.mark.parametrize("tile", [0, 1, 2])
+@pytest.mark.parametrize("M,N,K", [(1, 1, 32), (40, 300, 96), (257, 129, 512), (300, 700, 1120), (600, 515, 2080), (2100, 2111, 352),
+                                   (65, 90, 4096), (33, 40, 5024)])
+@pytest.mark.parametrize("tile", range(6))
 @pytest.mark.parametrize("fmt", ["mxfp8", "mxfp4"])
 def test_every_tile(M, N, K, tile, fmt):
-    """Each tile shape, whatever the plan would choose, whole and split."""
+    """Each tile shape, whatever the plan would choose."""
     case(f"mx_matmul tile {tile} {M}x{N}x{K} {fmt}")
-    with env(QGEMM_MX_TILE=tile, QGEMM_MX_SPLITS=1):
+    with env(QGEMM_MX_TILE=tile):
         check(M, N, K, fmt, torch.float32, True)
         assert q._binding.last_kernel() == TILES[tile]
-        check(M, N, K, fmt, torch.bfloat16, False)
-    if tile and K > 512:
-        for s in (2, 3, 5):
-            with env(QGEMM_MX_TILE=tile, QGEMM_MX_SPLITS=s):
-                check(M, N, K, fmt, torch.float32, True)
-                assert q._binding.last_kernel() == TILES[tile] + "_splitk"
-                check(M, N, K, fmt, torch.float16, False)
+        check(M, N, K, fmt, torch.bfloat16, False, spread=3.0)
+        check(M, N, K, fmt, torch.float16, True)
 
 
 @pytest.mark.parametrize("M,N,K,kernel", [
-    (1, 512, 512, "mx_decode"), (16, 512, 544, "mx_decode"), (17, 512, 512, "mx_tiled_64x128"),
-    (64, 4096, 8192, "mx_tiled_64x128_splitk"), (2048, 2048, 512, "mx_tiled_128x128"), (4096, 4096, 256, "mx_tiled_256x256")])
+    (1, 512, 512, "mx_decode"), (8, 512, 544, "mx_decode"), (9, 512, 544, "mx_tiled_32x32"), (16, 8192, 64, "mx_tiled_32x32"), (17, 512, 512, "mx_tiled_32x32"),
+    (64, 8192, 256, "mx_tiled_64x32"), (128, 8192, 256, "mx_tiled_64x64"), (512, 4096, 256, "mx_tiled_64x128"),
+    (2048, 2048, 512, "mx_tiled_128x128"), (1300, 6000, 96, "mx_tiled_128x128"), (4096, 4096, 256, "mx_tiled_256x256")])
 def test_kernel_choice(M, N, K, kernel):
     case(f"mx_matmul kernel for {M}x{N}x{K}")
     check(M, N, K, "mxfp4", torch.bfloat16, True)

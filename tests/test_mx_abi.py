@@ -101,7 +101,7 @@ def test_quantisers_reject_their_own():
 
 
 MUL = dict(M=4, N=40, K=64, A=FAKE, af=M4, lda=32, as_=FAKE, ldas=2, W=FAKE, ldw=32, ws=FAKE, ldws=2, padded=1, s=None,
-           out=FAKE, ot=BF16, ldo=40, work=None, wb=0, stream=None)
+           out=FAKE, ot=BF16, ldo=40, stream=None)
 
 
 @pytest.mark.parametrize("kw,code", [
@@ -109,7 +109,7 @@ MUL = dict(M=4, N=40, K=64, A=FAKE, af=M4, lda=32, as_=FAKE, ldas=2, W=FAKE, ldw
     (dict(K=48), INV), (dict(K=-32), INV), (dict(A=None), INV), (dict(as_=None), INV), (dict(W=None), INV),
     (dict(ws=None), INV), (dict(out=None), INV), (dict(lda=31), INV), (dict(af=M8, lda=63), INV), (dict(ldw=31), INV),
     (dict(ldas=1), INV), (dict(ldws=1), INV), (dict(ldo=39), INV), (dict(af=I8), INV), (dict(ot=I8), INV),
-    (dict(out=ODD), INV), (dict(s=ODD), INV), (dict(work=ODD, wb=1 << 20), INV), (dict(lda=1 << 22), UNS),
+    (dict(out=ODD), INV), (dict(s=ODD), INV), (dict(lda=1 << 22), UNS),
     (dict(ldw=1 << 22), UNS), (dict(ldas=1 << 22), UNS), (dict(ldws=1 << 22), UNS),
 ])
 def test_mx_matmul_rejects(kw, code):
