@@ -110,7 +110,8 @@ qg_status rms_norm_grad(int64_t M, int64_t n,
  * x [M,n] (`type` QG_FP32, QG_BF16 or QG_FP16) to MX form.  format QG_MXFP8
  * or QG_MXFP4; codes rows hold 32 B elements at a stride of ldc bytes, scale
  * is [M,B] at a stride of lds bytes.  mx_matmul's fast kernels want ldc a
- * multiple of 16 and lds a multiple of 4.
+ * multiple of 16 and lds a multiple of 4.  QG_ERR_UNSUPPORTED, here and in
+ * mx_dequantize, for 2^32 or more blocks.
  */
 qg_status mx_quantize(int64_t M, int64_t n,
                       const void* x, qg_dtype type, int64_t ldx,
@@ -141,9 +142,8 @@ qg_status mx_dequantize(int64_t M, int64_t n,
  *   out: QG_FP32, QG_BF16 or QG_FP16, [M,N], rounded once.
  * Operands with 16-byte aligned rows, scale rows at multiples of 4 bytes and
  * readable to the end of the 4-byte word that holds their last byte take the
- * fast kernels (few rows: one that streams W once); `scale_rows_padded` says
- * that they are readable so, the last row's too.  All others run a
- * slower kernel that reads bytes.
+ * fast kernels; `scale_rows_padded` says that they are readable so, the last
+ * row's too.  All others run a slower kernel that reads bytes.
  * Accuracy: e2m1 products are exact and summed in fp32.  With e4m3
  * activations the matrix cores add groups of 16 products k with what lies
  * 2^-14 below the largest of them cut off, an error of about 1e-5 of the
@@ -151,7 +151,8 @@ qg_status mx_dequantize(int64_t M, int64_t n,
  * fp32 output the activations are split in two by magnitude so that nothing
  * is cut off.  Sums are added in a fixed order: results repeat bit for bit.
  * An element whose block scale is 255 gives NaN.
- * QG_ERR_UNSUPPORTED if 512 rows of an operand span 2^31 bytes.
+ * QG_ERR_UNSUPPORTED if 512 rows of an operand span 2^31 bytes, or the output
+ * has 2^23 or more tiles of 256 x 256.
  */
 qg_status mx_matmul(int64_t M, int64_t N, int64_t K,
                     const void* A, qg_dtype a_format, int64_t lda,

@@ -130,7 +130,7 @@ qg_status mx_quantize(int64_t M, int64_t n, const void* x, qg_dtype type, int64_
     if (x == nullptr || codes == nullptr || scale == nullptr || ldx < n || ldc < code_bytes(format, n) ||
         lds < blocks_of(n) || !aligned_for(x, type))
         return QG_ERR_INVALID_ARGUMENT;
-    if (M * blocks_of(n) >= (int64_t)1 << 38) return QG_ERR_UNSUPPORTED;   // one grid dimension
+    if (M * blocks_of(n) >= (int64_t)1 << 32) return QG_ERR_UNSUPPORTED;   // one launch's threads
     (void)hipGetLastError();
     const qg::MxCodecArgs a{M, n, x, ldx, nullptr, 0, (uint8_t*)codes, ldc, scale, lds};
     const char* name = "";
@@ -144,7 +144,7 @@ qg_status mx_dequantize(int64_t M, int64_t n, const void* codes, qg_dtype format
     if (out == nullptr || codes == nullptr || scale == nullptr || ldo < n || ldc < code_bytes(format, n) ||
         lds < blocks_of(n) || !aligned_for(out, out_type))
         return QG_ERR_INVALID_ARGUMENT;
-    if (M * blocks_of(n) >= (int64_t)1 << 38) return QG_ERR_UNSUPPORTED;
+    if (M * blocks_of(n) >= (int64_t)1 << 32) return QG_ERR_UNSUPPORTED;
     (void)hipGetLastError();
     const qg::MxCodecArgs a{M, n, nullptr, 0, out, ldo, (uint8_t*)const_cast<void*>(codes), ldc,
                             const_cast<uint8_t*>(scale), lds};
@@ -172,6 +172,7 @@ qg_status mx_matmul(int64_t M, int64_t N, int64_t K, const void* A, qg_dtype a_f
                       (ld_a_scale % 4 == 0 || M == 1) && (ld_w_scale % 4 == 0 || N == 1) && aligned(a_scale, 4) &&
                       aligned(w_scale, 4) && !env_is("QGEMM_MX_KERNEL", "bytes");
     if (!fast && (M + 15) / 16 > 65535) return QG_ERR_UNSUPPORTED;   // the other kernel's second grid dimension
+    if (((M + 255) / 256) * ((N + 255) / 256) >= (int64_t)1 << 23) return QG_ERR_UNSUPPORTED;   // one launch's threads
     (void)hipGetLastError();
     qg::MxMatmulArgs a{};
     a.M = (int)M; a.N = (int)N; a.K = (int)K;
