@@ -9,8 +9,9 @@
 // is added in, and MX blocks leave before the row's sum is known.
 //
 // Bound by HBM: every value is read once and kept in registers (at most 64 a
-// lane), one barrier per row.  A row is shared by G lanes: one wave up to
-// 1024 columns (four rows per workgroup), 256 lanes up to 8192, 1024 beyond.
+// lane), one barrier per row.  A row is shared by G lanes: 16 up to 128 columns,
+// 32 up to 256, a wave up to 1024 (16, 8 and 4 rows per workgroup), 256 lanes up to
+// 8192, 512 up to 16384, 1024 beyond.
 // 8192 x 8192 bf16 with a residual to int8: 73.6 us, 6.4 TB/s over what is read
 // and written (a copy of 2 GiB runs at 4.85); one row 3.7 us, the launch's and one
 // load's latency.
@@ -26,7 +27,7 @@ enum { OUT_SAME = 0, OUT_F32 = 1, OUT_I8 = 2, OUT_MX8 = 3, OUT_MX4 = 4 };
 template <int G>
 __device__ __forceinline__ void row_reduce(float& ss, uint32_t& top) {
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) {
+    for (int off = G < 64 ? G / 2 : 32; off >= 1; off >>= 1) {
         ss += __shfl_xor(ss, off);
         top = umax(top, (uint32_t)__shfl_xor((int)top, off));
     }
@@ -55,8 +56,9 @@ template <typename T, int G, int ITER, int OUT, bool WF32, bool TINY, bool NT>
 __global__ __launch_bounds__(G < 256 ? 256 : G, ((std::is_same<T, _Float16>::value && G <= 512) ? 6 : 1)) void rms_norm_kernel(RmsNormArgs a) {
     constexpr int RPW = G < 256 ? 256 / G : 1;   // rows per workgroup
     const int t = threadIdx.x % G;
-    const int64_t row = (int64_t)blockIdx.x * RPW + __builtin_amdgcn_readfirstlane(threadIdx.x / G);
-    if (row >= a.M) return;                      // whole waves (G = 64 has no barrier)
+    const int sub = threadIdx.x / G;
+    const int64_t row = (int64_t)blockIdx.x * RPW + (G < 64 ? sub : __builtin_amdgcn_readfirstlane(sub));
+    if (row >= a.M) return;                      // whole groups (no barrier with several in a workgroup)
     const int n = a.n;
     const T* x = reinterpret_cast<const T*>(a.x) + row * a.ldx;
     const T* res = a.res != nullptr ? reinterpret_cast<const T*>(a.res) + row * a.ldr : nullptr;
@@ -159,7 +161,9 @@ hipError_t by_width(const RmsNormArgs& a, hipStream_t s) {
                            dim3((unsigned)((a.M + RPW - 1) / RPW)), dim3(G < 256 ? 256 : G), 0, s, a);         \
         return hipGetLastError();                                                                              \
     }
-    QG_NORM(64, 1, 7, true, false)
+    QG_NORM(16, 1, 7, true, false)
+    QG_NORM(16, 1, 128, false, false)
+    QG_NORM(32, 1, 256, false, false)
     QG_NORM(64, 1, 512, false, false)
     QG_NORM(64, 2, 1024, false, false)
     QG_NORM(256, 1, 2048, false, false)

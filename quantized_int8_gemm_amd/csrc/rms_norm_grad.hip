@@ -16,7 +16,7 @@ namespace {
 template <int G>
 __device__ __forceinline__ float row_sum(float v, float* red) {
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+    for (int off = G < 64 ? G / 2 : 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
     if constexpr (G > 64) {
         const int wave = threadIdx.x >> 6;
         if ((threadIdx.x & 63) == 0) red[wave] = v;
@@ -33,7 +33,7 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 // passes through the registers:
 //  * AHEAD, up to 256 lanes: the next row's loads are in flight while this one's
 //    sum is completed and its results are stored;
-//  * HOLD, 512 and 1024 lanes: one row at a time, in at most 128 registers, so
+//  * HOLD, 512 to 1024 lanes: one row at a time, in at most 128 registers, so
 //    that two workgroups share a CU and one's loads cover the other's barrier
 //    (5000 x 6144 bf16 54.7 us, AHEAD 59.3; 2000 x 16384 55.6, AHEAD 63.9);
 //  * AGAIN, past 16384 columns, where dw alone takes 32 or 64 registers: a row is
@@ -46,9 +46,9 @@ __global__ __launch_bounds__(G < 256 ? 256 : G, G < 512 ? 1 : 4) void rms_norm_g
     constexpr int RPW = G < 256 ? 256 / G : 1;
     constexpr int MODE = G < 512 ? AHEAD : ITER <= 2 ? HOLD : AGAIN;
     constexpr int WI = MODE == AGAIN ? 1 : ITER, BUFS = MODE == AHEAD ? 2 : 1;
-    __shared__ float red[2][G / 64];
+    __shared__ float red[2][G < 64 ? 1 : G / 64];
     __shared__ float part[RPW > 1 ? (RPW - 1) * G * ITER * 8 : 1];
-    const int t = threadIdx.x % G, sub = __builtin_amdgcn_readfirstlane(threadIdx.x / G);
+    const int t = threadIdx.x % G, group = threadIdx.x / G, sub = G < 64 ? group : __builtin_amdgcn_readfirstlane(group);
     const int n = a.n;
     float w[WI][8], dw[ITER][8];
 #pragma unroll
@@ -187,8 +187,8 @@ __global__ __launch_bounds__(32 * SUM_ROWS) void rms_norm_grad_sum(const float* 
     if (q == 0 && c < n) dw[c] = (W)(s + red[1][cl] + red[2][cl] + red[3][cl]);
 }
 
-// Lanes per row for n columns: as the kernel table below.
-int rows_per_group(int64_t n) { return n <= 1024 ? 4 : 1; }
+// Rows that a workgroup has in hand at once: as the kernel table below.
+int rows_per_group(int64_t n) { return n <= 128 ? 16 : n <= 256 ? 8 : n <= 1024 ? 4 : 1; }
 
 template <typename T, bool WF32>
 hipError_t by_width(const RmsNormGradArgs& a, hipStream_t s) {
@@ -200,7 +200,9 @@ hipError_t by_width(const RmsNormGradArgs& a, hipStream_t s) {
                            dim3(G < 256 ? 256 : G), 0, s, a);                                                  \
         done = true;                                                                                           \
     }
-    QG_GRAD(64, 1, 7, true, false)
+    QG_GRAD(16, 1, 7, true, false)
+    QG_GRAD(16, 1, 128, false, false)
+    QG_GRAD(32, 1, 256, false, false)
     QG_GRAD(64, 1, 512, false, false)
     QG_GRAD(64, 2, 1024, false, false)
     QG_GRAD(256, 1, 2048, false, false)
@@ -208,10 +210,12 @@ hipError_t by_width(const RmsNormGradArgs& a, hipStream_t s) {
         (a.dh == nullptr || whole_lines(a.dh, a.lddh * sizeof(T)))) {
         QG_GRAD(256, 2, 4096, false, true)
         QG_GRAD(512, 2, 8192, false, true)
+        QG_GRAD(768, 2, 12288, false, true)
         QG_GRAD(1024, 2, 16384, false, true)
     }
     QG_GRAD(256, 2, 4096, false, false)
     QG_GRAD(512, 2, 8192, false, false)
+    QG_GRAD(768, 2, 12288, false, false)
     QG_GRAD(1024, 2, 16384, false, false)
     QG_GRAD(1024, 4, 32768, false, false)
     QG_GRAD(1024, 8, 65536, false, false)

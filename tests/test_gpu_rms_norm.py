@@ -15,7 +15,7 @@ HALF = {torch.float32: U, torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
 TYPES = [torch.float32, torch.bfloat16, torch.float16]
 # a lane adds at most 64 squares, then at most 6 + 15 sums: half of that reaches 1/sqrt, which adds 4 steps
 R_STEPS = 48
-SHAPES = [(1, 1), (3, 7), (5, 32), (1, 4096), (4, 100), (9, 512), (7, 513), (6, 1024), (3, 1025), (2, 2048), (3, 4095),
+SHAPES = [(1, 1), (3, 7), (35, 5), (5, 32), (33, 127), (17, 128), (40, 129), (19, 250), (7, 256), (11, 257), (2, 12290), (1, 4096), (4, 100), (9, 512), (7, 513), (6, 1024), (3, 1025), (2, 2048), (3, 4095),
           (2, 5000), (2, 8192), (2, 8193), (1, 16384), (1, 20001), (1, 65536), (300, 256), (0, 64)]
 
 
@@ -141,7 +141,7 @@ def test_strides_in_place_and_rank(dtype):
     assert c.shape == (2, 3, 96) and s.shape == (2, 3, 6) and r.shape == (2, 3)
 
 
-GRAD_SHAPES = [(1, 1), (5, 7), (1, 4096), (37, 100), (9, 512), (700, 96), (65, 1000), (33, 1025), (700, 2048), (17, 4095),
+GRAD_SHAPES = [(1, 1), (5, 7), (9000, 6), (35, 128), (8300, 65), (19, 200), (5000, 256), (4, 257), (6, 12288), (5, 12289), (1, 4096), (37, 100), (9, 512), (700, 96), (65, 1000), (33, 1025), (700, 2048), (17, 4095),
                (1100, 4096), (40, 8192), (9, 8200), (5, 16384), (3, 20000), (2, 65536)]
 
 
@@ -165,8 +165,8 @@ def test_grad(rows, n, dtype):
             tol = tol + U * 2 * np.abs(d64(dh))
         tiny = 2.0 ** -25 if dtype == torch.float16 else 0
         assert np.all(np.abs(d64(dx) - wx) <= tol + HALF[dtype] * 1.01 * np.abs(wx) + tiny)
-        # dw: at most ceil(rows / 512) rows in a lane, 3 groups, 64 partial rows and 7 sums, 2 steps a term
-        steps = -(-rows // 512) + 3 + 64 + 7 + 4
+        # dw: at most ceil(rows / 256) rows in a lane, 15 groups, 16 partial rows, 7 + 3 sums, 2 steps a term
+        steps = -(-rows // 256) + 15 + 16 + 10 + 4
         tiny = 2.0 ** -25 if wdtype == torch.float16 else 0
         size = np.abs(d64(dy) * d64(h) * rr).sum(0)
         assert np.all(np.abs(d64(dw) - ww) <= steps * U * size + HALF[wdtype] * 1.01 * np.abs(ww) + tiny)
