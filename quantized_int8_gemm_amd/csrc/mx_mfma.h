@@ -33,10 +33,12 @@ __device__ __forceinline__ v8i words8(u32x4 a, u32x4 b) {
 __device__ __forceinline__ void split_e4m3(v8i a, v8i& hi, v8i& lo) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const uint32_t top = ((uint32_t)a[i] >> 6) & 0x01010101u;
-        const uint32_t mask = (top << 8) - top;   // 0xff for each byte whose bit 6 is set
-        hi[i] = (int)((uint32_t)a[i] & mask);
-        lo[i] = (int)((uint32_t)a[i] & ~mask);
+        // 0xff for each byte whose bit 6 is set: the byte permute's selectors 8 to 11
+        // repeat the top bit of bytes 1, 3, 5 and 7 of its two operands
+        const uint32_t x = (uint32_t)a[i];
+        const uint32_t mask = __builtin_amdgcn_perm(x << 1, x << 9, 0x0b090a08u);
+        hi[i] = (int)(x & mask);
+        lo[i] = (int)(x ^ (x & mask));
     }
 }
 

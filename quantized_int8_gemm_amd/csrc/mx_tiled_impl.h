@@ -421,17 +421,23 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * KW * 64) void mx_tiled_kern
         }
 }
 
+template <int BM, int BN, int WM, int WN, int KW, int NB, int STAGES, bool A8, typename T>
+hipError_t launch_one(const MxMatmulArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)(((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN)));
+    hipLaunchKernelGGL((mx_tiled_kernel<BM, BN, WM, WN, KW, NB, STAGES, A8, T>), grid, dim3((BM / WM) * (BN / WN) * KW * 64), 0, s, a);
+    return hipGetLastError();
+}
+
+template <int BM, int BN, int WM, int WN, int KW, int NB, int STAGES, bool A8>
+hipError_t launch_half(const MxMatmulArgs& a, hipStream_t s) {
+    if (a.out_type == QG_BF16) return launch_one<BM, BN, WM, WN, KW, NB, STAGES, A8, __bf16>(a, s);
+    return launch_one<BM, BN, WM, WN, KW, NB, STAGES, A8, _Float16>(a, s);
+}
+
 template <int BM, int BN, int WM, int WN, int KW, int NB, int STAGES, bool A8>
 hipError_t launch_out(const MxMatmulArgs& a, hipStream_t s) {
-    const dim3 grid((unsigned)(((a.M + BM - 1) / BM) * ((a.N + BN - 1) / BN)));
-    const dim3 block((BM / WM) * (BN / WN) * KW * 64);
-    if (a.out_type == QG_FP32)
-        hipLaunchKernelGGL((mx_tiled_kernel<BM, BN, WM, WN, KW, NB, STAGES, A8, float>), grid, block, 0, s, a);
-    else if (a.out_type == QG_BF16)
-        hipLaunchKernelGGL((mx_tiled_kernel<BM, BN, WM, WN, KW, NB, STAGES, A8, __bf16>), grid, block, 0, s, a);
-    else
-        hipLaunchKernelGGL((mx_tiled_kernel<BM, BN, WM, WN, KW, NB, STAGES, A8, _Float16>), grid, block, 0, s, a);
-    return hipGetLastError();
+    if (a.out_type == QG_FP32) return launch_one<BM, BN, WM, WN, KW, NB, STAGES, A8, float>(a, s);
+    return launch_half<BM, BN, WM, WN, KW, NB, STAGES, A8>(a, s);
 }
 
 }  // namespace mx
