@@ -7,42 +7,46 @@
 //    bytes land at consecutive LDS addresses, so the lane picks the global
 //    segment whose swizzled home is that address.  Rows past M or N, and
 //    segments past K, lie outside the buffer windows and read as zero.
-//  * Scale bytes come in groups of 16 a row (2 or 4 stages' worth) into two
-//    places beside the ring, a part of the next group with every stage.  Fetched
-//    a stage's 8 bytes at a time they asked L2 for as many cache lines as the
-//    codes did: 8192^3 MXFP4 292 us so, 276 us in groups.
+//  * Scale bytes come in groups of 16 a row (1, 2 or 4 stages' worth) into places
+//    beside the ring, a part of a later group with every stage.  Fetched a stage's 8
+//    bytes at a time they asked L2 for as many cache lines as the codes did: 8192^3
+//    MXFP4 292 us so, 276 in groups.
 //  * The contraction may visit blocks in any order, so that a lane's scales lie
 //    side by side: the two lane groups of a 32x32x64 instruction take blocks s
-//    and NB/2 + s of the stage in step s.  One NB/2-byte read per fragment row
-//    then brings the scales of the whole stage, and the instruction picks the
-//    byte.
+//    and NB/2 + s of the stage in step s.  One read per fragment row then brings
+//    the scales of all a wave's steps, and the instruction picks the byte.
 //  * While a step's products run, the next step's fragments are read, across the
 //    stages' border too: the barrier stands before the stage's last step, when
 //    every wave holds the last fragments of the old stage, so its ring place is
 //    free for the chunk STAGES on, whose loads are spread over that step and the
-//    next (all at once they hold the matrix instructions up: 287 us).  Against
-//    reading after the barrier: 8192^3 303 -> 292 us, 4096^3 with MXFP8
-//    activations 62.8 -> 58.3 us.
-// What bounds it (8192^3 MXFP4, 276 us, 4.0 PFLOP/s): the instruction alone on
-// register operands runs at 7.1 PFLOP/s on random data, the clock falling from
-// 2.4 to 1.7 GHz (9.7 PFLOP/s on zeros); here the matrix cores are busy 53 % of
-// the cycles at 1.8 GHz.  The same kernel without its loads takes 223 us, without
-// its fragment reads 265, without its products 226, with neither reads nor
-// products 172: the loads' path (64 B a cycle and CU) is busy half of the time and
-// what is left is that these streams do not overlap fully.  Four waves of 128 x
-// 128 (a third fewer fragment reads, one wave per SIMD) measured 284 us.
+//    next (all at once they hold the matrix instructions up).  Against reading
+//    after the barrier: 8192^3 303 -> 292 us, 4096^3 with MXFP8 activations 62.8 ->
+//    58.3.  The products of one row block may mix with the next one's reads: 8192^3
+//    with MXFP8 activations 410 -> 400 us.
 //  * KW waves share a wave tile, each with its part of every stage's steps; their
 //    sums are added through LDS, in order, so results repeat bit for bit.  Small
 //    tiles need it: with one wave a SIMD every step waits for its fragments.
-//  * The finished wave tile goes through LDS, 32 rows at a time, and leaves in
-//    whole rows of 64 columns.
+//  * The finished wave tile goes through LDS, 32 rows and 64 columns at a time, and
+//    leaves in whole rows of those.
+// What bounds 8192^3 MXFP4 (259 us, 4.2 PFLOP/s): the instruction alone on register
+// operands runs at 7.1 PFLOP/s on random data, the clock falling from 2.4 to 1.7 GHz
+// (9.7 PFLOP/s on zeros), and on this product's fragments at 5.9; the kernel keeps
+// the matrix cores busy 53 % of the cycles at 1.8 GHz.  Taken at 276 us, it ran 223 us
+// without its loads, 265 without its fragment reads, 226 without its products and 172
+// with its loads alone: no stream stands out, and each costs clock.  A stage takes
+// 2918 cycles of which 2048 are products; the first chunk's latency is 6500 cycles a
+// tile and the output 5400, but one workgroup a CU that walks its tiles and fetches
+// the next one's first chunk under the output ran at the same 272 us (the clock falls
+// as the stalls go).  Four waves of 128 x 128 (a third fewer fragment reads, one wave
+// per SIMD) measured 284 against 276 us, wave priorities the same, two steps' worth
+// of loads at once 287.
 #pragma once
 #include "mx_mfma.h"
 
 namespace qg {
 namespace mx {
 
-constexpr int GROUP_M = 8;
+constexpr int GROUP_M = 4;   // tile rows walked together (8: 8192^3 MXFP4 261.3 against 258.9 us)
 
 __device__ __forceinline__ v4i rsrc_words(const void* base, uint32_t bytes) {
     const uint64_t a = reinterpret_cast<uint64_t>(base);
@@ -289,8 +293,14 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * KW * 64) void mx_tiled_kern
         }
 #pragma unroll
         for (int a = 0; a < FM; ++a) {
-            // W's fragments go first: every product of the next step needs one
-            if (a == 0) read_w(S, ns, nxt);
+            // W's fragments: first where A's are twice their size, else along with A's
+            // (8192^3 MXFP4 261.5 against 259.7 us, MXFP8 398 against 401)
+            if constexpr (A8) {
+                if (a == 0) read_w(S, ns, nxt);
+            } else {
+#pragma unroll
+                for (int b = a * FN / FM; b < (a + 1) * FN / FM; ++b) wf[nxt][b] = read16(S + w_at[ns] + b * 32 * WW);
+            }
             read_a(S, a, ns, nxt);
             if (last && a == 0) {
                 read_scales(kt + 1);
@@ -303,7 +313,6 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * KW * 64) void mx_tiled_kern
             for (int b = 0; b < FN; ++b)
                 acc[a][b] = mfma_step<A8, EXACT>(s, words4(wf[cur][b]), ws[b], A8 ? words8(af[cur][a][0], af[cur][a][AV - 1]) : words4(af[cur][a][0]),
                                                  as[a], acc[a][b]);
-            __builtin_amdgcn_sched_barrier(0);
         }
     };
 #pragma unroll
