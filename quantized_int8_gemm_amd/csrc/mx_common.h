@@ -19,11 +19,22 @@ template <typename T> struct Pack8 { uint32_t w[2 * sizeof(T)]; };
 typedef int v4i_any __attribute__((ext_vector_type(4), aligned(1)));
 typedef _Float16 v2h __attribute__((ext_vector_type(2)));
 
+// One half of a dword as a float: v * 1 - 0, exact for every value.  From vector
+// elements the compiler shifts high halves down first and keeps halves apart in
+// registers (gradient 3691 x 4096 fp16 44.7 us so, 28.1 with this; norm 4000 x 8192 fp16
+// to int8 44.8 and 41.0).
+__device__ __forceinline__ float half_value(uint32_t pair, bool high) {
+    float v;
+    if (high) asm("v_fma_mix_f32 %0, %1, 1.0, neg(0) op_sel:[1,0,0] op_sel_hi:[1,0,0]" : "=v"(v) : "v"(pair));
+    else asm("v_fma_mix_f32 %0, %1, 1.0, neg(0) op_sel_hi:[1,0,0]" : "=v"(v) : "v"(pair));
+    return v;
+}
+
 template <typename T>
 __device__ __forceinline__ float value(const Pack8<T>& p, int e) {
     if constexpr (sizeof(T) == 4) return __uint_as_float(p.w[e]);
     else if constexpr (std::is_same<T, __bf16>::value) return __uint_as_float(e & 1 ? p.w[e / 2] & 0xffff0000u : p.w[e / 2] << 16);
-    else return (float)__builtin_bit_cast(v2h, p.w[e / 2])[e & 1];
+    else return half_value(p.w[e / 2], e & 1);
 }
 
 // Eight values rounded once to T.

@@ -31,29 +31,34 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 // The lane's columns are (i * G + t) * 8 .. + 7.  Row groups of G < 256 lanes
 // share a workgroup; their partial sums of dw are added through LDS.  How a row
 // passes through the registers:
-//  * AHEAD, up to 256 lanes: the next row's loads are in flight while this one's
-//    sum is completed and its results are stored;
+//  * AHEAD, up to 256 lanes, or 768 of 16-bit values, which have a CU to themselves and
+//    so 168 registers: the next row's loads are in flight while this one's sum is
+//    completed and its results are stored (3691 x 12288 bf16 67.1 us, HOLD 70.6; fp32
+//    would spill, 168 against 145);
 //  * HOLD, 512 to 1024 lanes: one row at a time, in at most 128 registers, so
 //    that two workgroups share a CU and one's loads cover the other's barrier
-//    (5000 x 6144 bf16 54.7 us, AHEAD 59.3; 2000 x 16384 55.6, AHEAD 63.9);
-//  * AGAIN, past 16384 columns, where dw alone takes 32 or 64 registers: a row is
-//    read once for its sum and again, from the caches, for its results.
+//    (5000 x 6144 bf16 54.7 us, AHEAD 59.3; 2000 x 16384 55.6, AHEAD 63.9); past
+//    16384 columns of 16 bits too, the weights read again where they are used (1000
+//    x 32768 bf16 105 us, AGAIN 115);
+//  * AGAIN, wider rows, where dw alone takes 32 or 64 registers: a row is read
+//    once for its sum and again, from the caches, for its results.
 enum { AHEAD, HOLD, AGAIN };
 
 template <typename T, int G, int ITER, bool WF32, bool TINY, bool NT>
-__global__ __launch_bounds__(G < 256 ? 256 : G, G < 512 ? 1 : 4) void rms_norm_grad_kernel(RmsNormGradArgs a) {
+__global__ __launch_bounds__(G < 256 ? 256 : G, (G < 512 ? 1 : G == 768 && sizeof(T) == 2 ? 3 : 4)) void rms_norm_grad_kernel(RmsNormGradArgs a) {
     typedef typename std::conditional<WF32, float, T>::type W;
     constexpr int RPW = G < 256 ? 256 / G : 1;
-    constexpr int MODE = G < 512 ? AHEAD : ITER <= 2 ? HOLD : AGAIN;
+    constexpr int MODE = G < 512 || (G == 768 && sizeof(T) == 2) ? AHEAD : ITER <= (sizeof(T) == 2 ? 4 : 2) ? HOLD : AGAIN;
+    constexpr bool WEIGHTS = ITER <= 2;   // in registers; else read again where they are used
     constexpr int WI = MODE == AGAIN ? 1 : ITER, BUFS = MODE == AHEAD ? 2 : 1;
     __shared__ float red[2][G < 64 ? 1 : G / 64];
     __shared__ float part[RPW > 1 ? (RPW - 1) * G * ITER * 8 : 1];
     const int t = threadIdx.x % G, group = threadIdx.x / G, sub = G < 64 ? group : __builtin_amdgcn_readfirstlane(group);
     const int n = a.n;
-    float w[WI][8], dw[ITER][8];
+    float w[WEIGHTS ? ITER : 1][8], dw[ITER][8];
 #pragma unroll
     for (int i = 0; i < ITER; ++i) {
-        if constexpr (MODE != AGAIN) load_weights<W, TINY>(a.weight, (i * G + t) * 8, n, w[i]);
+        if constexpr (WEIGHTS) load_weights<W, TINY>(a.weight, (i * G + t) * 8, n, w[i]);
 #pragma unroll
         for (int e = 0; e < 8; ++e) dw[i][e] = 0.f;
     }
@@ -73,6 +78,13 @@ __global__ __launch_bounds__(G < 256 ? 256 : G, G < 512 ? 1 : 4) void rms_norm_g
         }
         rv[buf] = a.rstd[row];
     };
+    // The weights' address, new to the compiler each time, lest it keep what it read
+    // for the next row in registers that are not there.
+    auto weight_now = [&]() {
+        const void* p = a.weight;
+        asm volatile("" : "+s"(p));
+        return p;
+    };
     auto hold_packed = [&](int buf) {
 #pragma unroll
         for (int i = 0; i < WI; ++i) {
@@ -89,14 +101,13 @@ __global__ __launch_bounds__(G < 256 ? 256 : G, G < 512 ? 1 : 4) void rms_norm_g
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
             const int at = MODE == AGAIN ? 0 : i;
-            if constexpr (MODE == AGAIN) {
-                load_weights<W, TINY>(a.weight, (i * G + t) * 8, n, w[0]);
-                fetch(row, i, buf, 0, false);
-            }
+            const int wi = WEIGHTS ? i : 0;
+            if constexpr (!WEIGHTS) load_weights<W, TINY>(weight_now(), (i * G + t) * 8, n, w[0]);
+            if constexpr (MODE == AGAIN) fetch(row, i, buf, 0, false);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const float yh = value(yv[buf][at], e) * value(hv[buf][at], e);
-                dot = __builtin_fmaf(yh, w[at][e], dot);
+                dot = __builtin_fmaf(yh, w[wi][e], dot);
                 dw[i][e] = __builtin_fmaf(yh, r, dw[i][e]);
             }
             __builtin_amdgcn_sched_barrier(0);   // one group unpacked at a time
@@ -106,15 +117,13 @@ __global__ __launch_bounds__(G < 256 ? 256 : G, G < 512 ? 1 : 4) void rms_norm_g
         if constexpr (MODE != AGAIN) hold_packed(buf);
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
-            const int c = (i * G + t) * 8, at = MODE == AGAIN ? 0 : i;
-            if constexpr (MODE == AGAIN) {
-                load_weights<W, TINY>(a.weight, c, n, w[0]);
-                fetch(row, i, buf, 0, true);
-            }
+            const int c = (i * G + t) * 8, at = MODE == AGAIN ? 0 : i, wi = WEIGHTS ? i : 0;
+            if constexpr (!WEIGHTS) load_weights<W, TINY>(weight_now(), c, n, w[0]);
+            if constexpr (MODE == AGAIN) fetch(row, i, buf, 0, true);
             float o[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                o[e] = r * (value(yv[buf][at], e) * w[at][e]) - k * value(hv[buf][at], e);
+                o[e] = r * (value(yv[buf][at], e) * w[wi][e]) - k * value(hv[buf][at], e);
                 if (a.dh != nullptr) o[e] += value(sv[buf][at], e);
             }
             if (c < n) store8(reinterpret_cast<T*>(a.dx) + (int64_t)row * a.ldx, c, n, pack<T>(o));

@@ -209,3 +209,14 @@ def test_gradient_of_the_forward_by_differences():
     assert abs(along - (dx.double() * u).sum().item()) <= noise + 100 * step ** 2
     along = (f(h, w + step * v) - f(h, w - step * v)) / (2 * step)
     assert abs(along - (dw.double() * v).sum().item()) <= noise + 1e-3
+
+
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_every_16_bit_value_passes_unchanged(dtype):
+    # h = x + (-0) is x itself, the sign of a zero too; NaN stays some NaN
+    case(f"every {dtype}")
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(dtype).reshape(256, 256)
+    h = q.rms_norm(*up(x, torch.ones(256, dtype=dtype)), residual=up(torch.full_like(x, -0.0))[0])[2].cpu()
+    nan = x.isnan()
+    assert torch.equal(h.isnan(), nan)
+    assert torch.equal(h.view(torch.int16)[~nan], x.view(torch.int16)[~nan])
