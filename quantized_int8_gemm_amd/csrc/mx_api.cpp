@@ -40,7 +40,8 @@ int env_int(const char* name, int dflt) {
 // Kernels of the MX product.
 enum MxKind { MX_256x256, MX_128x128, MX_64x128, MX_64x64, MX_64x32, MX_32x32, MX_DECODE };
 
-MxKind mx_kind(int64_t M, int64_t N) {
+// split: the activations' codes are split in two, so every tile multiplies twice.
+MxKind mx_kind(int64_t M, int64_t N, bool split) {
     const int forced = env_int("QGEMM_MX_TILE", -1);
     if (forced >= 0 && forced <= MX_DECODE && (forced != MX_DECODE || M <= qg::MX_DECODE_MAX_M)) return (MxKind)forced;
     auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
@@ -50,7 +51,15 @@ MxKind mx_kind(int64_t M, int64_t N) {
     if (tiles(64, 32) <= qg::MX_ROUND) return MX_64x32;
     if (tiles(64, 64) <= qg::MX_ROUND) return MX_64x64;
     if (tiles(64, 128) <= qg::MX_ROUND) return MX_64x128;
-    return tiles(256, 256) >= 160 ? MX_256x256 : MX_128x128;
+    // Beyond: by what the busiest CU gets.  A 256 x 256 tile, alone on its CU, takes as
+    // long as three 128 x 128 tiles, which run two to a CU (split: 3.75, since its waves
+    // then have no registers for the next fragments).  4096 x 4096 x 4096 MXFP4: one
+    // large 38.8 us, four small 47.8; 2444 x 3355 x 2464: one 25.3, three 32.0; 4096 x
+    // 4352 x 4096: two 59.2, five 57.3; 2560 x 2560 x 4096: one 29.5, two 24.5.  Split:
+    // 4096 x 5120 x 4096 two 163, five 128; 8192 x 8192 x 8192 four 688, sixteen 750.
+    const int64_t large = (tiles(256, 256) + qg::MX_ROUND - 1) / qg::MX_ROUND;
+    const int64_t small = (tiles(128, 128) + qg::MX_ROUND - 1) / qg::MX_ROUND;
+    return 4 * small >= (split ? 15 : 12) * large ? MX_256x256 : MX_128x128;
 }
 
 qg_status nothing() {
@@ -183,7 +192,7 @@ qg_status mx_matmul(int64_t M, int64_t N, int64_t K, const void* A, qg_dtype a_f
     const hipStream_t st = (hipStream_t)stream;
     const char* name = "";
     if (!fast) return done(qg::launch_mx_bytes(a, a8, st, &name), name);
-    switch (mx_kind(M, N)) {
+    switch (mx_kind(M, N, a8 && out_type == QG_FP32)) {
         case MX_256x256: return done(qg::launch_mx_256x256(a, a8, st), "mx_tiled_256x256");
         case MX_128x128: return done(qg::launch_mx_128x128(a, a8, st), "mx_tiled_128x128");
         case MX_64x128: return done(qg::launch_mx_64x128(a, a8, st), "mx_tiled_64x128");

@@ -194,7 +194,7 @@ def test_every_tile(M, N, K, tile, fmt):
 @pytest.mark.parametrize("M,N,K,kernel", [
     (1, 512, 512, "mx_decode"), (8, 512, 544, "mx_decode"), (9, 512, 544, "mx_tiled_32x32"), (16, 8192, 64, "mx_tiled_32x32"), (17, 512, 512, "mx_tiled_32x32"),
     (64, 8192, 256, "mx_tiled_64x32"), (128, 8192, 256, "mx_tiled_64x64"), (512, 4096, 256, "mx_tiled_64x128"),
-    (2048, 2048, 512, "mx_tiled_128x128"), (1300, 6000, 96, "mx_tiled_128x128"), (4096, 4096, 256, "mx_tiled_256x256")])
+    (2048, 2048, 512, "mx_tiled_128x128"), (1024, 6000, 96, "mx_tiled_128x128"), (1300, 6000, 96, "mx_tiled_256x256"), (2049, 8192, 96, "mx_tiled_128x128"), (4096, 4096, 256, "mx_tiled_256x256")])
 def test_kernel_choice(M, N, K, kernel):
     case(f"mx_matmul kernel for {M}x{N}x{K}")
     check(M, N, K, "mxfp4", torch.bfloat16, True)
