@@ -43,11 +43,12 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 //  * AGAIN, wider rows, where dw alone takes 32 or 64 registers: a row is read
 //    once for its sum and again, from the caches, for its results.
 enum { AHEAD, HOLD, AGAIN };
+constexpr int FEW = 256, MANY = 512;   // lanes of a workgroup that has several rows in hand
 
 template <typename T, int G, int ITER, bool WF32, bool TINY, bool NT>
-__global__ __launch_bounds__(G < 256 ? 256 : G, (G < 512 ? 1 : G == 768 && sizeof(T) == 2 ? 3 : 4)) void rms_norm_grad_kernel(RmsNormGradArgs a) {
+__global__ __launch_bounds__(G < 256 ? (ITER == 1 ? MANY : FEW) : G, (G < 256 && ITER == 1 ? 4 : G < 512 ? 1 : G == 768 && sizeof(T) == 2 ? 3 : 4)) void rms_norm_grad_kernel(RmsNormGradArgs a) {
     typedef typename std::conditional<WF32, float, T>::type W;
-    constexpr int RPW = G < 256 ? 256 / G : 1;
+    constexpr int RPW = G < 256 ? (ITER == 1 ? MANY : FEW) / G : 1;   // rows in hand, at most
     constexpr int MODE = G < 512 || (G == 768 && sizeof(T) == 2) ? AHEAD : ITER <= (sizeof(T) == 2 ? 4 : 2) ? HOLD : AGAIN;
     constexpr bool WEIGHTS = ITER <= 2;   // in registers; else read again where they are used
     constexpr int WI = MODE == AGAIN ? 1 : ITER, BUFS = MODE == AHEAD ? 2 : 1;
@@ -64,7 +65,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G, (G < 512 ? 1 : G == 768 && sizeo
     }
     Pack8<T> yv[BUFS][WI], hv[BUFS][WI], sv[BUFS][WI] = {};
     float rv[BUFS];
-    const int step = (int)gridDim.x * RPW, M = (int)a.M;   // M + step < 2^31
+    const int rpw = RPW > 1 ? (int)blockDim.x / G : 1, step = (int)gridDim.x * rpw, M = (int)a.M;   // M + step < 2^31
     auto fetch = [&](int row, int i, int buf, int at, bool also) {
         const int c = (i * G + t) * 8;
         load8<TINY, NT && MODE != AGAIN>(reinterpret_cast<const T*>(a.dy) + (int64_t)row * a.ldy, c, n, yv[buf][at]);
@@ -130,7 +131,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G, (G < 512 ? 1 : G == 768 && sizeo
             __builtin_amdgcn_sched_barrier(0);
         }
     };
-    int row = (int)blockIdx.x * RPW + sub;
+    int row = (int)blockIdx.x * rpw + sub;
     if constexpr (MODE == AHEAD) {
         if (row < M) fetch_row(row, 0);
         while (row < M) {
@@ -157,8 +158,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G, (G < 512 ? 1 : G == 768 && sizeo
         }
         __syncthreads();
         if (sub > 0) return;
-#pragma unroll
-        for (int q = 0; q < RPW - 1; ++q)
+        for (int q = 0; q < rpw - 1; ++q)
 #pragma unroll
             for (int i = 0; i < ITER; ++i)
 #pragma unroll
@@ -196,8 +196,23 @@ __global__ __launch_bounds__(32 * SUM_ROWS) void rms_norm_grad_sum(const float* 
     if (q == 0 && c < n) dw[c] = (W)(s + red[1][cl] + red[2][cl] + red[3][cl]);
 }
 
-// Rows that a workgroup has in hand at once: as the kernel table below.
-int rows_per_group(int64_t n) { return n <= 128 ? 16 : n <= 256 ? 8 : n <= 1024 ? 4 : 1; }
+// Lanes that share a row of up to 1024 columns: as the kernel table below.
+int lanes_of(int64_t n) { return n <= 128 ? 16 : n <= 256 ? 32 : 64; }
+
+// Workgroups of the row kernel, each with one partial row of dw: at most two per compute
+// unit, or one for wide rows (2000 x 16384: the partial rows of 512 workgroups are a
+// quarter of what the gradient itself moves).
+int most_parts(int64_t n) { return n > 8192 ? 256 : 512; }
+
+// Rows that a workgroup has in hand at once.  Up to 512 columns its lanes follow from
+// them: eight waves where four would take a second turn (12334 x 478 fp16 14.5 us, four
+// 17.5; 7623 x 369 bf16 12.3, 14.7; 60000 x 64 16.7, 20); up to 1024, whose lanes hold
+// twice as much, eight are slower (16384 x 1024 bf16 29.7, four 27.1).
+int rows_per_group(int64_t M, int64_t n) {
+    if (n > 1024) return 1;
+    const int few = FEW / lanes_of(n);
+    return n > 512 || M <= (int64_t)few * most_parts(n) ? few : MANY / lanes_of(n);
+}
 
 template <typename T, bool WF32>
 hipError_t by_width(const RmsNormGradArgs& a, hipStream_t s) {
@@ -206,7 +221,7 @@ hipError_t by_width(const RmsNormGradArgs& a, hipStream_t s) {
 #define QG_GRAD(G, ITER, LIMIT, TINY, NT)                                                                      \
     if (!done && a.n <= LIMIT) {                                                                               \
         hipLaunchKernelGGL((rms_norm_grad_kernel<T, G, ITER, WF32, TINY, NT>), dim3((unsigned)a.parts),        \
-                           dim3(G < 256 ? 256 : G), 0, s, a);                                                  \
+                           dim3(G < 256 ? rows_per_group(a.M, a.n) * G : G), 0, s, a);                                                  \
         done = true;                                                                                           \
     }
     QG_GRAD(16, 1, 7, true, false)
@@ -237,12 +252,10 @@ hipError_t by_width(const RmsNormGradArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// Workgroups of the row kernel, each with one partial row of dw, none without
-// rows: two per compute unit, or one for wide rows (2000 x 16384: the
-// partial rows of 512 workgroups are a quarter of what the gradient itself moves).
+// Workgroups of the row kernel, none without rows.
 int rms_norm_grad_parts(int64_t M, int64_t n) {
-    const int64_t groups = (M + rows_per_group(n) - 1) / rows_per_group(n), most = n > 8192 ? 256 : 512;
-    return (int)(groups < most ? groups : most);
+    const int64_t rows = rows_per_group(M, n), groups = (M + rows - 1) / rows;
+    return (int)(groups < most_parts(n) ? groups : most_parts(n));
 }
 
 hipError_t launch_rms_norm_grad(const RmsNormGradArgs& a, qg_dtype type, bool weight_f32, hipStream_t s,

@@ -174,6 +174,12 @@ def test_grad(rows, n, dtype):
         assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
 
 
+@pytest.mark.parametrize("rows,n", [(8193, 100), (4100, 200), (2049, 300), (5000, 511), (2049, 512), (2049, 513)])
+def test_grad_of_many_short_rows(rows, n):
+    # more rows than the workgroups have in hand at once; the bounds of test_grad
+    test_grad(rows, n, torch.bfloat16)
+
+
 def test_grad_without_rows_and_strided():
     case("rms_norm_grad no rows, strides")
     d = dev()
