@@ -42,6 +42,13 @@ def test_quantize_and_back(rows, n, dtype, fmt):
     assert same(q.mx_dequantize(codes, scale, torch.float32), torch.from_numpy(v))
 
 
+# rows of one group of eight, and of about as many as a workgroup moves (1024)
+@pytest.mark.parametrize("rows,n", [(5000, 3), (2100, 9), (1030, 17), (900, 33), (11, 8160), (11, 8184), (11, 8192), (11, 8200), (9, 8225), (5, 16385), (3, 40000)])
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_rows_between_workgroups(rows, n, fmt):
+    test_quantize_and_back(rows, n, torch.bfloat16, fmt)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_every_rounding_border(fmt):
     """Each value, each midpoint and both its neighbours, under three scales."""
