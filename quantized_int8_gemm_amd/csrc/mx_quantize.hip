@@ -123,8 +123,8 @@ hipError_t run(const MxCodecArgs& a, bool back, hipStream_t s) {
         hipLaunchKernelGGL((mx_dequantize_kernel<T, FP4>), dim3((unsigned)blocks), dim3(NT), 0, s, a, (uint32_t)gpr, part, groups);
     else if (a.n < 8)
         hipLaunchKernelGGL((mx_quantize_kernel<T, FP4, true, false>), dim3((unsigned)blocks), dim3(NT), 0, s, a, (uint32_t)gpr, part, groups);
-    else if (whole_lines(a.x, a.ldx * sizeof(T)))
-        hipLaunchKernelGGL((mx_quantize_kernel<T, FP4, false, true>), dim3((unsigned)blocks), dim3(NT), 0, s, a, (uint32_t)gpr, part, groups);
+    else if (sizeof(T) == 2 && whole_lines(a.x, a.ldx * sizeof(T)))
+        hipLaunchKernelGGL((mx_quantize_kernel<T, FP4, false, sizeof(T) == 2>), dim3((unsigned)blocks), dim3(NT), 0, s, a, (uint32_t)gpr, part, groups);
     else
         hipLaunchKernelGGL((mx_quantize_kernel<T, FP4, false, false>), dim3((unsigned)blocks), dim3(NT), 0, s, a, (uint32_t)gpr, part, groups);
     return hipGetLastError();

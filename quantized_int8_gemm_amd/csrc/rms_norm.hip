@@ -11,10 +11,15 @@
 // Bound by HBM: every value is read once and kept in registers (at most 64 a
 // lane), one barrier per row.  A row is shared by G lanes: 16 up to 128 columns,
 // 32 up to 256, a wave up to 1024 (16, 8 and 4 rows per workgroup), 256 lanes up to
-// 8192, 512 up to 16384, 1024 beyond.
-// 8192 x 8192 bf16 with a residual to int8: 73.6 us, 6.4 TB/s over what is read
-// and written (a copy of 2 GiB runs at 4.85); one row 3.7 us, the launch's and one
-// load's latency.
+// 8192, 512 up to 16384, 1024 beyond.  Up to 512 rows leave CUs without work, so the
+// lanes of each take as little of it as they can: 512 up to 4096 columns, 1024 beyond
+// (to int8, bf16: 1 x 8192 4.5 -> 3.7 us, 16 x 5000 5.2 -> 4.0, 256 x 4096 5.0 -> 4.6;
+// 768 x 5000 8.5 -> 9.5, 1024 x 8192 13.0 -> 13.8).  Lanes that have nothing of a row
+// cost as much as those that have: 8192 x 5120 bf16 54.9 us with the four groups a lane
+// that 8192 columns take, 49.5 with three.
+// 8192 x 8192 bf16 with a residual to int8: 73.9 us, 6.4 TB/s over what is read
+// and written (a copy of 2 GiB runs at 4.85); one row of 4096 3.2 us, the launch's and
+// one load's latency.
 #include "mx_common.h"
 
 namespace qg {
@@ -167,12 +172,21 @@ hipError_t by_width(const RmsNormArgs& a, hipStream_t s) {
     QG_NORM(64, 1, 512, false, false)
     QG_NORM(64, 2, 1024, false, false)
     QG_NORM(256, 1, 2048, false, false)
-    if (whole_lines(a.x, a.ldx * sizeof(T)) && (a.res == nullptr || whole_lines(a.res, a.ldr * sizeof(T)))) {
-        QG_NORM(256, 2, 4096, false, true)
-        QG_NORM(256, 4, 8192, false, true)
-        QG_NORM(512, 4, 16384, false, true)
+    if (a.M <= 512) {
+        if (a.n > 2048) QG_NORM(512, 1, 4096, false, false)
+        if (a.n > (a.M <= 256 ? 4096 : 6144)) QG_NORM(1024, 1, 8192, false, false)
+        if (a.n > 8192) QG_NORM(1024, 2, 16384, false, false)
+    }
+    if constexpr (sizeof(T) == 2) {
+        if (whole_lines(a.x, a.ldx * sizeof(T)) && (a.res == nullptr || whole_lines(a.res, a.ldr * sizeof(T)))) {
+            QG_NORM(256, 2, 4096, false, true)
+            QG_NORM(256, 3, 6144, false, true)
+            QG_NORM(256, 4, 8192, false, true)
+            QG_NORM(512, 4, 16384, false, true)
+        }
     }
     QG_NORM(256, 2, 4096, false, false)
+    QG_NORM(256, 3, 6144, false, false)
     QG_NORM(256, 4, 8192, false, false)
     QG_NORM(512, 4, 16384, false, false)
     QG_NORM(1024, 4, 32768, false, false)

@@ -201,8 +201,10 @@ int lanes_of(int64_t n) { return n <= 128 ? 16 : n <= 256 ? 32 : 64; }
 
 // Workgroups of the row kernel, each with one partial row of dw: at most two per compute
 // unit, or one for wide rows (2000 x 16384: the partial rows of 512 workgroups are a
-// quarter of what the gradient itself moves).
-int most_parts(int64_t n) { return n > 8192 ? 256 : 512; }
+// quarter of what the gradient itself moves) and for few rows of more than a wave's
+// width (512 x 4096 bf16 10.6 us, one workgroup a row 12.2; 512 x 8192 13.5, 17.1; 768 x
+// 4096 12.7, 13.6; but 1024 x 1368 12.5, 11.3).
+int most_parts(int64_t M, int64_t n) { return n > 8192 || (n > 1024 && M <= 768) ? 256 : 512; }
 
 // Rows that a workgroup has in hand at once.  Up to 512 columns its lanes follow from
 // them: eight waves where four would take a second turn (12334 x 478 fp16 14.5 us, four
@@ -211,7 +213,7 @@ int most_parts(int64_t n) { return n > 8192 ? 256 : 512; }
 int rows_per_group(int64_t M, int64_t n) {
     if (n > 1024) return 1;
     const int few = FEW / lanes_of(n);
-    return n > 512 || M <= (int64_t)few * most_parts(n) ? few : MANY / lanes_of(n);
+    return n > 512 || M <= (int64_t)few * most_parts(M, n) ? few : MANY / lanes_of(n);
 }
 
 template <typename T, bool WF32>
@@ -230,12 +232,20 @@ hipError_t by_width(const RmsNormGradArgs& a, hipStream_t s) {
     QG_GRAD(64, 1, 512, false, false)
     QG_GRAD(64, 2, 1024, false, false)
     QG_GRAD(256, 1, 2048, false, false)
-    if (whole_lines(a.dy, a.ldy * sizeof(T)) && whole_lines(a.h, a.ldh * sizeof(T)) &&
-        (a.dh == nullptr || whole_lines(a.dh, a.lddh * sizeof(T)))) {
-        QG_GRAD(256, 2, 4096, false, true)
-        QG_GRAD(512, 2, 8192, false, true)
-        QG_GRAD(768, 2, 12288, false, true)
-        QG_GRAD(1024, 2, 16384, false, true)
+    // a row or two a workgroup: as many lanes as take it in one piece (512 x 4096 bf16
+    // 12.2 us, 256 lanes 13.0; 16 x 8192 fp32 7.2, 512 lanes 8.0)
+    if (a.M <= 512) {
+        if (a.n > 2048) QG_GRAD(512, 1, 4096, false, false)
+        if (a.n > 4096) QG_GRAD(1024, 1, 8192, false, false)
+    }
+    if constexpr (sizeof(T) == 2) {
+        if (whole_lines(a.dy, a.ldy * sizeof(T)) && whole_lines(a.h, a.ldh * sizeof(T)) &&
+            (a.dh == nullptr || whole_lines(a.dh, a.lddh * sizeof(T)))) {
+            QG_GRAD(256, 2, 4096, false, true)
+            QG_GRAD(512, 2, 8192, false, true)
+            QG_GRAD(768, 2, 12288, false, true)
+            QG_GRAD(1024, 2, 16384, false, true)
+        }
     }
     QG_GRAD(256, 2, 4096, false, false)
     QG_GRAD(512, 2, 8192, false, false)
@@ -255,7 +265,7 @@ hipError_t by_width(const RmsNormGradArgs& a, hipStream_t s) {
 // Workgroups of the row kernel, none without rows.
 int rms_norm_grad_parts(int64_t M, int64_t n) {
     const int64_t rows = rows_per_group(M, n), groups = (M + rows - 1) / rows;
-    return (int)(groups < most_parts(n) ? groups : most_parts(n));
+    return (int)(groups < most_parts(M, n) ? groups : most_parts(M, n));
 }
 
 hipError_t launch_rms_norm_grad(const RmsNormGradArgs& a, qg_dtype type, bool weight_f32, hipStream_t s,

@@ -174,8 +174,20 @@ def test_grad(rows, n, dtype):
         assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
 
 
-@pytest.mark.parametrize("rows,n", [(8193, 100), (4100, 200), (2049, 300), (5000, 511), (2049, 512), (2049, 513)])
-def test_grad_of_many_short_rows(rows, n):
+@pytest.mark.parametrize("rows,n", [(513, 2049), (513, 4095), (260, 4100), (600, 6144), (600, 6145), (600, 8192), (513, 8200), (513, 12290)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_norm_of_few_and_many_rows(rows, n, dtype):
+    # the lanes of a row depend on how many rows there are; a row's codes and scale do not
+    case(f"rms_norm_quantize {rows}x{n} {dtype} whole and in parts")
+    x, w, res = up(*make(rows, n, dtype, n))
+    whole = q.rms_norm_quantize(x, w, 1e-6, residual=res)
+    part = [torch.cat(t) for t in zip(*[q.rms_norm_quantize(x[i:i + 250], w, 1e-6, residual=res[i:i + 250]) for i in range(0, rows, 250)])]
+    assert torch.equal(whole[0], part[0]) and torch.equal(whole[2], part[2])
+    assert torch.allclose(whole[1], part[1], rtol=2 * R_STEPS * U, atol=0)
+
+
+@pytest.mark.parametrize("rows,n", [(8193, 100), (4100, 200), (2049, 300), (5000, 511), (2049, 512), (2049, 513), (513, 4090), (300, 5000), (600, 8192), (769, 2050)])
+def test_grad_of_many_rows(rows, n):
     # more rows than the workgroups have in hand at once; the bounds of test_grad
     test_grad(rows, n, torch.bfloat16)
 

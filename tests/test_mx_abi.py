@@ -74,6 +74,7 @@ def test_grad_workspace():
     assert b.lib.rms_norm_grad_workspace_bytes(4, 40) == 160          # one workgroup of four rows
     assert b.lib.rms_norm_grad_workspace_bytes(8192, 4096) == 512 * 4096 * 4
     assert b.lib.rms_norm_grad_workspace_bytes(2049, 400) == 257 * 400 * 4   # eight rows each
+    assert b.lib.rms_norm_grad_workspace_bytes(768, 4096) == 256 * 4096 * 4
     assert b.lib.rms_norm_grad_workspace_bytes(0, 40) == 0
     assert b.lib.rms_norm_grad_workspace_bytes(4, 65537) == 0
 
