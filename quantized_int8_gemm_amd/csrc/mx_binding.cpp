@@ -2,9 +2,9 @@
 // torch's C++ tensors.  It checks dtypes (TypeError) and shapes (ValueError),
 // allocates the outputs and calls the C entry point on the tensors' device and
 // torch's current stream there; it computes nothing.  The smallest of these calls
-// take 4 us on the GPU, and the same marshalling through ctypes took 6 to 9 us of a
-// call, so it is done here: norm to int8 of one row 14.2 -> 6.5 us a call, gradient
-// of 1000 x 1000 15.1 -> 9.1, MXFP8 quantiser 16 x 8192 9.0 -> 5.5 (the launch itself
+// take 3 us on the GPU, and the same marshalling through ctypes took 6 to 9 us of a
+// call, so it is done here: norm to int8 of one row 14.2 -> 5.1 us a call, gradient
+// of 1000 x 1000 15.1 -> 9.7, MXFP8 quantiser 16 x 8192 9.0 -> 4.8 (the launch itself
 // takes about 2.8).
 #include <string>
 

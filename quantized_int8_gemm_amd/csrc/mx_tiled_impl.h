@@ -28,7 +28,7 @@
 //    tiles need it: with one wave a SIMD every step waits for its fragments.
 //  * The finished wave tile goes through LDS, 32 rows and 64 columns at a time, and
 //    leaves in whole rows of those.
-// What bounds 8192^3 MXFP4 (259 us, 4.2 PFLOP/s): the instruction alone on register
+// What bounds 8192^3 MXFP4 (262 us, 4.2 PFLOP/s): the instruction alone on register
 // operands runs at 7.1 PFLOP/s on random data, the clock falling from 2.4 to 1.7 GHz
 // (9.7 PFLOP/s on zeros), and on this product's fragments at 5.9; the kernel keeps
 // the matrix cores busy 53 % of the cycles at 1.8 GHz.  Taken at 276 us, it ran 223 us
