@@ -144,12 +144,11 @@ qg_status mx_dequantize(int64_t M, int64_t n,
  * readable to the end of the 4-byte word that holds their last byte take the
  * fast kernels; `scale_rows_padded` says that they are readable so, the last
  * row's too.  All others run a slower kernel that reads bytes.
- * Accuracy: e2m1 products are exact and summed in fp32.  With e4m3
- * activations the matrix cores add groups of 16 products k with what lies
- * 2^-14 below the largest of them cut off, an error of about 1e-5 of the
- * result's size on usual data, far below a 16-bit output's rounding; for an
- * fp32 output the activations are split in two by magnitude so that nothing
- * is cut off.  Sums are added in a fixed order: results repeat bit for bit.
+ * Accuracy: every product is exact, and sums are fp32, whatever the output's
+ * type.  (With e4m3 activations the matrix cores would cut off what lies 2^-14
+ * below the largest of 16 products; the activations are split in two by
+ * magnitude and multiplied twice, so that nothing is.)  Sums are added in a
+ * fixed order: results repeat bit for bit.
  * An element whose block scale is 255 gives NaN.
  * QG_ERR_UNSUPPORTED if 512 rows of an operand span 2^31 bytes, or the output
  * has 2^23 or more tiles of 256 x 256.

@@ -106,7 +106,8 @@ def mx_matmul(A, a_scale, W, w_scale, act_scale=None, out_dtype=torch.float32, o
     A: float8_e4m3fn [M, K] or packed e2m1 uint8 [M, K/2] with a_scale uint8
     [M, K/32]; W: packed e2m1 uint8 [N, K/2] with w_scale uint8 [N, K/32] (both
     as mx_quantize returns them); act_scale: fp32 [M], [M, 1], a scalar, or
-    None for 1.  out_dtype: torch.float32, bfloat16 or float16.  Fast kernels
+    None for 1.  out_dtype: torch.float32, bfloat16 or float16, rounded once from
+    fp32 sums of exact products.  Fast kernels
     need code rows at multiples of 16 bytes and scale rows at multiples of 4,
     as mx_quantize and rms_norm_quantize lay them out; other layouts run a
     slower one."""

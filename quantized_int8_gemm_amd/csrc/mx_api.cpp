@@ -40,7 +40,7 @@ int env_int(const char* name, int dflt) {
 // Kernels of the MX product.
 enum MxKind { MX_256x256, MX_128x128, MX_64x128, MX_64x64, MX_64x32, MX_32x32, MX_DECODE };
 
-// split: the activations' codes are split in two, so every tile multiplies twice.
+// split: MXFP8 activations, whose codes are split in two, so every tile multiplies twice.
 MxKind mx_kind(int64_t M, int64_t N, bool split) {
     const int forced = env_int("QGEMM_MX_TILE", -1);
     if (forced >= 0 && forced <= MX_DECODE && (forced != MX_DECODE || M <= qg::MX_DECODE_MAX_M)) return (MxKind)forced;
@@ -192,7 +192,7 @@ qg_status mx_matmul(int64_t M, int64_t N, int64_t K, const void* A, qg_dtype a_f
     const hipStream_t st = (hipStream_t)stream;
     const char* name = "";
     if (!fast) return done(qg::launch_mx_bytes(a, a8, st, &name), name);
-    switch (mx_kind(M, N, a8 && out_type == QG_FP32)) {
+    switch (mx_kind(M, N, a8)) {
         case MX_256x256: return done(qg::launch_mx_256x256(a, a8, st), "mx_tiled_256x256");
         case MX_128x128: return done(qg::launch_mx_128x128(a, a8, st), "mx_tiled_128x128");
         case MX_64x128: return done(qg::launch_mx_64x128(a, a8, st), "mx_tiled_64x128");

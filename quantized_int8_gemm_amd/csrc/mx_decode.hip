@@ -4,7 +4,7 @@
 // A workgroup of eight waves owns 16 output columns over all of K.  The waves
 // take chunks of 512 values of K in turn, straight from memory to registers:
 // per 128 values one 16-byte load of W and one (e2m1) or two (e4m3) of A per
-// lane, and one 16x16x128 matrix instruction; two chunks' loads are in flight at
+// lane, and one 16x16x128 matrix instruction or two; two chunks' loads are in flight at
 // once.  Scale bytes come four words at a time, and a lane shifts the byte of its
 // block into place.  The waves' partial tiles are added through LDS in a fixed
 // order.  Bound by latency: 1 x 2048 x 8192 7.1 us, where 32 x 32 tiles take 8.5 (64
@@ -22,7 +22,6 @@ constexpr uint32_t OUTSIDE = 0xffffff00u;   // past every window
 // scale words come in one load.
 template <bool A8, bool S16, typename T>
 __global__ __launch_bounds__(NW * 64) void mx_decode_kernel(MxMatmulArgs p) {
-    constexpr bool EXACT = A8 && sizeof(T) == 4;
     constexpr int AV = A8 ? 2 : 1, ABLK = A8 ? 32 : 16;
     __shared__ float part[NW][4][64];
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -89,7 +88,7 @@ __global__ __launch_bounds__(NW * 64) void mx_decode_kernel(MxMatmulArgs p) {
                 // scale bytes past K may be anything: 0 times the zero codes there
                 const bool live = S16 || chunk * 16 + 4 * q + g < nblk;
                 const uint32_t sw = live ? ws[u][q] >> (8 * g) : 0u, sa = live ? as[u][q] >> (8 * g) : 0u;
-                acc = mfma_mx16<A8, EXACT>(words4(w[u][q]), sw, A8 ? words8(a[u][q][0], a[u][q][AV - 1]) : words4(a[u][q][0]), sa, acc);
+                acc = mfma_mx16<A8>(words4(w[u][q]), sw, A8 ? words8(a[u][q][0], a[u][q][AV - 1]) : words4(a[u][q][0]), sa, acc);
             }
         }
     }

@@ -15,7 +15,7 @@ __device__ __forceinline__ u32x4 load16_if(const uint8_t* p, bool ok) {
     return r;
 }
 
-template <bool A8, bool EXACT, typename T>
+template <bool A8, typename T>
 __global__ __launch_bounds__(256) void mx_matmul_bytes_kernel(MxMatmulArgs p) {
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int r = lane & 15, g = lane >> 4;
@@ -40,7 +40,7 @@ __global__ __launch_bounds__(256) void mx_matmul_bytes_kernel(MxMatmulArgs p) {
         } else {
             a = words4(load16_if(A + b * 16, m_ok && k_ok));
         }
-        acc = mfma_mx16<A8, EXACT>(w, sw, a, sa, acc);
+        acc = mfma_mx16<A8>(w, sw, a, sa, acc);
     }
     if (!m_ok) return;
     const float s = p.act_scale != nullptr ? p.act_scale[m] : 1.0f;
@@ -54,11 +54,11 @@ template <bool A8>
 hipError_t by_out(const MxMatmulArgs& p, hipStream_t s) {
     const dim3 grid((unsigned)((p.N + 63) / 64), (unsigned)((p.M + 15) / 16));
     if (p.out_type == QG_FP32)
-        hipLaunchKernelGGL((mx_matmul_bytes_kernel<A8, true, float>), grid, dim3(256), 0, s, p);
+        hipLaunchKernelGGL((mx_matmul_bytes_kernel<A8, float>), grid, dim3(256), 0, s, p);
     else if (p.out_type == QG_BF16)
-        hipLaunchKernelGGL((mx_matmul_bytes_kernel<A8, false, __bf16>), grid, dim3(256), 0, s, p);
+        hipLaunchKernelGGL((mx_matmul_bytes_kernel<A8, __bf16>), grid, dim3(256), 0, s, p);
     else
-        hipLaunchKernelGGL((mx_matmul_bytes_kernel<A8, false, _Float16>), grid, dim3(256), 0, s, p);
+        hipLaunchKernelGGL((mx_matmul_bytes_kernel<A8, _Float16>), grid, dim3(256), 0, s, p);
     return hipGetLastError();
 }
 

@@ -93,13 +93,13 @@ __device__ __forceinline__ int slot(int r, int s) {
     else return s ^ (r & 15);
 }
 
-template <bool A8, bool EXACT>
+template <bool A8>
 __device__ __forceinline__ v16f mfma_step(int s, v8i w, uint32_t ws, v8i a, uint32_t as, v16f c) {
     switch (s) {   // the byte is an immediate; s is a constant of the unrolled loop
-        case 0: return mfma_mx32<A8, EXACT, 0, 0>(w, ws, a, as, c);
-        case 1: return mfma_mx32<A8, EXACT, 1, 1>(w, ws, a, as, c);
-        case 2: return mfma_mx32<A8, EXACT, 2, 2>(w, ws, a, as, c);
-        default: return mfma_mx32<A8, EXACT, 3, 3>(w, ws, a, as, c);
+        case 0: return mfma_mx32<A8, 0, 0>(w, ws, a, as, c);
+        case 1: return mfma_mx32<A8, 1, 1>(w, ws, a, as, c);
+        case 2: return mfma_mx32<A8, 2, 2>(w, ws, a, as, c);
+        default: return mfma_mx32<A8, 3, 3>(w, ws, a, as, c);
     }
 }
 
@@ -115,7 +115,6 @@ __device__ __forceinline__ uint32_t scalar(uint32_t v) {
 
 template <int BM, int BN, int WM, int WN, int KW, int NB, int STAGES, bool A8, typename T>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * KW * 64) void mx_tiled_kernel(MxMatmulArgs p) {
-    constexpr bool EXACT = A8 && sizeof(T) == 4;
     constexpr int NT = (BM / WM) * (BN / WN) * KW * 64, NW = NT / 64 / KW, WAVES_N = BN / WN;
     constexpr int FM = WM / 32, FN = WN / 32, NS = NB / 2, SPW = NS / KW;   // steps of a stage, of a wave
     constexpr int AW = NB * (A8 ? 32 : 16), WW = NB * 16;         // bytes of a stage's code rows
@@ -311,7 +310,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * KW * 64) void mx_tiled_kern
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int b = 0; b < FN; ++b)
-                acc[a][b] = mfma_step<A8, EXACT>(s, words4(wf[cur][b]), ws[b], A8 ? words8(af[cur][a][0], af[cur][a][AV - 1]) : words4(af[cur][a][0]),
+                acc[a][b] = mfma_step<A8>(s, words4(wf[cur][b]), ws[b], A8 ? words8(af[cur][a][0], af[cur][a][AV - 1]) : words4(af[cur][a][0]),
                                                  as[a], acc[a][b]);
         }
     };
@@ -438,15 +437,10 @@ hipError_t launch_one(const MxMatmulArgs& a, hipStream_t s) {
 }
 
 template <int BM, int BN, int WM, int WN, int KW, int NB, int STAGES, bool A8>
-hipError_t launch_half(const MxMatmulArgs& a, hipStream_t s) {
-    if (a.out_type == QG_BF16) return launch_one<BM, BN, WM, WN, KW, NB, STAGES, A8, __bf16>(a, s);
-    return launch_one<BM, BN, WM, WN, KW, NB, STAGES, A8, _Float16>(a, s);
-}
-
-template <int BM, int BN, int WM, int WN, int KW, int NB, int STAGES, bool A8>
 hipError_t launch_out(const MxMatmulArgs& a, hipStream_t s) {
     if (a.out_type == QG_FP32) return launch_one<BM, BN, WM, WN, KW, NB, STAGES, A8, float>(a, s);
-    return launch_half<BM, BN, WM, WN, KW, NB, STAGES, A8>(a, s);
+    if (a.out_type == QG_BF16) return launch_one<BM, BN, WM, WN, KW, NB, STAGES, A8, __bf16>(a, s);
+    return launch_one<BM, BN, WM, WN, KW, NB, STAGES, A8, _Float16>(a, s);
 }
 
 }  // namespace mx
