@@ -283,11 +283,11 @@ __global__ __launch_bounds__(CI_NT) void conv_implicit_kernel(ConvImplicitArgs p
 
     // operand windows: this group's packed weights, this tile's part of xp
     const int8_t* wbase = p.wp + (int64_t)g * c.Mg * p.kt;
-    const v4i w_rsrc = dma::rsrc_words(wbase, (uint32_t)((int64_t)c.Mg * p.kt));
+    const v4i w_rsrc = rsrc_words(wbase, (uint32_t)((int64_t)c.Mg * p.kt));
     const int64_t img = (int64_t)p.hp_rows * p.wp_cols * p.cgp;
     const int64_t tile_off = ((int64_t)oh0 * c.sh * p.wp_cols + (int64_t)ow0 * c.sw) * p.cgp;
     const int8_t* xbase = p.xp + (int64_t)ng * img + tile_off;
-    const v4i x_rsrc = dma::rsrc_words(xbase, (uint32_t)(img - tile_off));
+    const v4i x_rsrc = rsrc_words(xbase, (uint32_t)(img - tile_off));
 
     // Position wn*WNP + 16b + i16 of the tile sits at halo row rr[b], column
     // cc[b] for tap (0, 0).
@@ -443,7 +443,7 @@ __global__ __launch_bounds__(CI_NT) void conv_implicit_kernel(ConvImplicitArgs p
                         const int tp = as >> 2, j = (as & 3) ^ ((ar >> 2) & 3);
                         off = (uint32_t)((int64_t)(m0 + ar) * p.kt + kblk + 64 * tp + 16 * j);
                     }
-                    dma::dma16(w_rsrc, off, lds0 + (uint32_t)(q * CI_NT + wave * 64) * 16u);
+                    dma16(w_rsrc, off, lds0 + (uint32_t)(q * CI_NT + wave * 64) * 16u);
                     as += p.a_dr; ar += p.a_dq;
                     if (as >= a_upr) { as -= a_upr; ++ar; }
                 }
@@ -454,13 +454,13 @@ __global__ __launch_bounds__(CI_NT) void conv_implicit_kernel(ConvImplicitArgs p
                     uint32_t off = OUT;
                     if (hr_ < p.hr)
                         off = (uint32_t)(((int64_t)hr_ * p.wp_cols + hc_) * p.cgp + blk * 64 + 16 * halo_slot(hc_, h_slot));
-                    dma::dma16(x_rsrc, off, lds_h + (uint32_t)(q * CI_NT + wave * 64) * 16u);
+                    dma16(x_rsrc, off, lds_h + (uint32_t)(q * CI_NT + wave * 64) * 16u);
                     hc_ += p.h_dr; hr_ += p.h_dq;
                     if (hc_ >= p.hc) { hc_ -= p.hc; ++hr_; }
                 }
             }
         }
-        dma::wait_vmcnt<0>();
+        wait_vmcnt<0>();
         __syncthreads();
 
         const uint8_t* A = smem;

@@ -48,41 +48,6 @@ constexpr int EPI_F32_ACC = 3, EPI_BF16_ACC = 4;
 
 typedef int v2i __attribute__((ext_vector_type(2)));
 
-// Buffer descriptor words for [base, base + bytes); loads past the end give 0.
-__device__ __forceinline__ v4i rsrc_words(const void* base, uint32_t bytes) {
-    const uint64_t a = reinterpret_cast<uint64_t>(base);
-    v4i r;
-    r.x = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
-    r.y = __builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xffffu));
-    r.z = __builtin_amdgcn_readfirstlane((int)bytes);
-    r.w = 0x00020000;
-    return r;
-}
-
-// 16 bytes per lane from buffer offset `voff` into LDS at lds_base + 16*lane.
-// Written as inline assembly so that the compiler does not wait for these
-// loads before every LDS read; the kernel waits for them explicitly.  The
-// block sets M0 (the LDS destination) itself, so M0 is declared clobbered:
-// the compiler then treats it as redefined here.  M0 is a reserved register,
-// which the compiler never saves around an asm statement (hence the
-// suppressed warning); in these kernels nothing else uses M0 at all -- every
-// M0 reference in their compiled code is this block's own s_mov_b32.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void dma16(v4i rsrc, uint32_t voff, uint32_t lds_base) {
-    const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_base);  // wave-uniform
-    asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-                 :: "v"(voff), "s"(rsrc), "s"(m0) : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
-// s_waitcnt with vmcnt = n and the other counters unconstrained (gfx9 encoding).
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
-}
-
 __device__ __forceinline__ u32x4 xor4(u32x4 v, uint32_t f) {
     return u32x4{v.x ^ f, v.y ^ f, v.z ^ f, v.w ^ f};
 }

@@ -48,41 +48,6 @@ namespace mx {
 
 constexpr int GROUP_M = 4;   // tile rows walked together (8: 8192^3 MXFP4 261.3 against 258.9 us)
 
-__device__ __forceinline__ v4i rsrc_words(const void* base, uint32_t bytes) {
-    const uint64_t a = reinterpret_cast<uint64_t>(base);
-    v4i r;
-    r.x = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
-    r.y = __builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xffffu));
-    r.z = __builtin_amdgcn_readfirstlane((int)bytes);
-    r.w = 0x00020000;
-    return r;
-}
-
-// 16 (4) bytes per lane from buffer offset `voff` into LDS at lds_base + 16
-// (4) * lane.  Inline assembly, so that the compiler does not wait for these
-// loads before every LDS read; the kernel waits for them explicitly.  M0 (the
-// LDS destination) is set inside the block and declared clobbered; nothing else
-// in these kernels uses it.
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-__device__ __forceinline__ void dma16(v4i rsrc, uint32_t voff, uint32_t lds_base) {
-    const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_base);
-    asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
-                 :: "v"(voff), "s"(rsrc), "s"(m0) : "memory", "m0");
-}
-__device__ __forceinline__ void dma4(v4i rsrc, uint32_t voff, uint32_t lds_base) {
-    const uint32_t m0 = __builtin_amdgcn_readfirstlane(lds_base);
-    asm volatile("s_mov_b32 m0, %2\n\tbuffer_load_dword %0, %1, 0 offen lds"
-                 :: "v"(voff), "s"(rsrc), "s"(m0) : "memory", "m0");
-}
-#pragma clang diagnostic pop
-
-template <int N>
-__device__ __forceinline__ void wait_vmcnt() {
-    static_assert(N >= 0 && N < 64, "vmcnt range");
-    __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
-}
-
 // Slot of 16-byte segment s in a row of WIDTH bytes: the 16 rows that a
 // fragment read touches at one segment take 16 distinct 16-byte places of a
 // 256-byte span.
