@@ -1,7 +1,8 @@
 // Gradient of the root-mean-square norm.
 //
-// Mathematics: with g = dy w, dx = r g - h r^3 / n sum(g h) (+ dh) and dw =
-// sum over rows of dy h r.  Bound by HBM: dy, h (and dh) are read once.  A
+// Mathematics: with g = dy w and u = h r, the normalised row, dx = r (g - u sum(g u)
+// / n) (+ dh) and dw = sum over rows of dy u.  u is of ordinary size wherever the
+// norm is; r^3, or dy h, leaves fp32's range on rows of 10^13 or 10^-13.  Bound by HBM: dy, h (and dh) are read once.  A
 // workgroup walks rows with a fixed set of columns per lane, so dw is added up
 // in registers and leaves once, as one row of partial sums per workgroup; a
 // second kernel adds those.  No atomics: the order of every sum is fixed.
@@ -107,14 +108,14 @@ __global__ __launch_bounds__(G < 256 ? (ITER == 1 ? MANY : FEW) : G, (G < 256 &&
             if constexpr (MODE == AGAIN) fetch(row, i, buf, 0, false);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float yh = value(yv[buf][at], e) * value(hv[buf][at], e);
-                dot = __builtin_fmaf(yh, w[wi][e], dot);
-                dw[i][e] = __builtin_fmaf(yh, r, dw[i][e]);
+                const float yu = value(yv[buf][at], e) * (value(hv[buf][at], e) * r);
+                dot = __builtin_fmaf(yu, w[wi][e], dot);
+                dw[i][e] += yu;
             }
             __builtin_amdgcn_sched_barrier(0);   // one group unpacked at a time
         }
         dot = row_sum<G>(dot, red[slot]);
-        const float k = r * r * r * (dot / (float)n);
+        const float k = dot / (float)n;
         if constexpr (MODE != AGAIN) hold_packed(buf);
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
@@ -124,7 +125,7 @@ __global__ __launch_bounds__(G < 256 ? (ITER == 1 ? MANY : FEW) : G, (G < 256 &&
             float o[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                o[e] = r * (value(yv[buf][at], e) * w[wi][e]) - k * value(hv[buf][at], e);
+                o[e] = r * (value(yv[buf][at], e) * w[wi][e] - value(hv[buf][at], e) * r * k);
                 if (a.dh != nullptr) o[e] += value(sv[buf][at], e);
             }
             if (c < n) store8(reinterpret_cast<T*>(a.dx) + (int64_t)row * a.ldx, c, n, pack<T>(o));
