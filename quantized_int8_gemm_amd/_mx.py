@@ -6,7 +6,8 @@ As in the binding of the integer products, each function checks dtypes
 calls the C entry point of the same name on torch's current stream; all
 arithmetic runs in the HIP kernels.  The marshalling itself is the extension
 module _mx_binding (csrc/mx_binding.cpp), since for one token it took longer
-in Python than the kernels do; it calls libqgemm.so as ctypes loaded it.
+in Python than the kernels do; it calls libqgemm.so as ctypes loaded it.  Where
+the module is missing, each call raises ImportError.
 """
 import ctypes
 
@@ -14,11 +15,23 @@ import torch
 
 from ._binding import _check, _f32, _i64, _int, _p, _sz, lib
 
+
+class _Missing:
+    """In the extension module's place where it is not built or does not load
+    (another torch): the calls below raise, the integer products work."""
+
+    def __init__(self, why):
+        self._text = (f"quantized_int8_gemm_amd/_mx_binding.so is not built for this torch ({why}); run "
+                      "__graft_entry__.build() (python -c 'import __graft_entry__ as g; g.build()')")
+
+    def __getattr__(self, name):
+        raise ImportError(self._text)
+
+
 try:
     from . import _mx_binding
 except ImportError as e:
-    raise ImportError("quantized_int8_gemm_amd/_mx_binding.so is not built; run __graft_entry__.build() "
-                      "(python -c 'import __graft_entry__ as g; g.build()')") from e
+    _mx_binding = _Missing(e)
 
 QG_FP16, QG_MXFP8, QG_MXFP4 = 5, 6, 7
 MX_BLOCK = 32
@@ -42,7 +55,8 @@ def _bind(library):
     _mx_binding.bind(_check, *(ctypes.cast(getattr(library, name), ctypes.c_void_p).value for name in PROTOTYPES))
 
 
-_bind(lib)
+if not isinstance(_mx_binding, _Missing):
+    _bind(lib)
 
 
 def rms_norm(x, weight, eps=1e-6, residual=None, out_dtype=None, out=None, residual_out=None):
