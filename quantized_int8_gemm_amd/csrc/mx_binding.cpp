@@ -94,7 +94,8 @@ at::ScalarType dtype_arg(PyObject* o, const char* what) {
 }
 
 // A tensor seen as a matrix of its last dimension: rows, columns and row stride
-// in elements.  More than two dimensions have to lie like one matrix.
+// in elements.  More than two dimensions have to lie like one matrix; without rows
+// nothing lies anywhere.
 struct Matrix { int64_t rows, n, ld; };
 
 Matrix matrix(const Tensor& t, const char* name) {
@@ -102,6 +103,8 @@ Matrix matrix(const Tensor& t, const char* name) {
     const int64_t d = (int64_t)size.size();
     if (d == 0) value_error(std::string(name) + " must have at least one dimension");
     const int64_t n = size[d - 1];
+    for (int64_t i = 0; i < d - 1; ++i)
+        if (size[i] == 0) return {0, n, n};
     if (n > 1 && stride[d - 1] != 1) value_error(std::string(name) + " must have unit column stride");
     int64_t rows = 1, ld = -1;
     for (int64_t i = d - 2; i >= 0; --i) {
