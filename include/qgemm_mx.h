@@ -91,9 +91,11 @@ qg_status rms_norm(int64_t M, int64_t n,
  *   rstd: fp32 [M], r as rms_norm left it.
  *   weight, dweight: [n] of weight_type (`type` or QG_FP32).
  *   workspace: rms_norm_grad_workspace_bytes(M, n) bytes, 16-byte aligned,
- *     not cleared; calls that overlap in time must not share one.
- * Sums are fp32 in a fixed order: results repeat bit for bit.  M == 0 writes
- * dweight = 0.
+ *     not cleared; calls that overlap in time must not share one.  What a
+ *     larger M, n or both asks for is enough as well, though it may be less:
+ *     the call then runs on fewer workgroups.
+ * Sums are fp32 in a fixed order, which depends on the sizes and the workspace's
+ * alone: results repeat bit for bit.  M == 0 writes dweight = 0.
  */
 size_t rms_norm_grad_workspace_bytes(int64_t M, int64_t n);
 qg_status rms_norm_grad(int64_t M, int64_t n,

@@ -122,11 +122,18 @@ qg_status rms_norm_grad(int64_t M, int64_t n, const void* dy, qg_dtype type, int
             !aligned_for(weight, weight_type) || !aligned(rstd, 4))
             return QG_ERR_INVALID_ARGUMENT;
         if (workspace == nullptr || !aligned(workspace, 16)) return QG_ERR_INVALID_ARGUMENT;
-        if (workspace_bytes < rms_norm_grad_workspace_bytes(M, n)) return QG_ERR_WORKSPACE;
+    }
+    int parts = qg::rms_norm_grad_parts(M, n);
+    const int64_t fit = (int64_t)(workspace_bytes / ((size_t)n * 4));
+    if (M > 0 && fit < parts) {
+        // Some larger shapes run fewer workgroups, never fewer than GRAD_PARTS_KEPT of
+        // those this one has; with their workspace this one runs as many as it holds.
+        if (fit < std::min(parts, qg::GRAD_PARTS_KEPT)) return QG_ERR_WORKSPACE;
+        parts = (int)fit;
     }
     (void)hipGetLastError();
     const qg::RmsNormGradArgs a{M, (int)n, dy, ld_dy, h, ldh, weight, rstd, dh, ld_dh, dx, ld_dx, dweight,
-                                (float*)workspace, qg::rms_norm_grad_parts(M, n)};
+                                (float*)workspace, parts};
     const char* name = "";
     const hipError_t e = qg::launch_rms_norm_grad(a, type, weight_type == QG_FP32, (hipStream_t)stream, &name);
     return done(e, name);

@@ -29,6 +29,9 @@ struct RmsNormGradArgs {
     void* dx; int64_t ldx; void* dweight;
     float* part; int parts;                  // [parts, n] partial sums of dweight
 };
+// Partial rows that fill the machine.  Growing a shape (M, n or both) may lower their
+// number, but not below the smaller one of GRAD_PARTS_KEPT and what it was.
+constexpr int GRAD_PARTS_KEPT = 256;
 int rms_norm_grad_parts(int64_t M, int64_t n);
 hipError_t launch_rms_norm_grad(const RmsNormGradArgs& a, qg_dtype type, bool weight_f32, hipStream_t s,
                                 const char** name);
