@@ -187,7 +187,6 @@ qg_status mx_matmul(int64_t M, int64_t N, int64_t K, const void* A, qg_dtype a_f
     const bool fast = lda % 16 == 0 && ldw % 16 == 0 && aligned(A, 16) && aligned(W, 16) && scale_rows_padded != 0 &&
                       (ld_a_scale % 4 == 0 || M == 1) && (ld_w_scale % 4 == 0 || N == 1) && aligned(a_scale, 4) &&
                       aligned(w_scale, 4) && !env_is("QGEMM_MX_KERNEL", "bytes");
-    if (!fast && (M + 15) / 16 > 65535) return QG_ERR_UNSUPPORTED;   // the other kernel's second grid dimension
     if (((M + 255) / 256) * ((N + 255) / 256) >= (int64_t)1 << 23) return QG_ERR_UNSUPPORTED;   // one launch's threads
     (void)hipGetLastError();
     qg::MxMatmulArgs a{};

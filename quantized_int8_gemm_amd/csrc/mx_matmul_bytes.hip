@@ -51,7 +51,7 @@ __global__ __launch_bounds__(256) void mx_matmul_bytes_kernel(MxMatmulArgs p) {
 }
 
 template <bool A8>
-hipError_t by_out(const MxMatmulArgs& p, hipStream_t s) {
+hipError_t by_out(const MxMatmulArgs& p, hipStream_t s) {   // M <= ROWS, N <= COLUMNS
     const dim3 grid((unsigned)((p.N + 63) / 64), (unsigned)((p.M + 15) / 16));
     if (p.out_type == QG_FP32)
         hipLaunchKernelGGL((mx_matmul_bytes_kernel<A8, float>), grid, dim3(256), 0, s, p);
@@ -64,9 +64,27 @@ hipError_t by_out(const MxMatmulArgs& p, hipStream_t s) {
 
 }  // namespace
 
-hipError_t launch_mx_bytes(const MxMatmulArgs& a, bool a8, hipStream_t s, const char** name) {
+hipError_t launch_mx_bytes(const MxMatmulArgs& all, bool a8, hipStream_t s, const char** name) {
     *name = "mx_matmul_bytes";
-    return a8 ? by_out<true>(a, s) : by_out<false>(a, s);
+    // one launch's second grid dimension, and the threads of its first
+    constexpr int ROWS = 65535 * 16, COLUMNS = 1 << 29;
+    const int out_size = all.out_type == QG_FP32 ? 4 : 2;
+    for (int n = 0; n < all.N; n += COLUMNS) {
+        for (int m = 0; m < all.M; m += ROWS) {
+            MxMatmulArgs a = all;
+            a.M = all.M - m < ROWS ? all.M - m : ROWS;
+            a.N = all.N - n < COLUMNS ? all.N - n : COLUMNS;
+            a.A = all.A + m * all.lda;
+            a.as = all.as + m * all.ldas;
+            a.W = all.W + n * all.ldw;
+            a.ws = all.ws + n * all.ldws;
+            if (all.act_scale != nullptr) a.act_scale = all.act_scale + m;
+            a.out = (char*)all.out + (m * all.ldo + n) * out_size;
+            const hipError_t e = a8 ? by_out<true>(a, s) : by_out<false>(a, s);
+            if (e != hipSuccess) return e;
+        }
+    }
+    return hipSuccess;
 }
 
 }  // namespace qg
