@@ -45,7 +45,7 @@ MxKind mx_kind(int64_t M, int64_t N, bool split) {
     const int forced = env_int("QGEMM_MX_TILE", -1);
     if (forced >= 0 && forced <= MX_DECODE && (forced != MX_DECODE || M <= qg::MX_DECODE_MAX_M)) return (MxKind)forced;
     auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-    if (M <= 8 && tiles(32, 32) <= 112) return MX_DECODE;
+    if (M <= qg::MX_DECODE_MAX_M && tiles(32, 32) <= 112) return MX_DECODE;   // up to 3584 columns
     // the smallest tile of which every CU gets at most one
     if (tiles(32, 32) <= qg::MX_ROUND) return MX_32x32;
     if (tiles(64, 32) <= qg::MX_ROUND) return MX_64x32;

@@ -9,7 +9,7 @@
 // block into place.  The waves' partial tiles are added through LDS in a fixed
 // order.  Bound by latency: 1 x 2048 x 8192 7.1 us, where 32 x 32 tiles take 8.5 (64
 // workgroups instead of 128).  Its loads of A, which fill 16 rows whatever there are,
-// let the tiles win from 4096 columns on, or with more than eight rows.
+// let the tiles win past 3584 columns, or with more than eight rows.
 #include "mx_mfma.h"
 
 namespace qg {

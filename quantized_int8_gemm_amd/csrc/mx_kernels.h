@@ -68,9 +68,9 @@ hipError_t launch_mx_64x64(const MxMatmulArgs& a, bool a8, hipStream_t s);
 hipError_t launch_mx_64x32(const MxMatmulArgs& a, bool a8, hipStream_t s);
 hipError_t launch_mx_32x32(const MxMatmulArgs& a, bool a8, hipStream_t s);
 
-// At most 16 rows: W streamed once, 16 columns per workgroup; operands laid out as
+// At most 8 rows: W streamed once, 16 columns per workgroup; operands laid out as
 // for the tiled kernels.
-constexpr int MX_DECODE_MAX_M = 16;
+constexpr int MX_DECODE_MAX_M = 8;
 hipError_t launch_mx_decode(const MxMatmulArgs& a, bool a8, hipStream_t s);
 
 // Names the kernel for qgemm_last_kernel().

@@ -98,6 +98,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * KW * 64) void mx_tiled_kern
     // loads newer than the next chunk's and than the last part of its scale group
     constexpr int AFTER = STAGES == 2 ? 0 : LOADS + D * (LOADS + S_ROUNDS);
     constexpr int OB = sizeof(T), AV = A8 ? 2 : 1;
+    static_assert(SPW == 2 || SPW == 4, "an even number of steps alternates the fragments' buffers");
     static_assert(WN == 32 || WN % 64 == 0, "output staging");
     static_assert(A_BYTES % (NT * 16) == 0 && W_BYTES % (NT * 16) == 0, "whole load rounds");
     static_assert(BM % 16 == 0, "a wave's scale words are of one operand");
@@ -140,7 +141,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * KW * 64) void mx_tiled_kern
     // Part `part` of PARTS of the loads of chunk kt.  Blocks past K, whole chunks
     // too, are read from outside the windows: every chunk issues the same loads,
     // so the loop has no branches and its waits are constants.
-    constexpr int PARTS = SPW > 1 ? 2 * FM : FM;
+    constexpr int PARTS = 2 * FM;
     auto issue = [&](int kt, int stage, int part) __attribute__((always_inline)) {
         const uint32_t base = lds0 + (uint32_t)stage * STAGE, codes = base + wave * 1024;
         const uint32_t ka = scalar(kt * AW), kw = scalar(kt * WW);
@@ -216,8 +217,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * KW * 64) void mx_tiled_kern
     asm volatile("" : "+v"(as_at), "+v"(ws_at));
     auto read_scale = [&](const uint8_t* at) -> uint32_t {
         if constexpr (SPW == 4) return *reinterpret_cast<const uint32_t*>(at);
-        else if constexpr (SPW == 2) return *reinterpret_cast<const uint16_t*>(at);
-        else return *at;
+        else return *reinterpret_cast<const uint16_t*>(at);
     };
 
     // Fragments of the current step and the next; scales of the chunk, and of
@@ -271,7 +271,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * KW * 64) void mx_tiled_kern
                 issue_scales(kt + 1 + D, 1);
             }
             if (last) issue(kt + STAGES, stage, a);
-            if (s == 0 && SPW > 1) issue(kt + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1, FM + a);
+            if (s == 0) issue(kt + STAGES - 1, stage == 0 ? STAGES - 1 : stage - 1, FM + a);
             __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
             for (int b = 0; b < FN; ++b)
@@ -295,24 +295,17 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * KW * 64) void mx_tiled_kern
     for (int a = 0; a < FM; ++a) read_a(smem, a, 0, 0);
     read_scales(0);
     int stage = 0;
-    auto chunk = [&](int kt, int cur) __attribute__((always_inline)) {
+    auto chunk = [&](int kt) __attribute__((always_inline)) {
 #pragma unroll
-        for (int s = 0; s < SPW - 1; ++s) step(kt, stage, s, (cur + s) & 1);
+        for (int s = 0; s < SPW - 1; ++s) step(kt, stage, s, s & 1);
         // the next chunk and its scales are there, and every wave has read this
         // chunk's last fragments
         wait_vmcnt<AFTER>();
         __syncthreads();
-        step(kt, stage, SPW - 1, (cur + SPW - 1) & 1);
+        step(kt, stage, SPW - 1, 1);
         stage = stage + 1 == STAGES ? 0 : stage + 1;
     };
-    if constexpr (SPW % 2 == 0) {
-        for (int kt = 0; kt < nk; ++kt) chunk(kt, 0);
-    } else {
-        for (int kt = 0; kt < nk; kt += 2) {
-            chunk(kt, 0);
-            if (kt + 1 < nk) chunk(kt + 1, 1);
-        }
-    }
+    for (int kt = 0; kt < nk; ++kt) chunk(kt);
     wait_vmcnt<0>();   // loads past K write zeros
     __syncthreads();   // every wave is done with the stage ring
 
