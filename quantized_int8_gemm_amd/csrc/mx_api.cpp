@@ -45,7 +45,10 @@ MxKind mx_kind(int64_t M, int64_t N, bool split) {
     const int forced = env_int("QGEMM_MX_TILE", -1);
     if (forced >= 0 && forced <= MX_DECODE && (forced != MX_DECODE || M <= qg::MX_DECODE_MAX_M)) return (MxKind)forced;
     auto tiles = [&](int64_t bm, int64_t bn) { return ((M + bm - 1) / bm) * ((N + bn - 1) / bn); };
-    if (M <= qg::MX_DECODE_MAX_M && tiles(32, 32) <= 112) return MX_DECODE;   // up to 3584 columns
+    // up to 3584 columns; split, which costs tiles more than it does this kernel, up to
+    // 4096, whose 16-column workgroups are one a CU (K = 8192, W from memory, M = 1 / 8:
+    // 4096 8.5 / 9.5 us, 32 x 32 tiles 11.7 / 12.0; 6144 11.1 / 13.7, tiles 12.5 / 12.7)
+    if (M <= qg::MX_DECODE_MAX_M && tiles(32, 32) <= (split ? 128 : 112)) return MX_DECODE;
     // the smallest tile of which every CU gets at most one
     if (tiles(32, 32) <= qg::MX_ROUND) return MX_32x32;
     if (tiles(64, 32) <= qg::MX_ROUND) return MX_64x32;

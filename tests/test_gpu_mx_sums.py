@@ -59,8 +59,17 @@ def test_sums_of_the_byte_kernel(M, N, K):
 
 
 @pytest.mark.parametrize("tile", range(6))
-@pytest.mark.parametrize("M,N,K", [(40, 70, 128), (300, 290, 256), (2100, 2111, 96)])
+@pytest.mark.parametrize("M,N,K", [(40, 70, 128), (300, 290, 256), (2100, 2111, 128)])
 def test_sums_of_every_tile(tile, M, N, K):
     case(f"mx_matmul cancelling groups, tile {tile}, {M}x{N}x{K}")
     with env(QGEMM_MX_TILE=tile):
         check(M, N, K)
+        assert q._binding.last_kernel().startswith("mx_tiled_")
+
+
+@pytest.mark.parametrize("M,N,kernel", [(1, 4096, "mx_decode"), (8, 4096, "mx_decode"), (1, 4097, "mx_tiled_32x32"), (9, 4096, "mx_tiled_32x32")])
+def test_the_kernel_of_few_rows(M, N, kernel):
+    """MXFP8 activations, whose products are split."""
+    case(f"mx_matmul kernel for MXFP8 {M}x{N}")
+    check(M, N, 128)
+    assert q._binding.last_kernel() == kernel
