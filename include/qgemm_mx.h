@@ -44,7 +44,8 @@ extern "C" {
  *
  * The norm sees h as it is stored, so a later reader of h (the gradient)
  * sees the same values.  Sums and r are fp32; a row whose sum of squares
- * passes fp32's range gives r = 0.  `format` is the form y takes:
+ * passes fp32's range gives r = 0, and one whose squares fall below it r = 1 /
+ * sqrt(eps), infinity with eps = 0.  `format` is the form y takes:
  *   QG_FP32, QG_BF16, QG_FP16: out is y, [M,n], rounded once; row_scale
  *     (may be NULL) receives r.  16-bit formats need x of the same type.
  *   QG_INT8: with t = fl32(h * weight) and a = max_j |t[m,j]|,

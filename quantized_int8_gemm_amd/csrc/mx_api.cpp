@@ -59,7 +59,8 @@ MxKind mx_kind(int64_t M, int64_t N, bool split) {
     // then have no registers for the next fragments).  4096 x 4096 x 4096 MXFP4: one
     // large 38.8 us, four small 47.8; 2444 x 3355 x 2464: one 25.3, three 32.0; 4096 x
     // 4352 x 4096: two 59.2, five 57.3; 2560 x 2560 x 4096: one 29.5, two 24.5.  Split:
-    // 4096 x 5120 x 4096 two 163, five 128; 8192 x 8192 x 8192 four 688, sixteen 750.
+    // 4096 x 4096 x 4096 one 97, four 102; 2444 x 3355 x 2464 one 57, three 50; 4096 x 5120 x
+    // 4096 two 160, five 132; 8192 x 8192 x 8192 four 668, sixteen 729.
     const int64_t large = (tiles(256, 256) + qg::MX_ROUND - 1) / qg::MX_ROUND;
     const int64_t small = (tiles(128, 128) + qg::MX_ROUND - 1) / qg::MX_ROUND;
     return 4 * small >= (split ? 15 : 12) * large ? MX_256x256 : MX_128x128;

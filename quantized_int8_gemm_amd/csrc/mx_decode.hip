@@ -7,9 +7,10 @@
 // lane, and one 16x16x128 matrix instruction or two; two chunks' loads are in flight at
 // once.  Scale bytes come four words at a time, and a lane shifts the byte of its
 // block into place.  The waves' partial tiles are added through LDS in a fixed
-// order.  Bound by latency: 1 x 2048 x 8192 7.1 us, where 32 x 32 tiles take 8.5 (64
-// workgroups instead of 128).  Its loads of A, which fill 16 rows whatever there are,
-// let the tiles win past 3584 columns, or with more than eight rows.
+// order.  Bound by latency: 1 x 2048 x 8192 MXFP4 5.6 us, where 32 x 32 tiles take 7.1 (64
+// workgroups instead of 128); MXFP8 6.3 and 10.7.  Its loads of A, which fill 16 rows
+// whatever there are, let the tiles win past 3584 columns (MXFP8: 4096), or with more than
+// eight rows.
 #include "mx_mfma.h"
 
 namespace qg {

@@ -2,8 +2,8 @@
 // 16 x 16 tile of the output straight from memory, 128 values of K at a time,
 // with 16-byte loads at any byte address.  It serves layouts that the tiled
 // and the weight-streaming kernels do not take; nothing is reused between
-// waves but through the caches, so it is several times slower than they are
-// on large products.
+// waves but through the caches: 4096 columns, K = 4160, MXFP8, 1, 64 and 4096 rows
+// 15.9, 16.8 and 694 us a call, where they take 7.7, 10.2 and 101.
 #include "mx_mfma.h"
 
 namespace qg {

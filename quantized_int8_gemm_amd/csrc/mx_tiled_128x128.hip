@@ -1,11 +1,10 @@
 // 128 x 128 tiles of the MX product, wave tiles of 64 x 64 (MXFP4) or 32 x 128 (MXFP8
 // activations, whose fragments are split: half as many as in 64 x 64 ones, 2048 x 2048 x
-// 4096 with fp32 output 33.3 -> 29.3 us).  Where every CU has at
-// most one of them, eight waves (two to a wave tile) and a deep ring: four stages of
-// 256 values of K (MXFP4, 140 KiB) or three (MXFP8 activations, 152 KiB): 2048 x 2048
-// x 4096 MXFP4 17.4 us, with two stages and four waves 24.4.  For more, four waves
-// and two stages of 256 values (72 KiB, two workgroups a CU) or three of 128 (MXFP8
-// activations, 80 KiB).
+// 4096 with fp32 output 33.3 -> 29.3 us).  Where every CU has at most one of them, eight
+// waves (two to a wave tile) and a deep ring: four stages of 256 values of K (MXFP4, 140
+// KiB) or three (MXFP8 activations, 152 KiB): 2048 x 2048 x 4096 MXFP4 17.4 us, with two
+// stages and four waves 24.4.  For more, four waves and two stages of 256 values (72 KiB,
+// two workgroups a CU) or three of 128 (MXFP8 activations, 80 KiB).
 #include "mx_tiled_impl.h"
 
 namespace qg {

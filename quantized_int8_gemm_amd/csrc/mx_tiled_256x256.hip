@@ -2,7 +2,7 @@
 // stages of 256 values of K, two of them (144 KiB with the scales); MXFP8 activations:
 // 128 values, three (160 KiB), and wave tiles of 64 x 128, since every A fragment is
 // split (mx_mfma.h) and these split half as many for the same products, 8192^3 with
-// fp32 output 769 -> 688 us.
+// fp32 output 769 -> 688 us (bf16 668).
 #include "mx_tiled_impl.h"
 
 namespace qg {

@@ -20,18 +20,22 @@
 //    every wave holds the last fragments of the old stage, so its ring place is
 //    free for the chunk STAGES on, whose loads are spread over that step and the
 //    next (all at once they hold the matrix instructions up).  Against reading
-//    after the barrier: 8192^3 303 -> 292 us, 4096^3 with MXFP8 activations 62.8 ->
-//    58.3.  The products of one row block may mix with the next one's reads: 8192^3
-//    with MXFP8 activations 410 -> 400 us.
+//    after the barrier: 8192^3 MXFP4 303 -> 292 us.  The products of one row block may
+//    mix with the next one's reads: 8192^3 with MXFP8 activations, when they were
+//    multiplied once, 410 -> 400 us.
 //  * KW waves share a wave tile, each with its part of every stage's steps; their
 //    sums are added through LDS, in order, so results repeat bit for bit.  Small
 //    tiles need it: with one wave a SIMD every step waits for its fragments.
 //  * The finished wave tile goes through LDS, 32 rows and 64 columns at a time, and
 //    leaves in whole rows of those.
-// What bounds 8192^3 MXFP4 (262 us, 4.2 PFLOP/s): the instruction alone on register
+// Two figures side by side are of one run; from one run to another the same kernel
+// differs by 2 %.
+// What bounds 8192^3 MXFP4 (264 us, 4.2 PFLOP/s): the instruction alone on register
 // operands runs at 7.1 PFLOP/s on random data, the clock falling from 2.4 to 1.7 GHz
 // (9.7 PFLOP/s on zeros), and on this product's fragments at 5.9; the kernel keeps
-// the matrix cores busy 53 % of the cycles at 1.8 GHz.  Taken at 276 us, it ran 223 us
+// the matrix cores busy 55 % of the cycles at 1.77 GHz.  With MXFP8 activations, whose
+// products take two instructions at 4.3 PFLOP/s, 8192^3 takes 668 us and 4096^3 87, the
+// matrix cores busy 62 % of the cycles at 2.13 GHz.  Taken at 276 us, it ran 223 us
 // without its loads, 265 without its fragment reads, 226 without its products and 172
 // with its loads alone: no stream stands out, and each costs clock.  A stage takes
 // 2918 cycles of which 2048 are products; the first chunk's latency is 6500 cycles a
@@ -258,7 +262,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * KW * 64) void mx_tiled_kern
 #pragma unroll
         for (int a = 0; a < FM; ++a) {
             // W's fragments: first where A's are twice their size, else along with A's
-            // (8192^3 MXFP4 261.5 against 259.7 us, MXFP8 398 against 401)
+            // (8192^3 MXFP4 261.5 against 259.7 us, MXFP8 669 against 674)
             if constexpr (A8) {
                 if (a == 0) read_w(S, ns, nxt);
             } else {

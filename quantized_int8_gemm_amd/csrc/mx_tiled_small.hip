@@ -1,9 +1,10 @@
 // The small tiles of the MX product, for outputs that would leave CUs idle under
 // larger ones; wave tiles of 32 x 32, stages of 512 values of K.  At N = K = 8192
 // (36 MB of weights, from memory) with MXFP4 / MXFP8 activations: 32 x 32 tiles, four
-// waves, M = 1 10.8 / 11.0 us, M = 16 11.4 / 12.2; 64 x 32, four waves a wave tile, M
-// = 64 15.2 / 16.8; 64 x 64, two waves a wave tile, M = 128 16.4 / 18.9.  Each shape
-// with stages of 256 values is 4 to 10 % slower, with two waves fewer 15 to 30 %.
+// waves, M = 1 10.9 / 13.2 us, M = 16 11.3 / 14.2 (weights in the Infinity Cache: M = 1
+// 8.8 / 11.7, M = 16 9.3 / 12.4); 64 x 32, four waves a wave tile, M = 64 15.6 / 18.9; 64 x
+// 64, two waves a wave tile, M = 128 17.2 / 25.5.  When each was chosen, stages of 256
+// values were 4 to 10 % slower, two waves fewer 15 to 30 %.
 #include "mx_tiled_impl.h"
 
 namespace qg {

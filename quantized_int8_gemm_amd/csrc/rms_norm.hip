@@ -9,7 +9,10 @@
 // is added in, and MX blocks leave before the row's sum is known.
 //
 // Bound by HBM: every value is read once and kept in registers (at most 64 a
-// lane), one barrier per row.  A row is shared by G lanes: 16 up to 128 columns,
+// lane), one barrier per row.  Past 32768 columns that is more than 1024 lanes have:
+// fp32 spills (83 to 95 of a lane's 128 registers, 232 to 240 bytes), fp16 a little (8 to
+// 20): 1000 x 65536 with a residual to int8 fp32 263 us, 3.2 TB/s, fp16 128, 3.6, bf16
+// 102, 4.5; 1000 x 32768 fp32 88 us, 4.8.  A row is shared by G lanes: 16 up to 128 columns,
 // 32 up to 256, a wave up to 1024 (16, 8 and 4 rows per workgroup), 256 lanes up to
 // 8192, 512 up to 16384, 1024 beyond.  Up to 512 rows leave CUs without work, so the
 // lanes of each take as little of it as they can: 512 up to 4096 columns, 1024 beyond
@@ -17,9 +20,10 @@
 // 768 x 5000 8.5 -> 9.5, 1024 x 8192 13.0 -> 13.8).  Lanes that have nothing of a row
 // cost as much as those that have: 8192 x 5120 bf16 54.9 us with the four groups a lane
 // that 8192 columns take, 49.5 with three.
-// 8192 x 8192 bf16 with a residual to int8: 73.9 us, 6.4 TB/s over what is read
-// and written (a copy of 2 GiB runs at 4.85); one row of 4096 3.2 us, the launch's and
-// one load's latency.
+// 8192 x 8192 bf16 with a residual to int8: 75 us, 6.3 TB/s over what is read
+// and written (a copy of 2 GiB runs at 4.85), where calls write the same outputs again,
+// 81.5 where each allocates its own; one row of 4096 2.6 us, the launch's and one load's
+// latency.
 #include "mx_common.h"
 
 namespace qg {

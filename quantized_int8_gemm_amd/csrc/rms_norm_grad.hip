@@ -6,8 +6,8 @@
 // workgroup walks rows with a fixed set of columns per lane, so dw is added up
 // in registers and leaves once, as one row of partial sums per workgroup; a
 // second kernel adds those.  No atomics: the order of every sum is fixed.
-// 8192 x 4096 bf16 with dh: 49.7 us both kernels, 5.4 TB/s (a copy of 2 GiB runs at
-// 4.85); 86.9 us with one row at a time in the registers as single values, which
+// 8192 x 4096 with dh: bf16 51.2 us both kernels, 5.2 TB/s, fp32 103.7, 5.2 (a copy of 2
+// GiB runs at 4.85); bf16 86.9 us with one row at a time in the registers as single values, which
 // left two waves per SIMD nothing in flight between the barrier and the stores.
 #include "mx_common.h"
 
@@ -36,13 +36,18 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
 //    so 168 registers: the next row's loads are in flight while this one's sum is
 //    completed and its results are stored (3691 x 12288 bf16 67.1 us, HOLD 70.6; fp32
 //    would spill, 168 against 145);
-//  * HOLD, 512 to 1024 lanes: one row at a time, in at most 128 registers, so
-//    that two workgroups share a CU and one's loads cover the other's barrier
-//    (5000 x 6144 bf16 54.7 us, AHEAD 59.3; 2000 x 16384 55.6, AHEAD 63.9); past
-//    16384 columns of 16 bits too, the weights read again where they are used (1000
-//    x 32768 bf16 105 us, AGAIN 115);
+//  * HOLD, 512 to 1024 lanes: one row at a time, in at most 128 registers.  Of 512
+//    lanes two workgroups share a CU, and one's loads cover the other's barrier (5000
+//    x 6144 bf16 54.7 us, AHEAD 59.3); 768 (fp32) and 1024 have the CU to themselves
+//    and nothing covers theirs, but with two rows in hand they spill (2000 x 16384
+//    55.6, AHEAD 63.9); past 16384 columns of 16 bits too, the weights read again
+//    where they are used (1000 x 32768 bf16 105 us, AGAIN 115);
 //  * AGAIN, wider rows, where dw alone takes 32 or 64 registers: a row is read
-//    once for its sum and again, from the caches, for its results.
+//    once for its sum and again, from the caches, for its results (1000 x 32768 fp32
+//    218 us, 2.4 TB/s; 1000 x 65536 bf16 410, 1.3).
+// Registers spill from 16385 columns on, in fp32 from 12289 (4 of them, 20 bytes a lane:
+// 1000 x 16384 60 us, 4.4 TB/s).  The pairs above are of one run each, before rows were
+// normalised first, which costs 0 to 5 % (5000 x 6144 now 56.9, 2000 x 16384 56.4).
 enum { AHEAD, HOLD, AGAIN };
 constexpr int FEW = 256, MANY = 512;   // lanes of a workgroup that has several rows in hand
 
