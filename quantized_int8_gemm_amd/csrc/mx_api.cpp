@@ -198,6 +198,11 @@ qg_status mx_matmul(int64_t M, int64_t N, int64_t K, const void* A, qg_dtype a_f
     a.A = (const uint8_t*)A; a.lda = lda; a.as = a_scale; a.ldas = ld_a_scale;
     a.W = (const uint8_t*)W; a.ldw = ldw; a.ws = w_scale; a.ldws = ld_w_scale;
     a.act_scale = act_scale; a.out = out; a.ldo = ldo; a.out_type = out_type;
+    // A single row's stride may be anything.  The fast kernels ask for whole tiles of
+    // rows, by 4-byte words, and leave it to the buffer's end that there is only one: at a
+    // multiple of 4 the next ones start past that end, never inside its last word.
+    if (M == 1) a.ldas = (a.ldas + 3) & ~(int64_t)3;
+    if (N == 1) a.ldws = (a.ldws + 3) & ~(int64_t)3;
     const bool a8 = a_format == QG_MXFP8;
     const hipStream_t st = (hipStream_t)stream;
     const char* name = "";
