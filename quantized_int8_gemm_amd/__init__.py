@@ -36,6 +36,17 @@ Around the products (``include/qgemm_mx.h``):
 * ``mx_matmul(A, a_scale, W, w_scale, act_scale=None)``: MXFP8 or MXFP4
   activations times an MXFP4 weight.
 
+The A8W8 product as a feed-forward block uses it (``include/qgemm_fused.h``):
+
+* ``qgemm_a8w8_linear(A, W, act_scale, weight_scale, bias, activation,
+  residual)``: with bias, activation and residual in the epilogue;
+  ``qgemm_a8w8_gated(A, W_gate, W_up, ...)``: act(gate) * up of two products.
+* ``qgemm_a8w8_linear_grad`` and ``qgemm_a8w8_gated_grad``: their gradients,
+  from the 8-bit checkpoints that the forward calls leave on request.
+* ``int8_quantize(x, block=None)`` and ``int8_dequantize(codes, scale)``: int8
+  with a scale per row (the products' left operand) or per 32 columns (the
+  checkpoints' form), and back.
+
 ``calib_read``, ``calib_mfma_i8``, ``calib_mfma_f32`` and ``calib_mfma_bf16``
 measure the machine's HBM read and int8, fp32 and bf16 matrix-core ceilings
 for the roofline figures.
@@ -73,4 +84,12 @@ from ._mx import (  # noqa: F401
     rms_norm,
     rms_norm_grad,
     rms_norm_quantize,
+)
+from ._fused import (  # noqa: F401
+    int8_dequantize,
+    int8_quantize,
+    qgemm_a8w8_gated,
+    qgemm_a8w8_gated_grad,
+    qgemm_a8w8_linear,
+    qgemm_a8w8_linear_grad,
 )

@@ -20,8 +20,8 @@ class _Missing:
     """In the extension module's place where it is not built or does not load
     (another torch): the calls below raise, the integer products work."""
 
-    def __init__(self, why):
-        self._text = (f"quantized_int8_gemm_amd/_mx_binding.so is not built for this torch ({why}); run "
+    def __init__(self, why, name="_mx_binding"):
+        self._text = (f"quantized_int8_gemm_amd/{name}.so is not built for this torch ({why}); run "
                       "__graft_entry__.build() (python -c 'import __graft_entry__ as g; g.build()')")
 
     def __getattr__(self, name):

@@ -1,0 +1,339 @@
+// C entry points of qgemm_fused.h: argument checks (before any HIP call), workspace
+// plans, kernel choice and launch, with the launch-status convention of api.cpp.
+#include <algorithm>
+
+#include <hip/hip_runtime.h>
+
+#include "fused_kernels.h"
+#include "kernels.h"
+
+namespace {
+
+constexpr int64_t LIM = (int64_t)1 << 30;
+constexpr int64_t SPAN_LIMIT = (int64_t)1 << 31;   // 32-bit buffer offsets
+constexpr size_t Z_BYTES = (size_t)1 << 28;        // fp32 products in memory at once, about
+
+bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
+bool is_float(qg_dtype t) { return t == QG_FP32 || t == QG_BF16 || t == QG_FP16; }
+bool aligned_for(const void* p, qg_dtype t) { return aligned(p, t == QG_FP32 ? 4 : 2); }
+size_t up256(size_t n) { return (n + 255) / 256 * 256; }
+int64_t blocks_of(int64_t n) { return (n + 31) / 32; }
+
+qg_status nothing() {
+    qg::record_kernel("none");
+    return QG_OK;
+}
+
+qg_status done(hipError_t e, const char* name) {
+    if (e != hipSuccess) return QG_ERR_HIP;
+    qg::record_kernel(name);
+    return QG_OK;
+}
+
+#define QG_TRY(call)                                   \
+    do {                                               \
+        const qg_status st_ = (call);                  \
+        if (st_ != QG_OK) return st_;                  \
+    } while (0)
+#define QG_TRY_HIP(call)                               \
+    do {                                               \
+        if ((call) != hipSuccess) return QG_ERR_HIP;   \
+    } while (0)
+
+// Spans that 32-bit offsets reach, as qgemm_a8w8 checks them.
+bool span_ok(int64_t K, int64_t lda, int64_t ldw, int b_trans) {
+    return 256 * lda + K + 256 < SPAN_LIMIT && (b_trans ? 256 * ldw + K + 256 : (K + 256) * ldw) < SPAN_LIMIT;
+}
+
+// Products through memory: `count` fp32 matrices of `rows` rows at a time, and the
+// workspace of the products' own kernels.
+struct Through {
+    int64_t rows;
+    size_t z, gemm;   // bytes of one matrix, of the kernels' workspace
+    Through(int64_t M, int64_t N, int64_t K, int count) {
+        const int64_t fit = (int64_t)(Z_BYTES / ((size_t)N * 4 * count)) / 256 * 256;
+        rows = std::min(M, std::max<int64_t>(fit, 256));
+        z = up256((size_t)rows * N * 4);
+        gemm = qgemm_workspace_bytes(QG_OP_A8W8, 1, rows, N, K);
+        if (M % rows != 0) gemm = std::max(gemm, qgemm_workspace_bytes(QG_OP_A8W8, 1, M % rows, N, K));
+        gemm = up256(gemm);
+    }
+    size_t bytes(int count) const { return gemm + z * count; }
+};
+
+struct Scales { const float* p; int64_t len; };
+
+bool scale_ok(const Scales& s, int64_t n) { return s.p != nullptr && aligned(s.p, 4) && (s.len == 1 || s.len == n); }
+
+// The forward calls.
+struct Forward {
+    int64_t M, N, K;
+    const int8_t* A; int64_t lda;
+    const int8_t* W[2]; int64_t ldw[2]; int b_trans;
+    int pair;
+};
+
+bool sizes_bad(int64_t M, int64_t N, int64_t K) {
+    return M < 0 || N < 0 || K < 0 || M >= LIM || N >= LIM || K >= LIM;
+}
+
+size_t forward_workspace(const Forward& f) {
+    if (sizes_bad(f.M, f.N, f.K) || f.M == 0 || f.N == 0 || f.K == 0) return 0;
+    return Through(f.M, f.N, f.K, f.pair).bytes(f.pair);
+}
+
+bool checkpoint_ok(const int8_t* c, int64_t ldc, const float* s, int64_t lds, int64_t N) {
+    return c != nullptr && s != nullptr && aligned(s, 4) && ldc >= N && lds >= blocks_of(N);
+}
+
+qg_status forward(const Forward& f, const Scales& act, const Scales* ws, const float* bias, qg_activation activation,
+                  const void* res, int64_t ldr, void* out, qg_dtype out_dtype, int64_t ldo, int8_t* ckpt, int64_t ld_ckpt,
+                  float* ckpt_scale, int64_t ld_ckpt_scale, void* workspace, size_t workspace_bytes, void* stream) {
+    const int64_t M = f.M, N = f.N, K = f.K;
+    if (sizes_bad(M, N, K)) return QG_ERR_INVALID_ARGUMENT;
+    if (!is_float(out_dtype) || activation < QG_ACT_NONE || activation > QG_ACT_GELU_TANH || (f.b_trans != 0 && f.b_trans != 1))
+        return QG_ERR_INVALID_ARGUMENT;
+    if (M == 0 || N == 0) return nothing();
+    if (K == 0 || f.A == nullptr || out == nullptr || f.lda < K || ldo < N) return QG_ERR_INVALID_ARGUMENT;
+    if (!scale_ok(act, M) || !aligned(bias, 4) || !aligned_for(out, out_dtype)) return QG_ERR_INVALID_ARGUMENT;
+    for (int h = 0; h < f.pair; ++h)
+        if (f.W[h] == nullptr || f.ldw[h] < (f.b_trans ? K : N) || !scale_ok(ws[h], N)) return QG_ERR_INVALID_ARGUMENT;
+    if (res != nullptr && (ldr < N || !aligned_for(res, out_dtype))) return QG_ERR_INVALID_ARGUMENT;
+    if ((ckpt != nullptr || ckpt_scale != nullptr) && !checkpoint_ok(ckpt, ld_ckpt, ckpt_scale, ld_ckpt_scale, N))
+        return QG_ERR_INVALID_ARGUMENT;
+    if (workspace != nullptr && !aligned(workspace, 256)) return QG_ERR_INVALID_ARGUMENT;
+    for (int h = 0; h < f.pair; ++h)
+        if (!span_ok(K, f.lda, f.ldw[h], f.b_trans)) return QG_ERR_UNSUPPORTED;
+    const size_t need = forward_workspace(f);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return QG_ERR_WORKSPACE;
+
+    qg::Epilogue e{};
+    e.M = (int)M; e.N = (int)N;
+    e.act_scale = act.p; e.as_stride = act.len == 1 ? 0 : 1;
+    for (int h = 0; h < f.pair; ++h) {
+        e.w_scale[h] = ws[h].p;
+        e.ws_stride[h] = ws[h].len == 1 ? 0 : 1;
+        if (ckpt != nullptr) {
+            e.ckpt[h] = ckpt + (int64_t)h * M * ld_ckpt;
+            e.ckpt_scale[h] = ckpt_scale + (int64_t)h * M * ld_ckpt_scale;
+        }
+    }
+    e.bias = bias; e.activation = activation;
+    e.res = res; e.ldr = ldr;
+    e.out = out; e.ldo = ldo; e.out_type = out_dtype;
+    e.ld_ckpt = ld_ckpt; e.ld_ckpt_scale = ld_ckpt_scale;
+    (void)hipGetLastError();
+    const hipStream_t s = (hipStream_t)stream;
+
+    const Through t(M, N, K, f.pair);
+    char* const z = (char*)workspace + t.gemm;
+    if (t.gemm > 0) QG_TRY_HIP(qg::launch_clear((uint32_t*)workspace, qg::SKINNY_MAX_TICKETS, s));
+    for (int64_t m = 0; m < M; m += t.rows) {
+        const int64_t rows = std::min(t.rows, M - m);
+        for (int h = 0; h < f.pair; ++h)
+            QG_TRY(qgemm_a8w8(rows, N, K, f.A + m * f.lda, f.lda, f.W[h], f.ldw[h], f.b_trans,
+                              act.p + (act.len == 1 ? 0 : m), act.len == 1 ? 1 : rows, ws[h].p, ws[h].len, z + h * t.z, QG_FP32, N,
+                              t.gemm > 0 ? workspace : nullptr, t.gemm, stream));
+        QG_TRY_HIP(qg::launch_fused_finish(e, f.pair == 2, (const float*)z, (const float*)(z + t.z), (int)m, (int)rows, s));
+    }
+    return done(hipSuccess, "a8w8_then_finish");
+}
+
+// The gradients.
+struct Backward {
+    int64_t M, N, K;
+    const int8_t* W[2]; int64_t ldw[2]; int b_trans;
+    int pair;
+    bool with_bias;
+};
+
+// Where a gradient's workspace holds what.
+struct GradPlan {
+    int64_t np, ldq;
+    size_t hi, lo, row_scale, scales, part, gemm, z, bytes;
+    int parts;
+    Through t;
+    explicit GradPlan(const Backward& b)
+        : np((b.N + 127) / 128 * 128), ldq(np * b.pair), parts(b.with_bias ? qg::grad_rows_parts(b.M, b.N) : 0),
+          t(b.M, b.K, b.N, 2 * b.pair) {
+        size_t at = 0;
+        auto take = [&](size_t n) { const size_t here = at; at += up256(n); return here; };
+        gemm = take(t.gemm);
+        hi = take((size_t)b.M * ldq);
+        lo = take((size_t)b.M * ldq);
+        row_scale = take((size_t)b.M * 4);
+        scales = take((size_t)(2 * b.M + 1) * 4);
+        part = take((size_t)parts * b.N * 4);
+        z = take(t.z * 2 * b.pair);
+        bytes = at;
+    }
+};
+
+size_t backward_workspace(const Backward& b) {
+    if (sizes_bad(b.M, b.N, b.K) || b.M == 0 || b.N == 0 || b.K == 0 || b.N > QG_A8W8_GRAD_MAX_COLUMNS) return 0;
+    return GradPlan(b).bytes;
+}
+
+qg_status backward(const Backward& b, const void* dy, qg_dtype dtype, int64_t ld_dy, const Scales* ws, const int8_t* ckpt,
+                   int64_t ld_ckpt, const float* ckpt_scale, int64_t ld_ckpt_scale, qg_activation activation, void* dx,
+                   int64_t ld_dx, float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+    const int64_t M = b.M, N = b.N, K = b.K;
+    if (sizes_bad(M, N, K)) return QG_ERR_INVALID_ARGUMENT;
+    if ((dtype != QG_BF16 && dtype != QG_FP16) || activation < QG_ACT_NONE || activation > QG_ACT_GELU_TANH ||
+        (b.b_trans != 0 && b.b_trans != 1) || !aligned(dbias, 4))
+        return QG_ERR_INVALID_ARGUMENT;
+    if (N > QG_A8W8_GRAD_MAX_COLUMNS) return QG_ERR_UNSUPPORTED;
+    if (M == 0) {
+        if (dbias == nullptr || N == 0) return nothing();
+        (void)hipGetLastError();
+        qg::GradRowsArgs a{};
+        a.N = (int)N;
+        a.dbias = dbias;
+        return done(qg::launch_grad_rows(a, false, true, (hipStream_t)stream), "grad_rows");
+    }
+    if (N == 0 || K == 0 || dy == nullptr || dx == nullptr || ld_dy < N || ld_dx < K) return QG_ERR_INVALID_ARGUMENT;
+    if (!aligned_for(dy, dtype) || !aligned_for(dx, dtype)) return QG_ERR_INVALID_ARGUMENT;
+    for (int h = 0; h < b.pair; ++h)
+        if (b.W[h] == nullptr || b.ldw[h] < (b.b_trans ? K : N) || !scale_ok(ws[h], N)) return QG_ERR_INVALID_ARGUMENT;
+    const bool no_ckpt = b.pair == 1 && activation == QG_ACT_NONE && ckpt == nullptr && ckpt_scale == nullptr;
+    if (!no_ckpt && !checkpoint_ok(ckpt, ld_ckpt, ckpt_scale, ld_ckpt_scale, N)) return QG_ERR_INVALID_ARGUMENT;
+    if (workspace != nullptr && !aligned(workspace, 256)) return QG_ERR_INVALID_ARGUMENT;
+    const GradPlan p(b);
+    for (int h = 0; h < b.pair; ++h)
+        if (!span_ok(N, p.ldq, b.ldw[h], !b.b_trans)) return QG_ERR_UNSUPPORTED;
+    if (workspace == nullptr || workspace_bytes < p.bytes) return QG_ERR_WORKSPACE;
+    (void)hipGetLastError();
+    const hipStream_t s = (hipStream_t)stream;
+    char* const w = (char*)workspace;
+
+    qg::GradRowsArgs a{};
+    a.M = (int)M; a.N = (int)N; a.np = (int)p.np;
+    a.dy = dy; a.ldy = ld_dy;
+    for (int h = 0; h < b.pair; ++h) {
+        if (ckpt != nullptr) {
+            a.ckpt[h] = ckpt + (int64_t)h * M * ld_ckpt;
+            a.ckpt_scale[h] = ckpt_scale + (int64_t)h * M * ld_ckpt_scale;
+        }
+        a.w_scale[h] = ws[h].p;
+        a.ws_stride[h] = ws[h].len == 1 ? 0 : 1;
+    }
+    a.ld_ckpt = ld_ckpt; a.ld_ckpt_scale = ld_ckpt_scale;
+    a.activation = activation;
+    a.hi = (int8_t*)(w + p.hi); a.lo = (int8_t*)(w + p.lo); a.ldq = p.ldq;
+    a.row_scale = (float*)(w + p.row_scale);
+    a.scales = (float*)(w + p.scales);
+    a.part = (float*)(w + p.part); a.parts = p.parts;
+    a.dbias = dbias;
+    QG_TRY_HIP(qg::launch_grad_rows(a, b.pair == 2, dtype == QG_BF16, s));
+
+    if (p.t.gemm > 0) QG_TRY_HIP(qg::launch_clear((uint32_t*)(w + p.gemm), qg::SKINNY_MAX_TICKETS, s));
+    for (int64_t m = 0; m < M; m += p.t.rows) {
+        const int64_t rows = std::min(p.t.rows, M - m);
+        for (int h = 0; h < b.pair; ++h)
+            for (int part = 0; part < 2; ++part)
+                QG_TRY(qgemm_a8w8(rows, K, N, (part == 0 ? a.hi : a.lo) + m * p.ldq + h * p.np, p.ldq, b.W[h], b.ldw[h], !b.b_trans,
+                                  a.scales + part * M + m, rows, a.scales + 2 * M, 1, w + p.z + (2 * h + part) * p.t.z, QG_FP32, K,
+                                  p.t.gemm > 0 ? w + p.gemm : nullptr, p.t.gemm, stream));
+        QG_TRY_HIP(qg::launch_grad_sum((const float*)(w + p.z), (int64_t)(p.t.z / 4), 2 * b.pair, rows, K,
+                                       (char*)dx + m * ld_dx * 2, ld_dx, dtype == QG_BF16, s));
+    }
+    return done(hipSuccess, "grad_rows_a8w8_sum");
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qgemm_a8w8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const int8_t* W,
+                                         int64_t ldw, int b_trans) {
+    return forward_workspace({M, N, K, A, lda, {W, nullptr}, {ldw, 0}, b_trans, 1});
+}
+
+qg_status qgemm_a8w8_linear(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const int8_t* W, int64_t ldw,
+                            int b_trans, const float* act_scale, int64_t act_scale_len, const float* weight_scale,
+                            int64_t weight_scale_len, const float* bias, qg_activation activation, const void* residual,
+                            int64_t ld_residual, void* out, qg_dtype out_dtype, int64_t ldo, int8_t* checkpoint,
+                            int64_t ld_checkpoint, float* checkpoint_scale, int64_t ld_checkpoint_scale, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    const Scales ws[2] = {{weight_scale, weight_scale_len}, {nullptr, 0}};
+    return forward({M, N, K, A, lda, {W, nullptr}, {ldw, 0}, b_trans, 1}, {act_scale, act_scale_len}, ws, bias, activation, residual,
+                   ld_residual, out, out_dtype, ldo, checkpoint, ld_checkpoint, checkpoint_scale, ld_checkpoint_scale, workspace,
+                   workspace_bytes, stream);
+}
+
+size_t qgemm_a8w8_gated_workspace_bytes(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const int8_t* W_gate,
+                                        int64_t ld_gate, const int8_t* W_up, int64_t ld_up, int b_trans) {
+    return forward_workspace({M, N, K, A, lda, {W_gate, W_up}, {ld_gate, ld_up}, b_trans, 2});
+}
+
+qg_status qgemm_a8w8_gated(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const int8_t* W_gate, int64_t ld_gate,
+                           const int8_t* W_up, int64_t ld_up, int b_trans, const float* act_scale, int64_t act_scale_len,
+                           const float* gate_scale, int64_t gate_scale_len, const float* up_scale, int64_t up_scale_len,
+                           qg_activation activation, void* out, qg_dtype out_dtype, int64_t ldo, int8_t* checkpoint,
+                           int64_t ld_checkpoint, float* checkpoint_scale, int64_t ld_checkpoint_scale, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+    const Scales ws[2] = {{gate_scale, gate_scale_len}, {up_scale, up_scale_len}};
+    return forward({M, N, K, A, lda, {W_gate, W_up}, {ld_gate, ld_up}, b_trans, 2}, {act_scale, act_scale_len}, ws, nullptr,
+                   activation, nullptr, 0, out, out_dtype, ldo, checkpoint, ld_checkpoint, checkpoint_scale, ld_checkpoint_scale,
+                   workspace, workspace_bytes, stream);
+}
+
+size_t qgemm_a8w8_linear_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, const int8_t* W, int64_t ldw, int b_trans,
+                                              int with_bias) {
+    return backward_workspace({M, N, K, {W, nullptr}, {ldw, 0}, b_trans, 1, with_bias != 0});
+}
+
+qg_status qgemm_a8w8_linear_grad(int64_t M, int64_t N, int64_t K, const void* dy, qg_dtype dtype, int64_t ld_dy, const int8_t* W,
+                                 int64_t ldw, int b_trans, const float* weight_scale, int64_t weight_scale_len,
+                                 const int8_t* checkpoint, int64_t ld_checkpoint, const float* checkpoint_scale,
+                                 int64_t ld_checkpoint_scale, qg_activation activation, void* dx, int64_t ld_dx, float* dbias,
+                                 void* workspace, size_t workspace_bytes, void* stream) {
+    const Scales ws[2] = {{weight_scale, weight_scale_len}, {nullptr, 0}};
+    return backward({M, N, K, {W, nullptr}, {ldw, 0}, b_trans, 1, dbias != nullptr}, dy, dtype, ld_dy, ws, checkpoint, ld_checkpoint,
+                    checkpoint_scale, ld_checkpoint_scale, activation, dx, ld_dx, dbias, workspace, workspace_bytes, stream);
+}
+
+size_t qgemm_a8w8_gated_grad_workspace_bytes(int64_t M, int64_t N, int64_t K, const int8_t* W_gate, int64_t ld_gate,
+                                             const int8_t* W_up, int64_t ld_up, int b_trans) {
+    return backward_workspace({M, N, K, {W_gate, W_up}, {ld_gate, ld_up}, b_trans, 2, false});
+}
+
+qg_status qgemm_a8w8_gated_grad(int64_t M, int64_t N, int64_t K, const void* dy, qg_dtype dtype, int64_t ld_dy,
+                                const int8_t* W_gate, int64_t ld_gate, const int8_t* W_up, int64_t ld_up, int b_trans,
+                                const float* gate_scale, int64_t gate_scale_len, const float* up_scale, int64_t up_scale_len,
+                                const int8_t* checkpoint, int64_t ld_checkpoint, const float* checkpoint_scale,
+                                int64_t ld_checkpoint_scale, qg_activation activation, void* dx, int64_t ld_dx, void* workspace,
+                                size_t workspace_bytes, void* stream) {
+    const Scales ws[2] = {{gate_scale, gate_scale_len}, {up_scale, up_scale_len}};
+    return backward({M, N, K, {W_gate, W_up}, {ld_gate, ld_up}, b_trans, 2, false}, dy, dtype, ld_dy, ws, checkpoint, ld_checkpoint,
+                    checkpoint_scale, ld_checkpoint_scale, activation, dx, ld_dx, nullptr, workspace, workspace_bytes, stream);
+}
+
+qg_status int8_quantize(int64_t M, int64_t n, const void* x, qg_dtype type, int64_t ldx, int block, int8_t* codes, int64_t ldc,
+                        float* scale, int64_t ld_scale, void* stream) {
+    if (M < 0 || M >= LIM || n < 1 || n >= LIM || !is_float(type) || (block != 0 && block != qg::INT8_BLOCK))
+        return QG_ERR_INVALID_ARGUMENT;
+    if (block == 0 && n > QG_INT8_ROW_MAX_COLUMNS) return QG_ERR_UNSUPPORTED;
+    if (M == 0) return nothing();
+    if (x == nullptr || codes == nullptr || scale == nullptr || ldx < n || ldc < n || ld_scale < (block == 0 ? 1 : blocks_of(n)) ||
+        !aligned_for(x, type) || !aligned(scale, 4))
+        return QG_ERR_INVALID_ARGUMENT;
+    (void)hipGetLastError();
+    const qg::Int8Args a{M, n, block, x, ldx, nullptr, 0, codes, ldc, scale, ld_scale};
+    return done(qg::launch_int8_quantize(a, type, (hipStream_t)stream), block == 0 ? "int8_rows" : "int8_blocks");
+}
+
+qg_status int8_dequantize(int64_t M, int64_t n, const int8_t* codes, int64_t ldc, const float* scale, int64_t ld_scale, int block,
+                          void* out, qg_dtype out_type, int64_t ldo, void* stream) {
+    if (M < 0 || M >= LIM || n < 1 || n >= LIM || !is_float(out_type) || (block != 0 && block != qg::INT8_BLOCK))
+        return QG_ERR_INVALID_ARGUMENT;
+    if (M == 0) return nothing();
+    if (out == nullptr || codes == nullptr || scale == nullptr || ldo < n || ldc < n ||
+        ld_scale < (block == 0 ? 1 : blocks_of(n)) || !aligned_for(out, out_type) || !aligned(scale, 4))
+        return QG_ERR_INVALID_ARGUMENT;
+    (void)hipGetLastError();
+    const qg::Int8Args a{M, n, block, nullptr, 0, out, ldo, const_cast<int8_t*>(codes), ldc, const_cast<float*>(scale), ld_scale};
+    return done(qg::launch_int8_dequantize(a, out_type, (hipStream_t)stream), "int8_dequantize");
+}
+
+}  // extern "C"

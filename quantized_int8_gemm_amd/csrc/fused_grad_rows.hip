@@ -1,0 +1,262 @@
+// The factors of the fused products' gradients: for each row of dy the products of
+// dy with what the 8-bit checkpoint gives (and the weight's scale of the column), in
+// 16-bit fixed point as two int8 planes, the row's scale, and dbias.
+//
+// Mathematics: linear p = dy act'(z); gated p = dy u act'(g) and q = dy act(g).
+// The product dx = (p s) W would need p s in bf16 and the int8 weight widened to
+// bf16 in the kernel.  Held instead as t = rint(value * 32639 / a), a the row's largest
+// magnitude, and split as t = 256 hi + lo with both in int8 (|hi| <= 127, -128 <= lo <=
+// 127), it is two int8 products with the weight as it is: the same time on the
+// matrix cores as one bf16 product, and sums that are exact.  The rounding is a /
+// 65278 at most: half a bf16 step of a value of a / 128, so large factors are held
+// more closely than bf16 would, and values below that less, in proportion to what
+// they add to the sum.
+//
+// Bound by HBM: dy and the checkpoint are read once and stay packed in registers
+// between the row's maximum and its codes, where p and q are computed again.
+#include "fused_common.h"
+
+namespace qg {
+namespace {
+
+constexpr float STEPS = 32639.f;   // 127 * 256 + 127
+
+template <int G>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red) {
+#pragma unroll
+    for (int off = G < 64 ? G / 2 : 32; off >= 1; off >>= 1) v = umax(v, (uint32_t)__shfl_xor((int)v, off));
+    if constexpr (G > 64) {
+        if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+        __syncthreads();
+        v = red[0];
+#pragma unroll
+        for (int w = 1; w < G / 64; ++w) v = umax(v, red[w]);
+    }
+    return v;
+}
+
+// Eight codes of a row of n from column c on, those past its end 0.
+__device__ __forceinline__ uint2 load_codes(const int8_t* row, int c, int n) {
+    uint2 r = make_uint2(0u, 0u);
+    if (c + 8 <= n) {
+        __builtin_memcpy(&r, row + c, 8);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t b = c + i < n ? (uint32_t)(uint8_t)row[c + i] : 0u;
+            if (i < 4) r.x |= b << (8 * i);
+            else r.y |= b << (8 * (i - 4));
+        }
+    }
+    return r;
+}
+__device__ __forceinline__ float code_at(uint2 r, int i) {
+    return (float)(int8_t)((i < 4 ? r.x : r.y) >> (8 * (i & 3)));
+}
+
+// G lanes a row, ITER groups of eight columns a lane.  With BIAS a workgroup walks
+// rows and keeps the sums of p of its columns.
+template <typename T, int G, int ITER, bool PAIR, bool BIAS>
+__global__ __launch_bounds__(G < 256 ? 256 : G) void grad_rows_kernel(GradRowsArgs a) {
+    constexpr int RPW = G < 256 ? 256 / G : 1;
+    constexpr int H = PAIR ? 2 : 1;
+    __shared__ uint32_t red[2][G < 64 ? 1 : G / 64];
+    __shared__ float part[BIAS && RPW > 1 ? (RPW - 1) * G * ITER * 8 : 1];
+    const int t = threadIdx.x % G, group = threadIdx.x / G;
+    const int N = a.N, act = a.activation;
+    float db[BIAS ? ITER : 1][8];
+#pragma unroll
+    for (int i = 0; i < (BIAS ? ITER : 1); ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) db[i][e] = 0.f;
+
+    int turn = 0;
+    for (int64_t row0 = (int64_t)blockIdx.x * RPW; row0 < a.M; row0 += (int64_t)gridDim.x * RPW, turn ^= 1) {
+        const int64_t row = row0 + group;
+        const bool live = row < a.M;                   // whole groups; no barrier where a workgroup has several
+        const int64_t r = live ? row : a.M - 1;
+        Pack8<T> yv[ITER];
+        uint2 cv[H][ITER];
+        float cs[H][ITER];
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            const int c = (i * G + t) * 8;
+            if (c + 8 <= N) load8<false>(reinterpret_cast<const T*>(a.dy) + r * a.ldy, c, N, yv[i]);
+            else load8<true>(reinterpret_cast<const T*>(a.dy) + r * a.ldy, c, N, yv[i]);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                if (a.ckpt[h] == nullptr) continue;
+                cv[h][i] = load_codes(a.ckpt[h] + r * a.ld_ckpt, c, N);
+                cs[h][i] = c < N ? a.ckpt_scale[h][r * a.ld_ckpt_scale + c / INT8_BLOCK] : 0.f;
+            }
+        }
+        // The factors of group i, before and after the weight's scale.
+        auto factors = [&](int i, float* p, float* q) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float y = value(yv[i], e);
+                float f = 0.f, slope = 1.f;
+                if (a.ckpt[0] != nullptr) activate_both(act, code_at(cv[0][i], e) * cs[0][i], f, slope);
+                if constexpr (PAIR) {
+                    p[e] = y * (code_at(cv[1][i], e) * cs[1][i]) * slope;
+                    q[e] = y * f;
+                } else {
+                    p[e] = y * slope;
+                }
+            }
+        };
+        auto scaled = [&](int i, float* p, float* q) {
+            const int c = (i * G + t) * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int n = c + e < N ? c + e : N - 1;
+                p[e] *= a.w_scale[0][(int64_t)n * a.ws_stride[0]];
+                if constexpr (PAIR) q[e] *= a.w_scale[1][(int64_t)n * a.ws_stride[1]];
+                if (c + e >= N) p[e] = q[e] = 0.f;
+            }
+        };
+        uint32_t top = 0u;
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            float p[8], q[8];
+            factors(i, p, q);
+            if constexpr (BIAS) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) db[i][e] += live ? p[e] : 0.f;
+            }
+            scaled(i, p, q);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                top = umax(top, abs_bits(p[e]));
+                if constexpr (PAIR) top = umax(top, abs_bits(q[e]));
+            }
+        }
+        top = row_max<G>(top, red[turn]);
+        const bool bad = top >= INF_BITS;
+        const float most = __uint_as_float(top), up = most < 0x1p-90f ? 0x1p60f : 1.0f;   // STEPS / most stays finite
+        const float inv = bad || top == 0u ? 0.f : STEPS / (most * up);
+        if (!live) continue;
+        if (t == 0) {
+            const float s = bad ? __uint_as_float(0x7fc00000u) : most / STEPS;
+            a.row_scale[row] = s;
+            if (a.scales != nullptr) {
+                a.scales[row] = 256.f * s;
+                a.scales[a.M + row] = s;
+                if (row == 0) a.scales[2 * (int64_t)a.M] = 1.f;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            const int c = (i * G + t) * 8;
+            if (c >= a.np) continue;
+            float p[8], q[8];
+            factors(i, p, q);
+            scaled(i, p, q);
+#pragma unroll
+            for (int h = 0; h < H; ++h) {
+                uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float v = h == 0 ? p[e] : q[e];
+                    const int code = bad ? 0 : (int)__builtin_rintf((v * up) * inv);
+                    hi[e / 4] |= ((uint32_t)((code + 128) >> 8) & 0xffu) << (8 * (e & 3));
+                    lo[e / 4] |= ((uint32_t)code & 0xffu) << (8 * (e & 3));
+                }
+                const int64_t at = row * a.ldq + (int64_t)h * a.np + c;
+                *reinterpret_cast<uint2*>(a.hi + at) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2*>(a.lo + at) = make_uint2(lo[0], lo[1]);
+            }
+        }
+    }
+    if constexpr (BIAS) {
+        if constexpr (RPW > 1) {
+            if (group > 0) {
+#pragma unroll
+                for (int i = 0; i < ITER; ++i)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) part[(((group - 1) * ITER + i) * 8 + e) * G + t] = db[i][e];
+            }
+            __syncthreads();
+            if (group > 0) return;
+            for (int g = 0; g < RPW - 1; ++g)
+#pragma unroll
+                for (int i = 0; i < ITER; ++i)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) db[i][e] += part[((g * ITER + i) * 8 + e) * G + t];
+        }
+        float* out = a.part + (int64_t)blockIdx.x * N;
+#pragma unroll
+        for (int i = 0; i < ITER; ++i) {
+            const int c = (i * G + t) * 8;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (c + e < N) out[c + e] = db[i][e];
+        }
+    }
+}
+
+// dbias[n] = sum of the partial rows: 32 columns a workgroup, 32 lanes a column,
+// joined through LDS in a fixed order.
+constexpr int SUM_ROWS = 32;
+__global__ __launch_bounds__(32 * SUM_ROWS) void grad_bias_sum(const float* __restrict__ part, int parts, int n, float* __restrict__ db) {
+    __shared__ float red[SUM_ROWS][33];
+    const int cl = threadIdx.x & 31, q = threadIdx.x >> 5, c = blockIdx.x * 32 + cl;
+    float s = 0.f;
+    if (c < n) {
+#pragma unroll 8
+        for (int p = q; p < parts; p += SUM_ROWS) s += part[(int64_t)p * n + c];
+    }
+    red[q][cl] = s;
+    __syncthreads();
+    if (q == 0 && c < n) {
+#pragma unroll
+        for (int i = 1; i < SUM_ROWS; ++i) s += red[i][cl];
+        db[c] = s;
+    }
+}
+
+template <typename T, bool PAIR, bool BIAS>
+hipError_t by_width(const GradRowsArgs& a, hipStream_t s) {
+    bool done = a.M == 0;
+#define QG_ROWS(G, ITER, LIMIT)                                                                                     \
+    if (!done && a.N <= LIMIT) {                                                                                    \
+        constexpr int RPW = G < 256 ? 256 / G : 1;                                                                  \
+        const int64_t groups = ((int64_t)a.M + RPW - 1) / RPW;                                                      \
+        const unsigned grid = (unsigned)(BIAS ? a.parts : groups < (1 << 20) ? groups : (1 << 20));                 \
+        hipLaunchKernelGGL((grad_rows_kernel<T, G, ITER, PAIR, BIAS>), dim3(grid), dim3(G < 256 ? 256 : G), 0, s, a); \
+        done = true;                                                                                                \
+    }
+    QG_ROWS(64, 1, 512)
+    QG_ROWS(256, 1, 2048)
+    QG_ROWS(256, 2, 4096)
+    QG_ROWS(512, 2, 8192)
+    QG_ROWS(1024, 2, 16384)
+    QG_ROWS(1024, 4, 32768)
+    QG_ROWS(1024, 8, 65536)
+#undef QG_ROWS
+    if (!done) return hipErrorInvalidValue;
+    if constexpr (BIAS)
+        hipLaunchKernelGGL(grad_bias_sum, dim3((unsigned)((a.N + 31) / 32)), dim3(32 * SUM_ROWS), 0, s, a.part, a.M == 0 ? 0 : a.parts,
+                           a.N, a.dbias);
+    return hipGetLastError();
+}
+
+template <typename T>
+hipError_t by_form(const GradRowsArgs& a, bool pair, hipStream_t s) {
+    if (pair) return by_width<T, true, false>(a, s);
+    return a.dbias != nullptr ? by_width<T, false, true>(a, s) : by_width<T, false, false>(a, s);
+}
+
+}  // namespace
+
+// Workgroups of the row kernel where each leaves partial sums of dbias.
+int grad_rows_parts(int64_t M, int64_t N) {
+    const int64_t rows = N <= 512 ? 4 : 1, groups = (M + rows - 1) / rows;
+    return (int)(groups < 512 ? groups : 512);
+}
+
+hipError_t launch_grad_rows(const GradRowsArgs& a, bool pair, bool bf16, hipStream_t s) {
+    return bf16 ? by_form<__bf16>(a, pair, s) : by_form<_Float16>(a, pair, s);
+}
+
+}  // namespace qg

@@ -1,0 +1,66 @@
+// Argument blocks and launchers of the fused A8W8 products, their gradients and
+// the int8 quantiser.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "../../include/qgemm_fused.h"
+
+namespace qg {
+
+constexpr int INT8_BLOCK = 32;   // columns of a checkpoint's block
+
+// What follows a product: out [M,N], of one product or of a gated pair.
+struct Epilogue {
+    int M, N;
+    const float* act_scale; int as_stride;
+    const float* w_scale[2]; int ws_stride[2];
+    const float* bias;                        // NULL: none
+    int activation;
+    const void* res; int64_t ldr;             // NULL: none
+    void* out; int64_t ldo; int out_type;
+    int8_t* ckpt[2]; int64_t ld_ckpt;         // NULL: none
+    float* ckpt_scale[2]; int64_t ld_ckpt_scale;
+};
+
+// The epilogue after products that are in memory as fp32, scales applied.
+// z [rows,N] at a stride of N values, of rows m0 .. m0 + rows - 1.
+hipError_t launch_fused_finish(const Epilogue& e, bool pair, const float* z0, const float* z1, int m0, int rows, hipStream_t s);
+
+// The factors of a gradient, for each row of dy: `hi` and `lo` [M, branches * np]
+// with zeros behind each branch's N, and the row's scale.
+struct GradRowsArgs {
+    int M, N, np;                             // np: N rounded up to 128
+    const void* dy; int64_t ldy;
+    const int8_t* ckpt[2]; int64_t ld_ckpt;   // NULL without an activation
+    const float* ckpt_scale[2]; int64_t ld_ckpt_scale;
+    const float* w_scale[2]; int ws_stride[2];
+    int activation;
+    int8_t* hi; int8_t* lo; int64_t ldq;
+    float* row_scale;                         // [M]
+    float* scales;                            // NULL, or [2M + 1]: 256 s, s and 1, as qgemm_a8w8 takes them
+    float* part; int parts;                   // NULL, or [parts,N] partial sums of dbias
+    float* dbias;
+};
+int grad_rows_parts(int64_t M, int64_t N);
+hipError_t launch_grad_rows(const GradRowsArgs& a, bool pair, bool bf16, hipStream_t s);
+// dx [rows,K] = sum of `count` (2 or 4) fp32 matrices `stride` values apart.
+hipError_t launch_grad_sum(const float* z, int64_t stride, int count, int64_t rows, int64_t K, void* dx, int64_t ld_dx,
+                           bool bf16, hipStream_t s);
+
+struct Int8Args {
+    int64_t M; int64_t n; int block;
+    const void* x; int64_t ldx;               // quantise: values in
+    void* out; int64_t ldo;                   // dequantise: values out
+    int8_t* codes; int64_t ldc;
+    float* scale; int64_t lds;
+};
+hipError_t launch_int8_quantize(const Int8Args& a, qg_dtype type, hipStream_t s);
+hipError_t launch_int8_dequantize(const Int8Args& a, qg_dtype type, hipStream_t s);
+// Clears the ticket words at the head of a product's workspace.
+hipError_t launch_clear(uint32_t* words, int count, hipStream_t s);
+
+// Of api.cpp.
+void record_kernel(const char* name);
+
+}  // namespace qg
