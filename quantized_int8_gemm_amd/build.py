@@ -53,6 +53,9 @@ SOURCES = [
     "mx_tiled_small.hip",
     "mx_decode.hip",
     "mx_api.cpp",
+    "fused_tiled_one.hip",
+    "fused_tiled_pair.hip",
+    "fused_tiled_grad.hip",
     "fused_finish.hip",
     "fused_grad_rows.hip",
     "int8_quantize.hip",

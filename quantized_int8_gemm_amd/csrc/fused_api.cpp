@@ -1,6 +1,7 @@
 // C entry points of qgemm_fused.h: argument checks (before any HIP call), workspace
 // plans, kernel choice and launch, with the launch-status convention of api.cpp.
 #include <algorithm>
+#include <cstdlib>
 
 #include <hip/hip_runtime.h>
 
@@ -61,6 +62,50 @@ struct Through {
     size_t bytes(int count) const { return gemm + z * count; }
 };
 
+int env_int(const char* name, int dflt) {
+    const char* v = std::getenv(name);
+    return v != nullptr && *v ? std::atoi(v) : dflt;
+}
+
+constexpr int THROUGH = qg::FUSED_TILES;   // products through memory
+
+// Rows of whole 16-byte pieces.
+bool whole_pieces(const void* p, int64_t ld, int64_t n) { return aligned(p, 16) && ld % 16 == 0 && n % 16 == 0; }
+
+// The tile for `rows` x `cols` sums over K (a pair's columns and a gradient's rows counted
+// twice), or THROUGH.  QGEMM_FUSED_TILE forces one (tests and tuning), of an ANY tile's
+// shape where the operands need that.
+int pick_tile(int64_t rows, int64_t cols, int64_t K, bool pieces) {
+    auto tiles = [&](int64_t bm, int64_t bn) { return ((rows + bm - 1) / bm) * ((cols + bn - 1) / bn); };
+    const int forced = env_int("QGEMM_FUSED_TILE", -1);
+    int tile = forced;
+    if (forced < 0 || forced > THROUGH) {
+        const int64_t large = tiles(256, 256), small = tiles(128, 128);
+        if (large >= 512 || (large >= 160 && !(large > 256 && large <= 352))) tile = qg::FUSED_256x256;
+        else if (K <= 2048 && small <= 256) tile = qg::FUSED_64x128;
+        else tile = qg::FUSED_128x128;
+    }
+    if (pieces || tile >= qg::FUSED_ANY_128x128) return tile;
+    return tile == qg::FUSED_64x128 ? qg::FUSED_ANY_64x128 : qg::FUSED_ANY_128x128;
+}
+
+hipError_t launch_fused(int form, const qg::FusedArgs& a, int tile, bool kmajor, hipStream_t s) {
+    const qg::FusedTile t = (qg::FusedTile)tile;
+    return form == qg::FUSED_ONE ? qg::launch_fused_one(a, t, kmajor, s)
+           : form == qg::FUSED_PAIR ? qg::launch_fused_pair(a, t, kmajor, s) : qg::launch_fused_grad(a, t, kmajor, s);
+}
+
+const char* tile_name(int form, int tile) {
+    static const char* const names[3][qg::FUSED_TILES] = {
+        {"fused_one_256x256", "fused_one_128x128", "fused_one_64x128", "fused_one_any_128x128", "fused_one_any_64x128"},
+        {"fused_pair_256x256", "fused_pair_128x128", "fused_pair_64x128", "fused_pair_any_128x128", "fused_pair_any_64x128"},
+        {"fused_grad_256x256", "fused_grad_128x128", "fused_grad_64x128", "fused_grad_any_128x128", "fused_grad_any_64x128"}};
+    return names[form][tile];
+}
+
+// A launch holds fewer than 2^32 threads: of the smallest tile's 256.
+bool too_many_tiles(int64_t rows, int64_t cols) { return ((rows + 63) / 64) * ((cols + 127) / 128) >= (int64_t)1 << 24; }
+
 struct Scales { const float* p; int64_t len; };
 
 bool scale_ok(const Scales& s, int64_t n) { return s.p != nullptr && aligned(s.p, 4) && (s.len == 1 || s.len == n); }
@@ -71,6 +116,12 @@ struct Forward {
     const int8_t* A; int64_t lda;
     const int8_t* W[2]; int64_t ldw[2]; int b_trans;
     int pair;
+
+    int tile() const {
+        bool pieces = whole_pieces(A, lda, K);
+        for (int h = 0; h < pair; ++h) pieces = pieces && whole_pieces(W[h], ldw[h], b_trans ? K : N);
+        return pick_tile(M, N * pair, K, pieces);
+    }
 };
 
 bool sizes_bad(int64_t M, int64_t N, int64_t K) {
@@ -78,7 +129,7 @@ bool sizes_bad(int64_t M, int64_t N, int64_t K) {
 }
 
 size_t forward_workspace(const Forward& f) {
-    if (sizes_bad(f.M, f.N, f.K) || f.M == 0 || f.N == 0 || f.K == 0) return 0;
+    if (sizes_bad(f.M, f.N, f.K) || f.M == 0 || f.N == 0 || f.K == 0 || f.tile() != THROUGH) return 0;
     return Through(f.M, f.N, f.K, f.pair).bytes(f.pair);
 }
 
@@ -104,6 +155,7 @@ qg_status forward(const Forward& f, const Scales& act, const Scales* ws, const f
     if (workspace != nullptr && !aligned(workspace, 256)) return QG_ERR_INVALID_ARGUMENT;
     for (int h = 0; h < f.pair; ++h)
         if (!span_ok(K, f.lda, f.ldw[h], f.b_trans)) return QG_ERR_UNSUPPORTED;
+    if (too_many_tiles(M, N * f.pair)) return QG_ERR_UNSUPPORTED;
     const size_t need = forward_workspace(f);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return QG_ERR_WORKSPACE;
 
@@ -125,6 +177,18 @@ qg_status forward(const Forward& f, const Scales& act, const Scales* ws, const f
     (void)hipGetLastError();
     const hipStream_t s = (hipStream_t)stream;
 
+    const int tile = f.tile(), form = f.pair == 2 ? qg::FUSED_PAIR : qg::FUSED_ONE;
+    if (tile != THROUGH) {
+        qg::FusedArgs a{};
+        a.e = e;
+        a.A[0] = f.A; a.lda = f.lda;
+        for (int h = 0; h < f.pair; ++h) {
+            a.B[h] = f.W[h];
+            a.ldb[h] = f.ldw[h];
+        }
+        a.K = (int)K; a.branches = 1;
+        return done(launch_fused(form, a, tile, f.b_trans != 0, s), tile_name(form, tile));
+    }
     const Through t(M, N, K, f.pair);
     char* const z = (char*)workspace + t.gemm;
     if (t.gemm > 0) QG_TRY_HIP(qg::launch_clear((uint32_t*)workspace, qg::SKINNY_MAX_TICKETS, s));
@@ -145,26 +209,33 @@ struct Backward {
     const int8_t* W[2]; int64_t ldw[2]; int b_trans;
     int pair;
     bool with_bias;
+
+    int tile() const {
+        bool pieces = true;
+        for (int h = 0; h < pair; ++h) pieces = pieces && whole_pieces(W[h], ldw[h], b_trans ? K : N);
+        return pick_tile(2 * M, K, N * pair, pieces);
+    }
 };
 
 // Where a gradient's workspace holds what.
 struct GradPlan {
     int64_t np, ldq;
     size_t hi, lo, row_scale, scales, part, gemm, z, bytes;
-    int parts;
+    int parts, tile;
     Through t;
     explicit GradPlan(const Backward& b)
-        : np((b.N + 127) / 128 * 128), ldq(np * b.pair), parts(b.with_bias ? qg::grad_rows_parts(b.M, b.N) : 0),
+        : np((b.N + 127) / 128 * 128), ldq(np * b.pair), parts(b.with_bias ? qg::grad_rows_parts(b.M, b.N) : 0), tile(b.tile()),
           t(b.M, b.K, b.N, 2 * b.pair) {
+        const bool through = tile == THROUGH;
         size_t at = 0;
         auto take = [&](size_t n) { const size_t here = at; at += up256(n); return here; };
-        gemm = take(t.gemm);
+        gemm = take(through ? t.gemm : 0);
         hi = take((size_t)b.M * ldq);
         lo = take((size_t)b.M * ldq);
         row_scale = take((size_t)b.M * 4);
-        scales = take((size_t)(2 * b.M + 1) * 4);
+        scales = take(through ? (size_t)(2 * b.M + 1) * 4 : 0);
         part = take((size_t)parts * b.N * 4);
-        z = take(t.z * 2 * b.pair);
+        z = take(through ? t.z * 2 * b.pair : 0);
         bytes = at;
     }
 };
@@ -201,6 +272,7 @@ qg_status backward(const Backward& b, const void* dy, qg_dtype dtype, int64_t ld
     const GradPlan p(b);
     for (int h = 0; h < b.pair; ++h)
         if (!span_ok(N, p.ldq, b.ldw[h], !b.b_trans)) return QG_ERR_UNSUPPORTED;
+    if (too_many_tiles(2 * M, K)) return QG_ERR_UNSUPPORTED;
     if (workspace == nullptr || workspace_bytes < p.bytes) return QG_ERR_WORKSPACE;
     (void)hipGetLastError();
     const hipStream_t s = (hipStream_t)stream;
@@ -221,11 +293,24 @@ qg_status backward(const Backward& b, const void* dy, qg_dtype dtype, int64_t ld
     a.activation = activation;
     a.hi = (int8_t*)(w + p.hi); a.lo = (int8_t*)(w + p.lo); a.ldq = p.ldq;
     a.row_scale = (float*)(w + p.row_scale);
-    a.scales = (float*)(w + p.scales);
+    a.scales = p.tile == THROUGH ? (float*)(w + p.scales) : nullptr;
     a.part = (float*)(w + p.part); a.parts = p.parts;
     a.dbias = dbias;
     QG_TRY_HIP(qg::launch_grad_rows(a, b.pair == 2, dtype == QG_BF16, s));
 
+    if (p.tile != THROUGH) {
+        qg::FusedArgs f{};
+        f.e.M = (int)M; f.e.N = (int)K;
+        f.e.act_scale = a.row_scale; f.e.as_stride = 1;
+        f.e.out = dx; f.e.ldo = ld_dx; f.e.out_type = dtype;
+        f.A[0] = a.hi; f.A[1] = a.lo; f.lda = p.ldq;
+        for (int h = 0; h < b.pair; ++h) {
+            f.B[h] = b.W[h];
+            f.ldb[h] = b.ldw[h];
+        }
+        f.K = (int)N; f.branches = b.pair;
+        return done(launch_fused(qg::FUSED_GRAD, f, p.tile, b.b_trans == 0, s), tile_name(qg::FUSED_GRAD, p.tile));
+    }
     if (p.t.gemm > 0) QG_TRY_HIP(qg::launch_clear((uint32_t*)(w + p.gemm), qg::SKINNY_MAX_TICKETS, s));
     for (int64_t m = 0; m < M; m += p.t.rows) {
         const int64_t rows = std::min(p.t.rows, M - m);

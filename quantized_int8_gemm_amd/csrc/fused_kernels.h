@@ -23,6 +23,23 @@ struct Epilogue {
     float* ckpt_scale[2]; int64_t ld_ckpt_scale;
 };
 
+// A tiled product with its epilogue: one (A [M,K], B the weight), a pair (B[0] gate, B[1]
+// up), or a gradient (A the planes hi and lo [M, branches * np], B the branches' weights,
+// K the forward call's N, e.N its K, e.act_scale the rows' scales).
+enum { FUSED_ONE = 0, FUSED_PAIR = 1, FUSED_GRAD = 2 };
+struct FusedArgs {
+    Epilogue e;
+    const int8_t* A[2]; int64_t lda;
+    const int8_t* B[2]; int64_t ldb[2];
+    int K, branches;
+};
+// Rows and columns of sums of a tile; the ANY tiles take operands of any alignment.
+enum FusedTile { FUSED_256x256, FUSED_128x128, FUSED_64x128, FUSED_ANY_128x128, FUSED_ANY_64x128, FUSED_TILES };
+// kmajor: B's rows lie along the sum.
+hipError_t launch_fused_one(const FusedArgs& a, FusedTile tile, bool kmajor, hipStream_t s);
+hipError_t launch_fused_pair(const FusedArgs& a, FusedTile tile, bool kmajor, hipStream_t s);
+hipError_t launch_fused_grad(const FusedArgs& a, FusedTile tile, bool kmajor, hipStream_t s);
+
 // The epilogue after products that are in memory as fp32, scales applied.
 // z [rows,N] at a stride of N values, of rows m0 .. m0 + rows - 1.
 hipError_t launch_fused_finish(const Epilogue& e, bool pair, const float* z0, const float* z1, int m0, int rows, hipStream_t s);

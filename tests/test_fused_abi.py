@@ -109,8 +109,9 @@ def test_quantisers_reject_their_own():
         assert call("int8_dequantize", DEQUANT, kw) == code
 
 
-def test_a_short_workspace_is_refused():
-    """Rows that are not whole 16-byte pieces go through memory."""
+def test_a_short_workspace_is_refused(monkeypatch):
+    """Products through memory, and a gradient's factors."""
+    monkeypatch.setenv("QGEMM_FUSED_TILE", "5")
     kw = dict(LINEAR, K=47, lda=47)
     need = b.lib.qgemm_a8w8_linear_workspace_bytes(4, 40, 47, FAKE, 47, FAKE, 40, 0)
     assert need > 0

@@ -7,7 +7,7 @@ import torch
 
 import fused_reference as ref
 import quantized_int8_gemm_amd as q
-from gpu_util import case, dev
+from gpu_util import case, dev, env
 
 pytestmark = pytest.mark.gpu
 
@@ -185,3 +185,49 @@ def test_outputs_without_elements():
     assert out.shape == (4, 0) and codes.shape == (2, 4, 0) and scale.shape == (2, 4, 0)
     with pytest.raises(ValueError):
         q.qgemm_a8w8_linear(gpu(a)[:, :0], gpu(w)[:, :0], gpu(sa), gpu(sw), b_trans=True)
+
+
+TILES = {0: "256x256", 1: "128x128", 2: "64x128", 3: "any_128x128", 4: "any_64x128"}
+
+
+@pytest.mark.parametrize("b_trans", [True, False])
+@pytest.mark.parametrize("tile", range(6))
+def test_every_tile_gives_the_same_bits(tile, b_trans):
+    """Sums are exact and the epilogue is one, so outputs and checkpoints do not depend on
+    the kernel (5: products through memory)."""
+    for m, n, k in ((1, 16, 16), (33, 48, 80), (64, 128, 128), (300, 272, 400), (515, 528, 1040)):
+        case(f"tile {tile} {m} {n} {k} b_trans={b_trans}")
+        a, (wg, wu), sa, (sg, su) = inputs(m, n, k, m + n, 2)
+        args = (gpu(a), laid(wg, b_trans), laid(wu, b_trans), gpu(sa), gpu(sg), gpu(su))
+        res = torch.randn(m, n, device=dev()).half()
+        kw = dict(b_trans=b_trans, checkpoint=True)
+
+        def run():
+            y = q.qgemm_a8w8_gated(*args, out_dtype=torch.bfloat16, **kw)
+            first = q.last_kernel()
+            z = q.qgemm_a8w8_linear(args[0], args[1], args[3], args[4], residual=res, activation="gelu", out_dtype=torch.float16, **kw)
+            return (y[0], *y[1], z[0], *z[1]), first, q.last_kernel()
+
+        with env(QGEMM_FUSED_TILE=5):
+            want, first, second = run()
+            assert first == second == "a8w8_then_finish"
+        with env(QGEMM_FUSED_TILE=tile):
+            got, first, second = run()
+            if tile < 5:
+                assert first == "fused_pair_" + TILES[tile] and second == "fused_one_" + TILES[tile]
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("tile", range(5))
+def test_what_lies_past_k_adds_nothing(tile):
+    """Rows longer than K, with other values behind K, and a K that ends inside a chunk."""
+    m, n = 70, 144
+    for k in (16, 48, 144, 272):
+        a, (w, _), sa, (sw, _) = inputs(m, n, 512, k, 2)
+        A, W = gpu(a), gpu(w)
+        with env(QGEMM_FUSED_TILE=tile):
+            got = q.qgemm_a8w8_linear(A[:, :k], W[:, :k], gpu(sa), gpu(sw), b_trans=True)
+            also = q.qgemm_a8w8_linear(A[:, :k], W.t().contiguous()[:k], gpu(sa), gpu(sw))
+        want = ref.z32(ref.accumulate(a[:, :k], w[:, :k], True), sa, sw)
+        assert np.array_equal(got.cpu().numpy(), want) and torch.equal(got, also)
