@@ -23,7 +23,9 @@ __global__ __launch_bounds__(NT) void fused_finish_kernel(Epilogue e, const floa
     if constexpr (PAIR) b = load4(z1, row * e.N + n, QG_FP32, count);
     v4f bias = {0.f, 0.f, 0.f, 0.f};
     if (!PAIR && e.bias != nullptr) bias = load4(e.bias, n, QG_FP32, count);
-    finish4<PAIR>(e, live ? m0 + (int)row : e.M, n, a, b, bias);
+    Raw4 res = {};
+    if (!PAIR && e.res != nullptr && live) res = load_raw4(e.res, (m0 + row) * e.ldr + n, e.out_type, count);
+    finish4<PAIR>(e, live ? m0 + (int)row : e.M, n, a, b, bias, res);
 }
 
 __global__ __launch_bounds__(NT) void grad_sum_kernel(const float* __restrict__ z, int64_t stride, int count, int64_t rows, int K,

@@ -54,16 +54,34 @@ __device__ __forceinline__ float code_at(uint2 r, int i) {
     return (float)(int8_t)((i < 4 ? r.x : r.y) >> (8 * (i & 3)));
 }
 
+// A weight's scales of columns c .. c + 7, 0 past the last.
+__device__ __forceinline__ void load_scales(const float* w, int stride, int c, int n, float* s) {
+    if (stride == 0) {
+        const float one = w[0];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = c + e < n ? one : 0.f;
+    } else {
+        Pack8<float> v;
+        if (c + 8 <= n) load8<false>(w, c, n, v);
+        else load8<true>(w, c, n, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = value(v, e);
+    }
+}
+
 // G lanes a row, ITER groups of eight columns a lane.  With BIAS a workgroup walks
-// rows and keeps the sums of p of its columns.
+// rows and keeps the sums of p of its columns.  HOLD, up to two groups a lane: the
+// factors stay in registers between the row's maximum and their codes; wider rows
+// keep what they were read from and compute them again.
 template <typename T, int G, int ITER, bool PAIR, bool BIAS>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void grad_rows_kernel(GradRowsArgs a) {
     constexpr int RPW = G < 256 ? 256 / G : 1;
     constexpr int H = PAIR ? 2 : 1;
+    constexpr bool HOLD = ITER <= 2;
     __shared__ uint32_t red[2][G < 64 ? 1 : G / 64];
     __shared__ float part[BIAS && RPW > 1 ? (RPW - 1) * G * ITER * 8 : 1];
     const int t = threadIdx.x % G, group = threadIdx.x / G;
-    const int N = a.N, act = a.activation;
+    const int N = a.N;
     float db[BIAS ? ITER : 1][8];
 #pragma unroll
     for (int i = 0; i < (BIAS ? ITER : 1); ++i)
@@ -90,46 +108,51 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void grad_rows_kernel(GradRowsAr
                 cs[h][i] = c < N ? a.ckpt_scale[h][r * a.ld_ckpt_scale + c / INT8_BLOCK] : 0.f;
             }
         }
-        // The factors of group i, before and after the weight's scale.
-        auto factors = [&](int i, float* p, float* q) {
+        // The factors of group i with the weight's scales; dy is 0 past the last column.
+        auto factors = [&](int i, float (*v)[8], bool first) {
+            if (a.ckpt[0] == nullptr) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const float y = value(yv[i], e);
-                float f = 0.f, slope = 1.f;
-                if (a.ckpt[0] != nullptr) activate_both(act, code_at(cv[0][i], e) * cs[0][i], f, slope);
-                if constexpr (PAIR) {
-                    p[e] = y * (code_at(cv[1][i], e) * cs[1][i]) * slope;
-                    q[e] = y * f;
-                } else {
-                    p[e] = y * slope;
+                for (int e = 0; e < 8; ++e) v[0][e] = value(yv[i], e);
+            } else {
+                with_activation(a.activation, [&](auto kind) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        float f, slope;
+                        activate_both<decltype(kind)::value>(code_at(cv[0][i], e) * cs[0][i], f, slope);
+                        const float y = value(yv[i], e);
+                        if constexpr (PAIR) {
+                            v[0][e] = y * (code_at(cv[1][i], e) * cs[1][i]) * slope;
+                            v[1][e] = y * f;
+                        } else {
+                            v[0][e] = y * slope;
+                        }
+                    }
+                });
+            }
+            if constexpr (BIAS) {
+                if (first) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) db[i][e] += live ? v[0][e] : 0.f;
                 }
             }
-        };
-        auto scaled = [&](int i, float* p, float* q) {
-            const int c = (i * G + t) * 8;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int n = c + e < N ? c + e : N - 1;
-                p[e] *= a.w_scale[0][(int64_t)n * a.ws_stride[0]];
-                if constexpr (PAIR) q[e] *= a.w_scale[1][(int64_t)n * a.ws_stride[1]];
-                if (c + e >= N) p[e] = q[e] = 0.f;
+            for (int h = 0; h < H; ++h) {
+                float s[8];
+                load_scales(a.w_scale[h], a.ws_stride[h], (i * G + t) * 8, N, s);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) v[h][e] *= s[e];
             }
         };
+        float held[HOLD ? ITER : 1][H][8];
         uint32_t top = 0u;
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
-            float p[8], q[8];
-            factors(i, p, q);
-            if constexpr (BIAS) {
+            float (*v)[8] = held[HOLD ? i : 0];
+            factors(i, v, true);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) db[i][e] += live ? p[e] : 0.f;
-            }
-            scaled(i, p, q);
+            for (int h = 0; h < H; ++h)
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                top = umax(top, abs_bits(p[e]));
-                if constexpr (PAIR) top = umax(top, abs_bits(q[e]));
-            }
+                for (int e = 0; e < 8; ++e) top = umax(top, abs_bits(v[h][e]));
         }
         top = row_max<G>(top, red[turn]);
         const bool bad = top >= INF_BITS;
@@ -149,16 +172,14 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void grad_rows_kernel(GradRowsAr
         for (int i = 0; i < ITER; ++i) {
             const int c = (i * G + t) * 8;
             if (c >= a.np) continue;
-            float p[8], q[8];
-            factors(i, p, q);
-            scaled(i, p, q);
+            float (*v)[8] = held[HOLD ? i : 0];
+            if constexpr (!HOLD) factors(i, v, false);
 #pragma unroll
             for (int h = 0; h < H; ++h) {
                 uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    const float v = h == 0 ? p[e] : q[e];
-                    const int code = bad ? 0 : (int)__builtin_rintf((v * up) * inv);
+                    const int code = bad ? 0 : (int)__builtin_rintf((v[h][e] * up) * inv);
                     hi[e / 4] |= ((uint32_t)((code + 128) >> 8) & 0xffu) << (8 * (e & 3));
                     lo[e / 4] |= ((uint32_t)code & 0xffu) << (8 * (e & 3));
                 }

@@ -46,17 +46,29 @@ __device__ __forceinline__ int kn_slot_of(int r, int s) {
     else return dma::kn_slot<RB>(r, s);
 }
 
-// 16 bytes from column c of a row of `limit` on, zeros past its end.
+// 16 bytes from column c of a row of `limit` on, zeros past its end (limit 0: no load).
+// Where they would pass the end, the row's last 16 are read and moved down.
 __device__ __forceinline__ u32x4 load16_any(const int8_t* row, int c, int limit) {
-    if (c + 16 <= limit) {
-        const v4i_any v = *reinterpret_cast<const v4i_any*>(row + c);
-        return u32x4{(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]};
+    const int past = c + 16 - limit;
+    if (past >= 16) return u32x4{0u, 0u, 0u, 0u};
+    if (limit >= 16) {
+        const v4i_any v = *reinterpret_cast<const v4i_any*>(row + (past > 0 ? limit - 16 : c));
+        uint32_t w[5] = {(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3], 0u};
+        if (past > 0) {
+#pragma unroll
+            for (int d = 2; d >= 1; d /= 2)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = past & 4 * d ? (i + d < 4 ? w[i + d] : 0u) : w[i];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_alignbyte(w[i + 1], w[i], (uint32_t)past & 3u);
+        }
+        return u32x4{w[0], w[1], w[2], w[3]};
     }
     uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if (c < limit) {
+    for (int i = 0; c + i < limit; ++i) {
+        const uint32_t b = (uint32_t)(uint8_t)row[c + i] << (8 * (i & 3));
 #pragma unroll
-        for (int i = 0; i < 15; ++i)
-            if (c + i < limit) w[i / 4] |= (uint32_t)(uint8_t)row[c + i] << (8 * (i & 3));
+        for (int q = 0; q < 4; ++q) w[q] |= i / 4 == q ? b : 0u;
     }
     return u32x4{w[0], w[1], w[2], w[3]};
 }
@@ -179,8 +191,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
                 } else {
                     const int o = (q * ROUND) % (BK * RB) + wave * 1024 + lane * 16;
                     const int r = o / RB, k = kc * BK + r;
-                    br[q] = load16_any(b_base(h) + (int64_t)(k < K ? k : 0) * p.ldb[h], 16 * kn_slot_of<RB>(r, (o % RB) / 16),
-                                       k < K ? cols_b : 0);
+                    br[q] = load16_any(p.B[h] + (int64_t)(k < K ? k : 0) * p.ldb[h], n0 + 16 * kn_slot_of<RB>(r, (o % RB) / 16),
+                                       k < K ? N : 0);
                 }
             }
         }
@@ -280,6 +292,23 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
             for (int i = 0; i < 4; ++i) ws[h][i] = i < count ? p.e.w_scale[h][(int64_t)(n + i) * p.e.ws_stride[h]] : 0.f;
         if (!PAIR && p.e.bias != nullptr) bias = load4(p.e.bias, n, QG_FP32, count);
     }
+    // What a row needs beside its sums, U rows ahead: a residual read where it is used would
+    // cost a memory latency a row, which nothing covers (8192 x 8192 x 8192, bf16: 547 us).
+    constexpr int TURNS = PR / ROWS_AT_ONCE, U = TURNS < 4 ? TURNS : 4;
+    Raw4 res_next[U];
+    float as_next[U];
+    auto fetch = [&](int pass, int q0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int m = m0 + pass * PR + (q0 + u) * ROWS_AT_ONCE + tid / CPT;
+            res_next[u] = Raw4{};
+            as_next[u] = 0.f;
+            if (m >= M) continue;
+            as_next[u] = p.e.act_scale[(int64_t)m * p.e.as_stride];
+            if (MODE == FUSED_ONE && p.e.res != nullptr) res_next[u] = load_raw4(p.e.res, (int64_t)m * p.e.ldr + n, p.e.out_type, count);
+        }
+    };
+    fetch(0, 0);
     int* const stage = reinterpret_cast<int*>(smem);
     __syncthreads();   // every wave has read the last chunk
 #pragma unroll
@@ -297,28 +326,39 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
                 }
         }
         __syncthreads();
-#pragma unroll 2
-        for (int q = 0; q < PR / ROWS_AT_ONCE; ++q) {
-            const int rr = q * ROWS_AT_ONCE + tid / CPT, m = m0 + pass * PR + rr;
-            const int at = rr * BNR + ((c4 ^ (rr & 15)) << 2);
-            const v4i s0 = *reinterpret_cast<const v4i*>(stage + at);
-            const float as = m < M ? p.e.act_scale[(int64_t)m * p.e.as_stride] : 0.f;
-            if constexpr (GRAD) {
-                const v4i s1 = *reinterpret_cast<const v4i*>(stage + PR * BNR + at);
-                v4f v;
+#pragma unroll 1
+        for (int q0 = 0; q0 < TURNS; q0 += U) {
+            Raw4 res[U];
+            float as[U];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf((float)s0[i], 256.f, (float)s1[i]) * as;
-                if (m < M && count > 0) store4(p.e.out, (int64_t)m * p.e.ldo + n, p.e.out_type, count, v);
-            } else {
-                v4f z0, z1 = {0.f, 0.f, 0.f, 0.f};
+            for (int u = 0; u < U; ++u) {
+                res[u] = res_next[u];
+                as[u] = as_next[u];
+            }
+            if (q0 + U < TURNS) fetch(pass, q0 + U);
+            else if (pass + 1 < PASSES) fetch(pass + 1, 0);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) z0[i] = (float)s0[i] * as * ws[0][i];
-                if constexpr (PAIR) {
+            for (int u = 0; u < U; ++u) {
+                const int rr = (q0 + u) * ROWS_AT_ONCE + tid / CPT, m = m0 + pass * PR + rr;
+                const int at = rr * BNR + ((c4 ^ (rr & 15)) << 2);
+                const v4i s0 = *reinterpret_cast<const v4i*>(stage + at);
+                if constexpr (GRAD) {
                     const v4i s1 = *reinterpret_cast<const v4i*>(stage + PR * BNR + at);
+                    v4f v;
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) z1[i] = (float)s1[i] * as * ws[1][i];
+                    for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf((float)s0[i], 256.f, (float)s1[i]) * as[u];
+                    if (m < M && count > 0) store4(p.e.out, (int64_t)m * p.e.ldo + n, p.e.out_type, count, v);
+                } else {
+                    v4f z0, z1 = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) z0[i] = (float)s0[i] * as[u] * ws[0][i];
+                    if constexpr (PAIR) {
+                        const v4i s1 = *reinterpret_cast<const v4i*>(stage + PR * BNR + at);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) z1[i] = (float)s1[i] * as[u] * ws[1][i];
+                    }
+                    finish4<PAIR>(p.e, m, n, z0, z1, bias, res[u]);
                 }
-                finish4<PAIR>(p.e, m, n, z0, z1, bias);
             }
         }
     }

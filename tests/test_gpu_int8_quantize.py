@@ -96,3 +96,19 @@ def test_offsets_past_32_bits():
         assert torch.equal(codes[-2:], c2) and torch.equal(scale[-2:], s2) and (codes[:-2] == 0).all()
         back = q.int8_dequantize(codes, scale)
         assert torch.equal(back[-2:], q.int8_dequantize(c2, s2)) and (back[:-2] == 0).all()
+
+
+def test_every_mantissa():
+    """The largest magnitude takes every mantissa, at several exponents: codes of it and of
+    its half, and the scale, as the division gives them."""
+    m = torch.arange(1 << 23, device=dev(), dtype=torch.int32)
+    for e in (0, 27, 28, 90, 127, 128, 200, 247, 248, 254):
+        top = (m | (e << 23)).view(torch.float32)
+        x = torch.stack([top, -top * 0.5, top * 0.3, top * 0.77], 1).contiguous()
+        codes, scale = q.int8_quantize(x)
+        t, y = top.cpu().numpy(), x.cpu().numpy()
+        up = np.where(t < np.float32(2.0 ** -100), np.float32(2.0 ** 60), np.float32(1))
+        with np.errstate(divide="ignore"):
+            inv = np.where(t > 0, np.float32(127) / (t * up), np.float32(0))
+        assert np.array_equal(scale.cpu().numpy(), np.where(t > 0, t / np.float32(127), np.float32(1)))
+        assert np.array_equal(codes.cpu().numpy(), np.rint((y * up[:, None]) * inv[:, None]).astype(np.int8))
