@@ -6,13 +6,11 @@
 #include <hip/hip_runtime.h>
 
 #include "fused_kernels.h"
-#include "kernels.h"
 
 namespace {
 
 constexpr int64_t LIM = (int64_t)1 << 30;
 constexpr int64_t SPAN_LIMIT = (int64_t)1 << 31;   // 32-bit buffer offsets
-constexpr size_t Z_BYTES = (size_t)1 << 28;        // fp32 products in memory at once, about
 
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 bool is_float(qg_dtype t) { return t == QG_FP32 || t == QG_BF16 || t == QG_FP16; }
@@ -31,11 +29,6 @@ qg_status done(hipError_t e, const char* name) {
     return QG_OK;
 }
 
-#define QG_TRY(call)                                   \
-    do {                                               \
-        const qg_status st_ = (call);                  \
-        if (st_ != QG_OK) return st_;                  \
-    } while (0)
 #define QG_TRY_HIP(call)                               \
     do {                                               \
         if ((call) != hipSuccess) return QG_ERR_HIP;   \
@@ -46,47 +39,44 @@ bool span_ok(int64_t K, int64_t lda, int64_t ldw, int b_trans) {
     return 256 * lda + K + 256 < SPAN_LIMIT && (b_trans ? 256 * ldw + K + 256 : (K + 256) * ldw) < SPAN_LIMIT;
 }
 
-// Products through memory: `count` fp32 matrices of `rows` rows at a time, and the
-// workspace of the products' own kernels.
-struct Through {
-    int64_t rows;
-    size_t z, gemm;   // bytes of one matrix, of the kernels' workspace
-    Through(int64_t M, int64_t N, int64_t K, int count) {
-        const int64_t fit = (int64_t)(Z_BYTES / ((size_t)N * 4 * count)) / 256 * 256;
-        rows = std::min(M, std::max<int64_t>(fit, 256));
-        z = up256((size_t)rows * N * 4);
-        gemm = qgemm_workspace_bytes(QG_OP_A8W8, 1, rows, N, K);
-        if (M % rows != 0) gemm = std::max(gemm, qgemm_workspace_bytes(QG_OP_A8W8, 1, M % rows, N, K));
-        gemm = up256(gemm);
-    }
-    size_t bytes(int count) const { return gemm + z * count; }
-};
-
 int env_int(const char* name, int dflt) {
     const char* v = std::getenv(name);
     return v != nullptr && *v ? std::atoi(v) : dflt;
 }
 
-constexpr int THROUGH = qg::FUSED_TILES;   // products through memory
-
 // Rows of whole 16-byte pieces.
 bool whole_pieces(const void* p, int64_t ld, int64_t n) { return aligned(p, 16) && ld % 16 == 0 && n % 16 == 0; }
 
-// The tile for `rows` x `cols` sums over K (a pair's columns and a gradient's rows counted
-// twice), or THROUGH.  QGEMM_FUSED_TILE forces one (tests and tuning), of an ANY tile's
-// shape where the operands need that.
-int pick_tile(int64_t rows, int64_t cols, int64_t K, bool pieces) {
+// How a product runs: its tile, and in how many parts K is divided.
+struct Choice {
+    int tile, splits, split_chunks;
+    size_t bytes;          // of their sums
+    int64_t ld_partial;
+};
+
+// For `rows` x `cols` sums over `chunks` chunks of K (a pair's columns and a gradient's rows
+// counted twice), out_cols columns of the output.  QGEMM_FUSED_TILE and QGEMM_FUSED_SPLITS force a
+// tile (of an ANY tile's shape where the operands need that) and a number of parts, for
+// tests and tuning.
+Choice choose(int64_t rows, int64_t cols, int64_t chunks, int64_t out_cols, bool pieces) {
     auto tiles = [&](int64_t bm, int64_t bn) { return ((rows + bm - 1) / bm) * ((cols + bn - 1) / bn); };
     const int forced = env_int("QGEMM_FUSED_TILE", -1);
-    int tile = forced;
-    if (forced < 0 || forced > THROUGH) {
+    Choice c{forced, 1, 0, 0, (out_cols + 3) / 4 * 4};
+    if (forced < 0 || forced >= qg::FUSED_TILES) {
         const int64_t large = tiles(256, 256), small = tiles(128, 128);
-        if (large >= 512 || (large >= 160 && !(large > 256 && large <= 352))) tile = qg::FUSED_256x256;
-        else if (K <= 2048 && small <= 256) tile = qg::FUSED_64x128;
-        else tile = qg::FUSED_128x128;
+        if (large >= 512 || (large >= 160 && !(large > 256 && large <= 352))) c.tile = qg::FUSED_256x256;
+        else if (chunks <= 16 && small <= 256) c.tile = qg::FUSED_64x128;
+        else c.tile = qg::FUSED_128x128;
     }
-    if (pieces || tile >= qg::FUSED_ANY_128x128) return tile;
-    return tile == qg::FUSED_64x128 ? qg::FUSED_ANY_64x128 : qg::FUSED_ANY_128x128;
+    if (!pieces && c.tile < qg::FUSED_ANY_128x128)
+        c.tile = c.tile == qg::FUSED_64x128 || c.tile == qg::FUSED_64x128_DEEP ? qg::FUSED_ANY_64x128 : qg::FUSED_ANY_128x128;
+    const int64_t want = std::min<int64_t>(env_int("QGEMM_FUSED_SPLITS", 1), chunks);
+    if (want > 1) {
+        c.split_chunks = (int)((chunks + want - 1) / want);
+        c.splits = (int)((chunks + c.split_chunks - 1) / c.split_chunks);
+        c.bytes = (size_t)c.splits * (size_t)(rows * cols / out_cols) * c.ld_partial * 4;
+    }
+    return c;
 }
 
 hipError_t launch_fused(int form, const qg::FusedArgs& a, int tile, bool kmajor, hipStream_t s) {
@@ -95,12 +85,29 @@ hipError_t launch_fused(int form, const qg::FusedArgs& a, int tile, bool kmajor,
            : form == qg::FUSED_PAIR ? qg::launch_fused_pair(a, t, kmajor, s) : qg::launch_fused_grad(a, t, kmajor, s);
 }
 
-const char* tile_name(int form, int tile) {
+const char* kernel_name(int form, const Choice& c) {
     static const char* const names[3][qg::FUSED_TILES] = {
-        {"fused_one_256x256", "fused_one_128x128", "fused_one_64x128", "fused_one_any_128x128", "fused_one_any_64x128"},
-        {"fused_pair_256x256", "fused_pair_128x128", "fused_pair_64x128", "fused_pair_any_128x128", "fused_pair_any_64x128"},
-        {"fused_grad_256x256", "fused_grad_128x128", "fused_grad_64x128", "fused_grad_any_128x128", "fused_grad_any_64x128"}};
-    return names[form][tile];
+        {"fused_one_256x256", "fused_one_128x128", "fused_one_128x128_deep", "fused_one_64x128", "fused_one_64x128_deep",
+         "fused_one_any_128x128", "fused_one_any_64x128"},
+        {"fused_pair_256x256", "fused_pair_128x128", "fused_pair_128x128_deep", "fused_pair_64x128", "fused_pair_64x128_deep",
+         "fused_pair_any_128x128", "fused_pair_any_64x128"},
+        {"fused_grad_256x256", "fused_grad_128x128", "fused_grad_128x128_deep", "fused_grad_64x128", "fused_grad_64x128_deep",
+         "fused_grad_any_128x128", "fused_grad_any_64x128"}};
+    static const char* const joined[3] = {"fused_one_joined", "fused_pair_joined", "fused_grad_joined"};
+    return c.splits > 1 ? joined[form] : names[form][c.tile];
+}
+
+// The product, and the second kernel where K is divided.
+qg_status run(int form, qg::FusedArgs& a, const Choice& c, bool kmajor, void* partial, hipStream_t s) {
+    if (c.splits > 1) {
+        a.partial = (int*)partial;
+        a.splits = c.splits;
+        a.split_chunks = c.split_chunks;
+        a.ld_partial = c.ld_partial;
+    }
+    QG_TRY_HIP(launch_fused(form, a, c.tile, kmajor, s));
+    if (c.splits > 1) QG_TRY_HIP(qg::launch_fused_join(a, form, s));
+    return done(hipSuccess, kernel_name(form, c));
 }
 
 // A launch holds fewer than 2^32 threads: of the smallest tile's 256.
@@ -117,10 +124,10 @@ struct Forward {
     const int8_t* W[2]; int64_t ldw[2]; int b_trans;
     int pair;
 
-    int tile() const {
+    Choice choice() const {
         bool pieces = whole_pieces(A, lda, K);
         for (int h = 0; h < pair; ++h) pieces = pieces && whole_pieces(W[h], ldw[h], b_trans ? K : N);
-        return pick_tile(M, N * pair, K, pieces);
+        return choose(M, N * pair, (K + 127) / 128, N, pieces);
     }
 };
 
@@ -129,8 +136,8 @@ bool sizes_bad(int64_t M, int64_t N, int64_t K) {
 }
 
 size_t forward_workspace(const Forward& f) {
-    if (sizes_bad(f.M, f.N, f.K) || f.M == 0 || f.N == 0 || f.K == 0 || f.tile() != THROUGH) return 0;
-    return Through(f.M, f.N, f.K, f.pair).bytes(f.pair);
+    if (sizes_bad(f.M, f.N, f.K) || f.M == 0 || f.N == 0 || f.K == 0) return 0;
+    return up256(f.choice().bytes);
 }
 
 bool checkpoint_ok(const int8_t* c, int64_t ldc, const float* s, int64_t lds, int64_t N) {
@@ -156,8 +163,8 @@ qg_status forward(const Forward& f, const Scales& act, const Scales* ws, const f
     for (int h = 0; h < f.pair; ++h)
         if (!span_ok(K, f.lda, f.ldw[h], f.b_trans)) return QG_ERR_UNSUPPORTED;
     if (too_many_tiles(M, N * f.pair)) return QG_ERR_UNSUPPORTED;
-    const size_t need = forward_workspace(f);
-    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return QG_ERR_WORKSPACE;
+    const Choice c = f.choice();
+    if (c.bytes > 0 && (workspace == nullptr || workspace_bytes < up256(c.bytes))) return QG_ERR_WORKSPACE;
 
     qg::Epilogue e{};
     e.M = (int)M; e.N = (int)N;
@@ -175,32 +182,15 @@ qg_status forward(const Forward& f, const Scales& act, const Scales* ws, const f
     e.out = out; e.ldo = ldo; e.out_type = out_dtype;
     e.ld_ckpt = ld_ckpt; e.ld_ckpt_scale = ld_ckpt_scale;
     (void)hipGetLastError();
-    const hipStream_t s = (hipStream_t)stream;
-
-    const int tile = f.tile(), form = f.pair == 2 ? qg::FUSED_PAIR : qg::FUSED_ONE;
-    if (tile != THROUGH) {
-        qg::FusedArgs a{};
-        a.e = e;
-        a.A[0] = f.A; a.lda = f.lda;
-        for (int h = 0; h < f.pair; ++h) {
-            a.B[h] = f.W[h];
-            a.ldb[h] = f.ldw[h];
-        }
-        a.K = (int)K; a.branches = 1;
-        return done(launch_fused(form, a, tile, f.b_trans != 0, s), tile_name(form, tile));
+    qg::FusedArgs a{};
+    a.e = e;
+    a.A[0] = f.A; a.lda = f.lda;
+    for (int h = 0; h < f.pair; ++h) {
+        a.B[h] = f.W[h];
+        a.ldb[h] = f.ldw[h];
     }
-    const Through t(M, N, K, f.pair);
-    char* const z = (char*)workspace + t.gemm;
-    if (t.gemm > 0) QG_TRY_HIP(qg::launch_clear((uint32_t*)workspace, qg::SKINNY_MAX_TICKETS, s));
-    for (int64_t m = 0; m < M; m += t.rows) {
-        const int64_t rows = std::min(t.rows, M - m);
-        for (int h = 0; h < f.pair; ++h)
-            QG_TRY(qgemm_a8w8(rows, N, K, f.A + m * f.lda, f.lda, f.W[h], f.ldw[h], f.b_trans,
-                              act.p + (act.len == 1 ? 0 : m), act.len == 1 ? 1 : rows, ws[h].p, ws[h].len, z + h * t.z, QG_FP32, N,
-                              t.gemm > 0 ? workspace : nullptr, t.gemm, stream));
-        QG_TRY_HIP(qg::launch_fused_finish(e, f.pair == 2, (const float*)z, (const float*)(z + t.z), (int)m, (int)rows, s));
-    }
-    return done(hipSuccess, "a8w8_then_finish");
+    a.K = (int)K; a.branches = 1;
+    return run(f.pair == 2 ? qg::FUSED_PAIR : qg::FUSED_ONE, a, c, f.b_trans != 0, workspace, (hipStream_t)stream);
 }
 
 // The gradients.
@@ -210,32 +200,28 @@ struct Backward {
     int pair;
     bool with_bias;
 
-    int tile() const {
+    Choice choice() const {
         bool pieces = true;
         for (int h = 0; h < pair; ++h) pieces = pieces && whole_pieces(W[h], ldw[h], b_trans ? K : N);
-        return pick_tile(2 * M, K, N * pair, pieces);
+        return choose(2 * M, K, (N + 127) / 128 * pair, K, pieces);
     }
 };
 
 // Where a gradient's workspace holds what.
 struct GradPlan {
     int64_t np, ldq;
-    size_t hi, lo, row_scale, scales, part, gemm, z, bytes;
-    int parts, tile;
-    Through t;
+    size_t hi, lo, row_scale, part, sums, bytes;
+    int parts;
+    Choice c;
     explicit GradPlan(const Backward& b)
-        : np((b.N + 127) / 128 * 128), ldq(np * b.pair), parts(b.with_bias ? qg::grad_rows_parts(b.M, b.N) : 0), tile(b.tile()),
-          t(b.M, b.K, b.N, 2 * b.pair) {
-        const bool through = tile == THROUGH;
+        : np((b.N + 127) / 128 * 128), ldq(np * b.pair), parts(b.with_bias ? qg::grad_rows_parts(b.M, b.N) : 0), c(b.choice()) {
         size_t at = 0;
         auto take = [&](size_t n) { const size_t here = at; at += up256(n); return here; };
-        gemm = take(through ? t.gemm : 0);
         hi = take((size_t)b.M * ldq);
         lo = take((size_t)b.M * ldq);
         row_scale = take((size_t)b.M * 4);
-        scales = take(through ? (size_t)(2 * b.M + 1) * 4 : 0);
         part = take((size_t)parts * b.N * 4);
-        z = take(through ? t.z * 2 * b.pair : 0);
+        sums = take(c.bytes);
         bytes = at;
     }
 };
@@ -293,36 +279,21 @@ qg_status backward(const Backward& b, const void* dy, qg_dtype dtype, int64_t ld
     a.activation = activation;
     a.hi = (int8_t*)(w + p.hi); a.lo = (int8_t*)(w + p.lo); a.ldq = p.ldq;
     a.row_scale = (float*)(w + p.row_scale);
-    a.scales = p.tile == THROUGH ? (float*)(w + p.scales) : nullptr;
     a.part = (float*)(w + p.part); a.parts = p.parts;
     a.dbias = dbias;
     QG_TRY_HIP(qg::launch_grad_rows(a, b.pair == 2, dtype == QG_BF16, s));
 
-    if (p.tile != THROUGH) {
-        qg::FusedArgs f{};
-        f.e.M = (int)M; f.e.N = (int)K;
-        f.e.act_scale = a.row_scale; f.e.as_stride = 1;
-        f.e.out = dx; f.e.ldo = ld_dx; f.e.out_type = dtype;
-        f.A[0] = a.hi; f.A[1] = a.lo; f.lda = p.ldq;
-        for (int h = 0; h < b.pair; ++h) {
-            f.B[h] = b.W[h];
-            f.ldb[h] = b.ldw[h];
-        }
-        f.K = (int)N; f.branches = b.pair;
-        return done(launch_fused(qg::FUSED_GRAD, f, p.tile, b.b_trans == 0, s), tile_name(qg::FUSED_GRAD, p.tile));
+    qg::FusedArgs f{};
+    f.e.M = (int)M; f.e.N = (int)K;
+    f.e.act_scale = a.row_scale; f.e.as_stride = 1;
+    f.e.out = dx; f.e.ldo = ld_dx; f.e.out_type = dtype;
+    f.A[0] = a.hi; f.A[1] = a.lo; f.lda = p.ldq;
+    for (int h = 0; h < b.pair; ++h) {
+        f.B[h] = b.W[h];
+        f.ldb[h] = b.ldw[h];
     }
-    if (p.t.gemm > 0) QG_TRY_HIP(qg::launch_clear((uint32_t*)(w + p.gemm), qg::SKINNY_MAX_TICKETS, s));
-    for (int64_t m = 0; m < M; m += p.t.rows) {
-        const int64_t rows = std::min(p.t.rows, M - m);
-        for (int h = 0; h < b.pair; ++h)
-            for (int part = 0; part < 2; ++part)
-                QG_TRY(qgemm_a8w8(rows, K, N, (part == 0 ? a.hi : a.lo) + m * p.ldq + h * p.np, p.ldq, b.W[h], b.ldw[h], !b.b_trans,
-                                  a.scales + part * M + m, rows, a.scales + 2 * M, 1, w + p.z + (2 * h + part) * p.t.z, QG_FP32, K,
-                                  p.t.gemm > 0 ? w + p.gemm : nullptr, p.t.gemm, stream));
-        QG_TRY_HIP(qg::launch_grad_sum((const float*)(w + p.z), (int64_t)(p.t.z / 4), 2 * b.pair, rows, K,
-                                       (char*)dx + m * ld_dx * 2, ld_dx, dtype == QG_BF16, s));
-    }
-    return done(hipSuccess, "grad_rows_a8w8_sum");
+    f.K = (int)N; f.branches = b.pair;
+    return run(qg::FUSED_GRAD, f, p.c, b.b_trans == 0, w + p.sums, s);
 }
 
 }  // namespace

@@ -159,15 +159,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void grad_rows_kernel(GradRowsAr
         const float most = __uint_as_float(top), up = most < 0x1p-90f ? 0x1p60f : 1.0f;   // STEPS / most stays finite
         const float inv = bad || top == 0u ? 0.f : STEPS / (most * up);
         if (!live) continue;
-        if (t == 0) {
-            const float s = bad ? __uint_as_float(0x7fc00000u) : most / STEPS;
-            a.row_scale[row] = s;
-            if (a.scales != nullptr) {
-                a.scales[row] = 256.f * s;
-                a.scales[a.M + row] = s;
-                if (row == 0) a.scales[2 * (int64_t)a.M] = 1.f;
-            }
-        }
+        if (t == 0) a.row_scale[row] = bad ? __uint_as_float(0x7fc00000u) : most / STEPS;
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
             const int c = (i * G + t) * 8;

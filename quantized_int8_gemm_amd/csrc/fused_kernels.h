@@ -32,17 +32,21 @@ struct FusedArgs {
     const int8_t* A[2]; int64_t lda;
     const int8_t* B[2]; int64_t ldb[2];
     int K, branches;
+    // NULL, or where `splits` workgroups a tile, of split_chunks chunks of 128 each, leave
+    // their sums: int32 [splits, 1 or 2 (a pair's or a gradient's), e.M, ld_partial]
+    int* partial; int splits, split_chunks; int64_t ld_partial;
 };
-// Rows and columns of sums of a tile; the ANY tiles take operands of any alignment.
-enum FusedTile { FUSED_256x256, FUSED_128x128, FUSED_64x128, FUSED_ANY_128x128, FUSED_ANY_64x128, FUSED_TILES };
+// Rows and columns of sums of a tile, of two LDS stages or more (DEEP); the ANY tiles
+// take operands of any alignment.
+enum FusedTile { FUSED_256x256, FUSED_128x128, FUSED_128x128_DEEP, FUSED_64x128, FUSED_64x128_DEEP,
+                 FUSED_ANY_128x128, FUSED_ANY_64x128, FUSED_TILES };
 // kmajor: B's rows lie along the sum.
 hipError_t launch_fused_one(const FusedArgs& a, FusedTile tile, bool kmajor, hipStream_t s);
 hipError_t launch_fused_pair(const FusedArgs& a, FusedTile tile, bool kmajor, hipStream_t s);
 hipError_t launch_fused_grad(const FusedArgs& a, FusedTile tile, bool kmajor, hipStream_t s);
 
-// The epilogue after products that are in memory as fp32, scales applied.
-// z [rows,N] at a stride of N values, of rows m0 .. m0 + rows - 1.
-hipError_t launch_fused_finish(const Epilogue& e, bool pair, const float* z0, const float* z1, int m0, int rows, hipStream_t s);
+// The second kernel of a divided sum.
+hipError_t launch_fused_join(const FusedArgs& a, int form, hipStream_t s);
 
 // The factors of a gradient, for each row of dy: `hi` and `lo` [M, branches * np]
 // with zeros behind each branch's N, and the row's scale.
@@ -55,16 +59,11 @@ struct GradRowsArgs {
     int activation;
     int8_t* hi; int8_t* lo; int64_t ldq;
     float* row_scale;                         // [M]
-    float* scales;                            // NULL, or [2M + 1]: 256 s, s and 1, as qgemm_a8w8 takes them
     float* part; int parts;                   // NULL, or [parts,N] partial sums of dbias
     float* dbias;
 };
 int grad_rows_parts(int64_t M, int64_t N);
 hipError_t launch_grad_rows(const GradRowsArgs& a, bool pair, bool bf16, hipStream_t s);
-// dx [rows,K] = sum of `count` (2 or 4) fp32 matrices `stride` values apart.
-hipError_t launch_grad_sum(const float* z, int64_t stride, int count, int64_t rows, int64_t K, void* dx, int64_t ld_dx,
-                           bool bf16, hipStream_t s);
-
 struct Int8Args {
     int64_t M; int64_t n; int block;
     const void* x; int64_t ldx;               // quantise: values in
@@ -74,9 +73,6 @@ struct Int8Args {
 };
 hipError_t launch_int8_quantize(const Int8Args& a, qg_dtype type, hipStream_t s);
 hipError_t launch_int8_dequantize(const Int8Args& a, qg_dtype type, hipStream_t s);
-// Clears the ticket words at the head of a product's workspace.
-hipError_t launch_clear(uint32_t* words, int count, hipStream_t s);
-
 // Of api.cpp.
 void record_kernel(const char* name);
 

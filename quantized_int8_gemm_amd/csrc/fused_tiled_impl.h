@@ -12,11 +12,11 @@
 //
 // A workgroup computes a BM x BN tile of sums (BN / 2 columns of a pair, BM / 2 rows of
 // a gradient), K in chunks of 128 bytes:
-//  * DMA: chunks go global -> LDS directly (buffer_load ... lds), in a ring of two
-//    stages, the next one in flight while this one is multiplied.  Wants rows of whole
+//  * DMA: chunks go global -> LDS directly (buffer_load ... lds), in a ring of RING
+//    stages, the next ones in flight while one is multiplied.  Wants rows of whole
 //    16-byte pieces.  A piece of A past K is asked for past the buffer's end, which
 //    gives zeros; whatever B holds there then adds nothing.
-//  * else through registers with loads of any alignment, the next chunk's in flight
+//  * RING 0: through registers with loads of any alignment, the next chunk's in flight
 //    while this one is multiplied, and one stage.
 //  * Fragments as in the int8 products: K-contiguous operands by ds_read_b128, [K,N]
 //    weights by ds_read_b64_tr_b8; segments swizzled so that both are free of bank
@@ -24,6 +24,8 @@
 //    registers are four consecutive columns of a row.
 //  * The int32 sums pass through LDS, so that each lane finishes four columns of a row
 //    and whole rows leave together; the epilogue is the same code for every kernel.
+//    With p.partial, K is divided among workgroups (blockIdx.y), each leaves its sums there
+//    as they are, and a second kernel adds them and finishes.
 #pragma once
 #include "fused_common.h"
 #include "fused_kernels.h"
@@ -73,7 +75,7 @@ __device__ __forceinline__ u32x4 load16_any(const int8_t* row, int c, int limit)
     return u32x4{w[0], w[1], w[2], w[3]};
 }
 
-template <int MODE, int BM, int BN, int WM, int WN, bool B_KMAJOR, bool DMA>
+template <int MODE, int BM, int BN, int WM, int WN, bool B_KMAJOR, int RING>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel(FusedArgs p) {
     constexpr bool PAIR = MODE == FUSED_PAIR, GRAD = MODE == FUSED_GRAD;
     constexpr int H = MODE == FUSED_ONE ? 1 : 2;
@@ -83,10 +85,13 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
     constexpr int WAVES_N = BN / WN, WAVES_M = BM / WM, FM = WM / 16, FN = WN / 16;
     constexpr int A_BYTES = BM * BK, B_BYTES = BN * BK, STAGE = A_BYTES + B_BYTES;
     constexpr int A_ROUNDS = A_BYTES / ROUND, B_ROUNDS = B_BYTES / ROUND;
-    constexpr int STAGES = DMA ? 2 : 1;
+    constexpr bool DMA = RING > 0;
+    constexpr int STAGES = DMA ? RING : 1;
+    constexpr int LOADS = A_ROUNDS + B_ROUNDS;                         // per lane and chunk
     constexpr int RB = PAIR ? BN / 2 : BN;                             // row bytes of a [K,N] tile (of each half)
     static_assert(NT == 256 || NT == 512, "four or eight waves");
     static_assert(A_BYTES % ROUND == 0 && B_BYTES % ROUND == 0 && (BK * RB) % ROUND == 0, "whole load rounds");
+    static_assert(LOADS * (STAGES - 2) < 64, "vmcnt range");
     static_assert((!GRAD || FM % 2 == 0) && (!PAIR || FN % 2 == 0), "fragments in pairs");
     __shared__ __attribute__((aligned(1024))) uint8_t smem[STAGES * STAGE];
 
@@ -103,7 +108,10 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
     const int cols_b = N - n0 < BNR ? N - n0 : BNR;
     const int lda = (int)p.lda;
     // K of one weight, and chunks of it; of GRAD's planes each weight's part is whole chunks
-    const int K = p.K, nkb = (K + BK - 1) / BK, nk = GRAD ? nkb * p.branches : nkb;
+    const int K = p.K, nkb = (K + BK - 1) / BK, all = GRAD ? nkb * p.branches : nkb;
+    // this workgroup's chunks: all, or one split's
+    const int k0 = p.partial != nullptr ? (int)blockIdx.y * p.split_chunks : 0;
+    const int nk = p.partial != nullptr && all - k0 > p.split_chunks ? k0 + p.split_chunks : all;
     const uint32_t lds0 = (uint32_t)(uintptr_t)smem;
 
     // A wave's load instruction covers eight LDS rows of a K-contiguous tile, all of one
@@ -119,7 +127,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
     };
     v4i a_rsrc = {}, b_rsrc = {}, b_rsrc2 = {};   // b_rsrc2: the second half of a [K,N] pair, or GRAD's second weight
     if constexpr (DMA) {
-        a_rsrc = rsrc_words(A, (uint32_t)((rows_a - 1) * lda + (GRAD ? nk * BK : K)));
+        a_rsrc = rsrc_words(A, (uint32_t)((rows_a - 1) * lda + (GRAD ? all * BK : K)));
         b_rsrc = b_words(PAIR && B_KMAJOR ? half : 0);
         if ((PAIR && !B_KMAJOR) || (GRAD && p.branches == 2)) b_rsrc2 = b_words(1);
     }
@@ -180,7 +188,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
 #pragma unroll
             for (int q = 0; q < A_ROUNDS; ++q) {
                 const int r = GRAD ? real(kc_row(q)) : kc_row(q);
-                ar[q] = load16_any(A + (int64_t)(r < rows_a ? r : 0) * p.lda, kt * BK + kc_col, r < rows_a ? (GRAD ? nk * BK : K) : 0);
+                ar[q] = load16_any(A + (int64_t)(r < rows_a ? r : 0) * p.lda, kt * BK + kc_col, r < rows_a ? (GRAD ? all * BK : K) : 0);
             }
 #pragma unroll
             for (int q = 0; q < B_ROUNDS; ++q) {
@@ -236,7 +244,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
 
     // Every fragment of B is read at the start of a chunk, A's one ahead of its products; the
     // next chunk's loads are issued right after the first reads.
-    auto compute = [&](int stage, int next) {
+    auto compute = [&](int stage, int next, int next_stage) {
         const uint8_t* S = smem + stage * STAGE;
         u32x4 bfs[KB][FN];
         read_b(S, 0, bfs[0]);
@@ -244,7 +252,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
 #pragma unroll
         for (int kb = 1; kb < KB; ++kb) read_b(S, kb, bfs[kb]);
         __builtin_amdgcn_sched_barrier(0);
-        if (next < nk) issue(next, next % STAGES);
+        if (next < nk) issue(next, next_stage);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
@@ -261,19 +269,27 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
         }
     };
 
-    issue(0, 0);
     if constexpr (DMA) {
-        for (int kt = 0; kt < nk; ++kt) {
-            wait_vmcnt<0>();     // chunk kt has landed
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i)
+            if (k0 + i < nk) issue(k0 + i, i);
+        int at = 0;
+        for (int kt = k0; kt < nk; ++kt) {
+            // chunk kt has landed once at most the later ones are on their way
+            if (STAGES > 2 && kt + STAGES - 2 < nk) wait_vmcnt<LOADS * (STAGES - 2)>();
+            else if (STAGES > 2 && kt + 1 < nk) wait_vmcnt<LOADS>();
+            else wait_vmcnt<0>();
             __syncthreads();
-            compute(kt & 1, kt + 1);
+            compute(at, kt + STAGES - 1, at == 0 ? STAGES - 1 : at - 1);
+            at = at + 1 == STAGES ? 0 : at + 1;
         }
     } else {
-        for (int kt = 0; kt < nk; ++kt) {
-            if (kt > 0) __syncthreads();   // every wave has read the last chunk
+        issue(k0, 0);
+        for (int kt = k0; kt < nk; ++kt) {
+            if (kt > k0) __syncthreads();   // every wave has read the last chunk
             put();
             __syncthreads();
-            compute(0, kt + 1);
+            compute(0, kt + 1, 0);
         }
     }
 
@@ -303,7 +319,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
             const int m = m0 + pass * PR + (q0 + u) * ROWS_AT_ONCE + tid / CPT;
             res_next[u] = Raw4{};
             as_next[u] = 0.f;
-            if (m >= M) continue;
+            if (m >= M || p.partial != nullptr) continue;
             as_next[u] = p.e.act_scale[(int64_t)m * p.e.as_stride];
             if (MODE == FUSED_ONE && p.e.res != nullptr) res_next[u] = load_raw4(p.e.res, (int64_t)m * p.e.ldr + n, p.e.out_type, count);
         }
@@ -342,7 +358,13 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
                 const int rr = (q0 + u) * ROWS_AT_ONCE + tid / CPT, m = m0 + pass * PR + rr;
                 const int at = rr * BNR + ((c4 ^ (rr & 15)) << 2);
                 const v4i s0 = *reinterpret_cast<const v4i*>(stage + at);
-                if constexpr (GRAD) {
+                if (p.partial != nullptr) {
+                    if (m < M && count > 0) {
+                        int* to = p.partial + ((int64_t)blockIdx.y * H * M + m) * p.ld_partial + n;
+                        *reinterpret_cast<v4i*>(to) = s0;
+                        if constexpr (H == 2) *reinterpret_cast<v4i*>(to + (int64_t)M * p.ld_partial) = *reinterpret_cast<const v4i*>(stage + PR * BNR + at);
+                    }
+                } else if constexpr (GRAD) {
                     const v4i s1 = *reinterpret_cast<const v4i*>(stage + PR * BNR + at);
                     v4f v;
 #pragma unroll
@@ -364,25 +386,28 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
     }
 }
 
-template <int MODE, int BM, int BN, int WM, int WN, bool DMA>
+template <int MODE, int BM, int BN, int WM, int WN, int RING>
 hipError_t launch_tile(const FusedArgs& a, bool kmajor, hipStream_t s) {
     constexpr int BMR = MODE == FUSED_GRAD ? BM / 2 : BM, BNR = MODE == FUSED_PAIR ? BN / 2 : BN;
     constexpr int NT = (BM / WM) * (BN / WN) * 64;
     const int64_t tiles = (int64_t)((a.e.M + BMR - 1) / BMR) * ((a.e.N + BNR - 1) / BNR);
     if (tiles * NT >= (int64_t)1 << 32) return hipErrorInvalidValue;
-    if (kmajor) hipLaunchKernelGGL((fused_tiled_kernel<MODE, BM, BN, WM, WN, true, DMA>), dim3((unsigned)tiles), dim3(NT), 0, s, a);
-    else hipLaunchKernelGGL((fused_tiled_kernel<MODE, BM, BN, WM, WN, false, DMA>), dim3((unsigned)tiles), dim3(NT), 0, s, a);
+    const dim3 grid((unsigned)tiles, a.partial != nullptr ? a.splits : 1);
+    if (kmajor) hipLaunchKernelGGL((fused_tiled_kernel<MODE, BM, BN, WM, WN, true, RING>), grid, dim3(NT), 0, s, a);
+    else hipLaunchKernelGGL((fused_tiled_kernel<MODE, BM, BN, WM, WN, false, RING>), grid, dim3(NT), 0, s, a);
     return hipGetLastError();
 }
 
 template <int MODE>
 hipError_t launch_form(const FusedArgs& a, FusedTile tile, bool kmajor, hipStream_t s) {
     switch (tile) {
-        case FUSED_256x256: return launch_tile<MODE, 256, 256, 128, 64, true>(a, kmajor, s);
-        case FUSED_128x128: return launch_tile<MODE, 128, 128, 64, 64, true>(a, kmajor, s);
-        case FUSED_64x128: return launch_tile<MODE, 64, 128, 32, 64, true>(a, kmajor, s);
-        case FUSED_ANY_128x128: return launch_tile<MODE, 128, 128, 64, 64, false>(a, kmajor, s);
-        default: return launch_tile<MODE, 64, 128, 32, 64, false>(a, kmajor, s);
+        case FUSED_256x256: return launch_tile<MODE, 256, 256, 128, 64, 2>(a, kmajor, s);
+        case FUSED_128x128: return launch_tile<MODE, 128, 128, 64, 64, 2>(a, kmajor, s);
+        case FUSED_128x128_DEEP: return launch_tile<MODE, 128, 128, 64, 64, 4>(a, kmajor, s);
+        case FUSED_64x128: return launch_tile<MODE, 64, 128, 32, 64, 2>(a, kmajor, s);
+        case FUSED_64x128_DEEP: return launch_tile<MODE, 64, 128, 32, 64, 6>(a, kmajor, s);
+        case FUSED_ANY_128x128: return launch_tile<MODE, 128, 128, 64, 64, 0>(a, kmajor, s);
+        default: return launch_tile<MODE, 64, 128, 32, 64, 0>(a, kmajor, s);
     }
 }
 
