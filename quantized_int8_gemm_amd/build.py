@@ -56,7 +56,9 @@ SOURCES = [
     "fused_tiled_one.hip",
     "fused_tiled_pair.hip",
     "fused_tiled_grad.hip",
-    "fused_finish.hip",
+    "fused_direct.hip",
+    "fused_pad.hip",
+    "fused_join.hip",
     "fused_grad_rows.hip",
     "int8_quantize.hip",
     "fused_api.cpp",

@@ -1,6 +1,7 @@
 // C entry points of qgemm_fused.h: argument checks (before any HIP call), workspace
 // plans, kernel choice and launch, with the launch-status convention of api.cpp.
 #include <algorithm>
+#include <cmath>
 #include <cstdlib>
 
 #include <hip/hip_runtime.h>
@@ -15,6 +16,7 @@ constexpr int64_t SPAN_LIMIT = (int64_t)1 << 31;   // 32-bit buffer offsets
 bool aligned(const void* p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1)) == 0; }
 bool is_float(qg_dtype t) { return t == QG_FP32 || t == QG_BF16 || t == QG_FP16; }
 bool aligned_for(const void* p, qg_dtype t) { return aligned(p, t == QG_FP32 ? 4 : 2); }
+int64_t up16(int64_t n) { return (n + 15) / 16 * 16; }
 size_t up256(size_t n) { return (n + 255) / 256 * 256; }
 int64_t blocks_of(int64_t n) { return (n + 31) / 32; }
 
@@ -47,65 +49,160 @@ int env_int(const char* name, int dflt) {
 // Rows of whole 16-byte pieces.
 bool whole_pieces(const void* p, int64_t ld, int64_t n) { return aligned(p, 16) && ld % 16 == 0 && n % 16 == 0; }
 
-// How a product runs: its tile, and in how many parts K is divided.
+// How a product runs.  tile: a FusedTile, or DIRECT + 0 .. 5 for workgroups of 16, 32 or 64
+// rows by 16 or 32 columns.
+constexpr int DIRECT = qg::FUSED_TILES, KINDS = DIRECT + 6;
+int direct_rows(int tile) { return 16 << (tile - DIRECT) / 2; }
+int direct_cols(int tile) { return (tile - DIRECT) % 2 == 0 ? 16 : 32; }
+
 struct Choice {
     int tile, splits, split_chunks;
-    size_t bytes;          // of their sums
+    bool pad;              // operands that need it are laid out once more
+    size_t bytes;          // of the divided sums
     int64_t ld_partial;
 };
 
-// For `rows` x `cols` sums over `chunks` chunks of K (a pair's columns and a gradient's rows
-// counted twice), out_cols columns of the output.  QGEMM_FUSED_TILE and QGEMM_FUSED_SPLITS force a
-// tile (of an ANY tile's shape where the operands need that) and a number of parts, for
-// tests and tuning.
-Choice choose(int64_t rows, int64_t cols, int64_t chunks, int64_t out_cols, bool pieces) {
-    auto tiles = [&](int64_t bm, int64_t bn) { return ((rows + bm - 1) / bm) * ((cols + bn - 1) / bn); };
-    const int forced = env_int("QGEMM_FUSED_TILE", -1);
-    Choice c{forced, 1, 0, 0, (out_cols + 3) / 4 * 4};
-    if (forced < 0 || forced >= qg::FUSED_TILES) {
-        const int64_t large = tiles(256, 256), small = tiles(128, 128);
-        if (large >= 512 || (large >= 160 && !(large > 256 && large <= 352))) c.tile = qg::FUSED_256x256;
-        else if (chunks <= 16 && small <= 256) c.tile = qg::FUSED_64x128;
-        else c.tile = qg::FUSED_128x128;
+struct Shape {
+    int form;
+    int64_t M, N, K;       // of the output, and of one weight's sum
+    int branches;          // weights along the sum (a gradient's)
+    bool kmajor, pieces;   // B's rows lie along the sum; all rows are whole 16-byte pieces
+    bool blocks;           // with a checkpoint
+    int64_t pad_bytes;     // of the operands whose rows are not; -1: they cannot be padded
+};
+
+// Microseconds that a kind takes, about, fitted to measured calls (those in parentheses).  A
+// chunk of 128 of K costs a tile what its CU needs with the workgroups that run there at
+// once: 1.75 for 256 x 256 (4000 x 4096 x 4096 71 us, 8192^3 446), 0.75 and 1.1 for one and two of
+// 128 x 128 on two stages (1000 and 2000 x 4096 x 4096 29 and 40), 0.58 on four (24, 48; 1000 x
+// 4096 x 14336 70, two stages 111), 0.36 for 64 x 128 on six (300 x 4096 x 14336 51, 90 x 1008 x 1008
+// 7.9), 0.52 through registers (1000 x 4095 x 4095 71).  A direct workgroup takes its operands at
+// 35 bytes a nanosecond (64 x 4096 x 4096 gated 15 us, 64 x 4096 x 14336 34; 300 x 1008 x 1008 6.6), 16
+// unaligned ones (4 x 4095 x 4095 gated 20).
+double time_of(const Shape& s, int tile, int splits, bool pad) {
+    const double chunks = (double)((s.K + 127) / 128 * s.branches);
+    const double rows = (double)s.M * (s.form == qg::FUSED_GRAD ? 2 : 1), cols = (double)s.N * (s.form == qg::FUSED_PAIR ? 2 : 1);
+    const double per = std::ceil(chunks / splits);
+    auto tiles = [&](double bm, double bn) { return std::ceil(rows / bm) * std::ceil(cols / bn) * splits; };
+    double t;
+    switch (tile) {
+        case qg::FUSED_256x256: t = std::ceil(tiles(256, 256) / 256) * (per * 1.75 + 6); break;
+        case qg::FUSED_128x128: {
+            const double n = tiles(128, 128), full = std::floor(n / 512), rest = n - 512 * full;
+            t = full * (per * 1.1 + 4) + (rest > 256 ? per * 1.1 + 4 : rest > 0 ? per * 0.75 + 3 : 0);
+            break;
+        }
+        case qg::FUSED_128x128_DEEP: t = std::ceil(tiles(128, 128) / 256) * (per * 0.58 + 2.5); break;
+        case qg::FUSED_64x128_DEEP: t = std::ceil(tiles(64, 128) / 256) * (per * 0.36 + 1.5); break;
+        case qg::FUSED_ANY_64x128: t = std::max(1.6, std::ceil(tiles(64, 128) / 256) * 1.04) * per + 2; break;
+        default: {
+            const double tm = direct_rows(tile), tn = direct_cols(tile);
+            const double bytes = (std::min<double>(tm, s.M) + tn * (s.form == qg::FUSED_PAIR ? 2 : 1)) * (double)s.K;
+            t = 1.5 + std::max(1.0, std::ceil(s.M / tm) * std::ceil(s.N / tn) / 256) * (bytes / (s.pieces || pad ? 35e3 : 16e3) + 0.8);
+        }
     }
-    if (!pieces && c.tile < qg::FUSED_ANY_128x128)
-        c.tile = c.tile == qg::FUSED_64x128 || c.tile == qg::FUSED_64x128_DEEP ? qg::FUSED_ANY_64x128 : qg::FUSED_ANY_128x128;
-    const int64_t want = std::min<int64_t>(env_int("QGEMM_FUSED_SPLITS", 1), chunks);
-    if (want > 1) {
-        c.split_chunks = (int)((chunks + want - 1) / want);
-        c.splits = (int)((chunks + c.split_chunks - 1) / c.split_chunks);
-        c.bytes = (size_t)c.splits * (size_t)(rows * cols / out_cols) * c.ld_partial * 4;
-    }
-    return c;
+    if (splits > 1) t += 3 + rows * cols * 8 * splits / 3e6;
+    if (pad) t += 3 + 2 * (double)s.pad_bytes / 4e6;
+    // no faster than the operands come from memory
+    const double floor = (rows + cols) * (double)s.K * s.branches / 5e6;
+    return std::max(t, floor) + 0.02 * t;
 }
 
-hipError_t launch_fused(int form, const qg::FusedArgs& a, int tile, bool kmajor, hipStream_t s) {
+// The kind that takes the least time by this reckoning.  QGEMM_FUSED_TILE, QGEMM_FUSED_SPLITS and
+// QGEMM_FUSED_PAD force a kind, a number of parts of K and padding (0: none), where the call allows
+// them; for tests and tuning.
+Choice choose(const Shape& s) {
+    const int64_t chunks = (s.K + 127) / 128 * s.branches;
+    const int tile = env_int("QGEMM_FUSED_TILE", -1), splits = env_int("QGEMM_FUSED_SPLITS", 0), pad = env_int("QGEMM_FUSED_PAD", -1);
+    Choice best{qg::FUSED_ANY_64x128, 1, 0, false, 0, (s.N + 3) / 4 * 4};
+    double least = 1e30;
+    static const int parts[] = {1, 2, 3, 4, 6, 8, 12, 16};
+    for (int with_pad = 0; with_pad < 2; ++with_pad) {
+        if (with_pad == 1 && (s.pieces || s.pad_bytes < 0)) continue;
+        for (int k = 0; k < KINDS; ++k) {
+            const bool direct = k >= DIRECT;
+            if (direct && (!s.kmajor || s.form == qg::FUSED_GRAD || (s.blocks && direct_cols(k) == 16))) continue;
+            if (k < qg::FUSED_ANY_64x128 && !s.pieces && with_pad == 0) continue;
+            for (const int p : parts) {
+                if (p > 1 && (direct || k == qg::FUSED_256x256 || p > chunks)) break;
+                // what is forced goes before what is not
+                const double t = time_of(s, k, p, with_pad == 1) + (tile >= 0 && tile < KINDS && k != tile ? 1e12 : 0) +
+                                 (pad >= 0 && with_pad != (pad != 0) ? 1e9 : 0) + (splits > 0 && p != splits ? 1e6 : 0);
+                if (t >= least) continue;
+                least = t;
+                best.tile = k;
+                best.pad = with_pad == 1;
+                best.splits = p;
+            }
+        }
+    }
+    if (best.splits > 1) {
+        best.split_chunks = (int)((chunks + best.splits - 1) / best.splits);
+        best.splits = (int)((chunks + best.split_chunks - 1) / best.split_chunks);
+        best.bytes = (size_t)best.splits * (s.form == qg::FUSED_ONE ? 1 : 2) * (size_t)s.M * best.ld_partial * 4;
+    }
+    return best;
+}
+
+hipError_t launch_fused(int form, const qg::FusedArgs& a, int tile, bool kmajor, bool any, hipStream_t s) {
+    if (tile >= DIRECT) return qg::launch_fused_direct(a, form == qg::FUSED_PAIR, direct_rows(tile), direct_cols(tile), any, s);
     const qg::FusedTile t = (qg::FusedTile)tile;
     return form == qg::FUSED_ONE ? qg::launch_fused_one(a, t, kmajor, s)
            : form == qg::FUSED_PAIR ? qg::launch_fused_pair(a, t, kmajor, s) : qg::launch_fused_grad(a, t, kmajor, s);
 }
 
 const char* kernel_name(int form, const Choice& c) {
-    static const char* const names[3][qg::FUSED_TILES] = {
-        {"fused_one_256x256", "fused_one_128x128", "fused_one_128x128_deep", "fused_one_64x128", "fused_one_64x128_deep",
-         "fused_one_any_128x128", "fused_one_any_64x128"},
-        {"fused_pair_256x256", "fused_pair_128x128", "fused_pair_128x128_deep", "fused_pair_64x128", "fused_pair_64x128_deep",
-         "fused_pair_any_128x128", "fused_pair_any_64x128"},
-        {"fused_grad_256x256", "fused_grad_128x128", "fused_grad_128x128_deep", "fused_grad_64x128", "fused_grad_64x128_deep",
-         "fused_grad_any_128x128", "fused_grad_any_64x128"}};
+    static const char* const names[3][KINDS] = {
+        {"fused_one_256x256", "fused_one_128x128", "fused_one_128x128_deep", "fused_one_64x128_deep", "fused_one_any_64x128",
+         "fused_one_direct_16x16", "fused_one_direct_16x32", "fused_one_direct_32x16", "fused_one_direct_32x32",
+         "fused_one_direct_64x16", "fused_one_direct_64x32"},
+        {"fused_pair_256x256", "fused_pair_128x128", "fused_pair_128x128_deep", "fused_pair_64x128_deep", "fused_pair_any_64x128",
+         "fused_pair_direct_16x16", "fused_pair_direct_16x32", "fused_pair_direct_32x16", "fused_pair_direct_32x32",
+         "fused_pair_direct_64x16", "fused_pair_direct_64x32"},
+        {"fused_grad_256x256", "fused_grad_128x128", "fused_grad_128x128_deep", "fused_grad_64x128_deep", "fused_grad_any_64x128",
+         "", "", "", "", "", ""}};
     static const char* const joined[3] = {"fused_one_joined", "fused_pair_joined", "fused_grad_joined"};
     return c.splits > 1 ? joined[form] : names[form][c.tile];
 }
 
-// The product, and the second kernel where K is divided.
-qg_status run(int form, qg::FusedArgs& a, const Choice& c, bool kmajor, void* partial, hipStream_t s) {
+// An operand whose rows are laid out once more, and where.
+struct Padded {
+    const int8_t** p; int64_t* ld;
+    int64_t rows, cols;
+    bool needed() const { return !whole_pieces(*p, *ld, cols); }
+    int64_t ldd() const { return up16(cols); }
+    size_t bytes() const { return up256((size_t)rows * ldd()); }
+};
+
+// The product: its operands padded first where the choice says so, the second kernel behind
+// it where K is divided.
+qg_status run(int form, qg::FusedArgs& a, const Choice& c, bool kmajor, bool any, Padded* ops, int count, char* pad, void* partial,
+              hipStream_t s) {
+    a.b_cols = a.e.N;
+    a.k_bytes = a.K;
+    if (c.pad) {
+        qg::PadArgs p{};
+        for (int i = 0; i < count; ++i) {
+            if (!ops[i].needed()) continue;
+            p.src[p.count] = *ops[i].p; p.ld[p.count] = *ops[i].ld;
+            p.rows[p.count] = ops[i].rows; p.cols[p.count] = ops[i].cols;
+            p.dst[p.count] = (int8_t*)pad; p.ldd[p.count] = ops[i].ldd();
+            ++p.count;
+            *ops[i].p = (const int8_t*)pad; *ops[i].ld = ops[i].ldd();
+            pad += ops[i].bytes();
+        }
+        QG_TRY_HIP(qg::launch_fused_pad(p, s));
+        a.k_bytes = (int)up16(a.K);
+        a.b_cols = (int)up16(a.e.N);
+        any = false;
+    }
     if (c.splits > 1) {
         a.partial = (int*)partial;
         a.splits = c.splits;
         a.split_chunks = c.split_chunks;
         a.ld_partial = c.ld_partial;
     }
-    QG_TRY_HIP(launch_fused(form, a, c.tile, kmajor, s));
+    QG_TRY_HIP(launch_fused(form, a, c.tile, kmajor, any, s));
     if (c.splits > 1) QG_TRY_HIP(qg::launch_fused_join(a, form, s));
     return done(hipSuccess, kernel_name(form, c));
 }
@@ -124,10 +221,22 @@ struct Forward {
     const int8_t* W[2]; int64_t ldw[2]; int b_trans;
     int pair;
 
-    Choice choice() const {
-        bool pieces = whole_pieces(A, lda, K);
-        for (int h = 0; h < pair; ++h) pieces = pieces && whole_pieces(W[h], ldw[h], b_trans ? K : N);
-        return choose(M, N * pair, (K + 127) / 128, N, pieces);
+    // Operands whose rows may have to be padded.
+    int operands(Padded* o) {
+        o[0] = {&A, &lda, M, K};
+        for (int h = 0; h < pair; ++h) o[1 + h] = {&W[h], &ldw[h], b_trans ? N : K, b_trans ? K : N};
+        return 1 + pair;
+    }
+    size_t pad_bytes() {
+        Padded o[3];
+        size_t n = 0;
+        for (int i = operands(o); i-- > 0;) n += o[i].needed() ? o[i].bytes() : 0;
+        return n;
+    }
+    Choice choice(bool blocks) {
+        const size_t pad = pad_bytes();
+        return choose({pair == 2 ? qg::FUSED_PAIR : qg::FUSED_ONE, M, N, K, 1, b_trans != 0, pad == 0, blocks,
+                       span_ok(K, up16(lda), std::max(up16(ldw[0]), up16(ldw[pair - 1])), b_trans) ? (int64_t)pad : -1});
     }
 };
 
@@ -135,16 +244,22 @@ bool sizes_bad(int64_t M, int64_t N, int64_t K) {
     return M < 0 || N < 0 || K < 0 || M >= LIM || N >= LIM || K >= LIM;
 }
 
-size_t forward_workspace(const Forward& f) {
+// With and without a checkpoint: the larger.
+size_t forward_workspace(Forward f) {
     if (sizes_bad(f.M, f.N, f.K) || f.M == 0 || f.N == 0 || f.K == 0) return 0;
-    return up256(f.choice().bytes);
+    size_t most = 0;
+    for (const bool blocks : {false, true}) {
+        const Choice c = f.choice(blocks);
+        most = std::max(most, (c.pad ? f.pad_bytes() : 0) + up256(c.bytes));
+    }
+    return most;
 }
 
 bool checkpoint_ok(const int8_t* c, int64_t ldc, const float* s, int64_t lds, int64_t N) {
     return c != nullptr && s != nullptr && aligned(s, 4) && ldc >= N && lds >= blocks_of(N);
 }
 
-qg_status forward(const Forward& f, const Scales& act, const Scales* ws, const float* bias, qg_activation activation,
+qg_status forward(Forward f, const Scales& act, const Scales* ws, const float* bias, qg_activation activation,
                   const void* res, int64_t ldr, void* out, qg_dtype out_dtype, int64_t ldo, int8_t* ckpt, int64_t ld_ckpt,
                   float* ckpt_scale, int64_t ld_ckpt_scale, void* workspace, size_t workspace_bytes, void* stream) {
     const int64_t M = f.M, N = f.N, K = f.K;
@@ -163,8 +278,9 @@ qg_status forward(const Forward& f, const Scales& act, const Scales* ws, const f
     for (int h = 0; h < f.pair; ++h)
         if (!span_ok(K, f.lda, f.ldw[h], f.b_trans)) return QG_ERR_UNSUPPORTED;
     if (too_many_tiles(M, N * f.pair)) return QG_ERR_UNSUPPORTED;
-    const Choice c = f.choice();
-    if (c.bytes > 0 && (workspace == nullptr || workspace_bytes < up256(c.bytes))) return QG_ERR_WORKSPACE;
+    const Choice c = f.choice(ckpt != nullptr);
+    const size_t pad = c.pad ? f.pad_bytes() : 0, need = pad + up256(c.bytes);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return QG_ERR_WORKSPACE;
 
     qg::Epilogue e{};
     e.M = (int)M; e.N = (int)N;
@@ -182,15 +298,22 @@ qg_status forward(const Forward& f, const Scales& act, const Scales* ws, const f
     e.out = out; e.ldo = ldo; e.out_type = out_dtype;
     e.ld_ckpt = ld_ckpt; e.ld_ckpt_scale = ld_ckpt_scale;
     (void)hipGetLastError();
+    Padded ops[3];
+    const int count = f.operands(ops);
+    bool any = false;
+    for (int i = 0; i < count; ++i) any = any || ops[i].needed();
     qg::FusedArgs a{};
     a.e = e;
     a.A[0] = f.A; a.lda = f.lda;
+    ops[0].p = &a.A[0]; ops[0].ld = &a.lda;
     for (int h = 0; h < f.pair; ++h) {
         a.B[h] = f.W[h];
         a.ldb[h] = f.ldw[h];
+        ops[1 + h].p = &a.B[h]; ops[1 + h].ld = &a.ldb[h];
     }
     a.K = (int)K; a.branches = 1;
-    return run(f.pair == 2 ? qg::FUSED_PAIR : qg::FUSED_ONE, a, c, f.b_trans != 0, workspace, (hipStream_t)stream);
+    return run(f.pair == 2 ? qg::FUSED_PAIR : qg::FUSED_ONE, a, c, f.b_trans != 0, any, ops, count, (char*)workspace,
+               (char*)workspace + pad, (hipStream_t)stream);
 }
 
 // The gradients.
@@ -200,20 +323,31 @@ struct Backward {
     int pair;
     bool with_bias;
 
-    Choice choice() const {
-        bool pieces = true;
-        for (int h = 0; h < pair; ++h) pieces = pieces && whole_pieces(W[h], ldw[h], b_trans ? K : N);
-        return choose(2 * M, K, (N + 127) / 128 * pair, K, pieces);
+    int operands(Padded* o) {
+        for (int h = 0; h < pair; ++h) o[h] = {&W[h], &ldw[h], b_trans ? N : K, b_trans ? K : N};
+        return pair;
+    }
+    size_t pad_bytes() {
+        Padded o[2];
+        size_t n = 0;
+        for (int i = operands(o); i-- > 0;) n += o[i].needed() ? o[i].bytes() : 0;
+        return n;
+    }
+    // the product's: outputs [M,K], sums over N
+    Choice choice() {
+        const size_t pad = pad_bytes();
+        return choose({qg::FUSED_GRAD, M, K, N, pair, b_trans == 0, pad == 0, false,
+                       span_ok(N, 0, std::max(up16(ldw[0]), up16(ldw[pair - 1])), !b_trans) ? (int64_t)pad : -1});
     }
 };
 
 // Where a gradient's workspace holds what.
 struct GradPlan {
     int64_t np, ldq;
-    size_t hi, lo, row_scale, part, sums, bytes;
+    size_t hi, lo, row_scale, part, pad, sums, bytes;
     int parts;
     Choice c;
-    explicit GradPlan(const Backward& b)
+    explicit GradPlan(Backward b)
         : np((b.N + 127) / 128 * 128), ldq(np * b.pair), parts(b.with_bias ? qg::grad_rows_parts(b.M, b.N) : 0), c(b.choice()) {
         size_t at = 0;
         auto take = [&](size_t n) { const size_t here = at; at += up256(n); return here; };
@@ -221,17 +355,18 @@ struct GradPlan {
         lo = take((size_t)b.M * ldq);
         row_scale = take((size_t)b.M * 4);
         part = take((size_t)parts * b.N * 4);
+        pad = take(c.pad ? b.pad_bytes() : 0);
         sums = take(c.bytes);
         bytes = at;
     }
 };
 
-size_t backward_workspace(const Backward& b) {
+size_t backward_workspace(Backward b) {
     if (sizes_bad(b.M, b.N, b.K) || b.M == 0 || b.N == 0 || b.K == 0 || b.N > QG_A8W8_GRAD_MAX_COLUMNS) return 0;
     return GradPlan(b).bytes;
 }
 
-qg_status backward(const Backward& b, const void* dy, qg_dtype dtype, int64_t ld_dy, const Scales* ws, const int8_t* ckpt,
+qg_status backward(Backward b, const void* dy, qg_dtype dtype, int64_t ld_dy, const Scales* ws, const int8_t* ckpt,
                    int64_t ld_ckpt, const float* ckpt_scale, int64_t ld_ckpt_scale, qg_activation activation, void* dx,
                    int64_t ld_dx, float* dbias, void* workspace, size_t workspace_bytes, void* stream) {
     const int64_t M = b.M, N = b.N, K = b.K;
@@ -288,12 +423,17 @@ qg_status backward(const Backward& b, const void* dy, qg_dtype dtype, int64_t ld
     f.e.act_scale = a.row_scale; f.e.as_stride = 1;
     f.e.out = dx; f.e.ldo = ld_dx; f.e.out_type = dtype;
     f.A[0] = a.hi; f.A[1] = a.lo; f.lda = p.ldq;
+    Padded ops[2];
+    const int count = b.operands(ops);
+    bool any = false;
     for (int h = 0; h < b.pair; ++h) {
+        any = any || ops[h].needed();
         f.B[h] = b.W[h];
         f.ldb[h] = b.ldw[h];
+        ops[h].p = &f.B[h]; ops[h].ld = &f.ldb[h];
     }
     f.K = (int)N; f.branches = b.pair;
-    return run(qg::FUSED_GRAD, f, p.c, b.b_trans == 0, w + p.sums, s);
+    return run(qg::FUSED_GRAD, f, p.c, b.b_trans == 0, any, ops, count, w + p.pad, w + p.sums, s);
 }
 
 }  // namespace

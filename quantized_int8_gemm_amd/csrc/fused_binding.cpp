@@ -73,7 +73,8 @@ Scale scale_of(PyObject* o, const char* name, int64_t n, bool of_rows) {
         value_error(std::string(name) + " of shape " + str(z) + " is not [" + dim + "], " + (of_rows ? "[M,1]" : "[1,N]") +
                     " or scalar (" + dim + "=" + std::to_string(n) + ")");
     }
-    return {s.reshape({-1}).contiguous(), count};
+    if (s.is_contiguous()) return {s, count};
+    return {s.contiguous(), count};
 }
 
 // A weight: [K,N], or [N,K] with b_trans.

@@ -1,0 +1,186 @@
+// Fused A8W8 products of few outputs, of weights whose rows lie along the sum: each
+// workgroup owns TM x TN outputs over all of K, its eight waves take one range of K each and
+// read their fragments straight from memory, and the waves' sums meet in LDS, where the
+// epilogue takes them.  One launch, no stages, one barrier.
+//
+// A few rows are bound by streaming the weight: lane (g, i) reads 16 bytes of row i at k-bytes
+// 64 kb + 16 g of a step, which is the matrix core's fragment as it lies in memory, NB steps
+// in flight a wave.  Small products of more rows are bound by latency: the range of K that a
+// wave walks is an eighth of what a tiled kernel's workgroup does.
+//
+// ANY: rows that are not whole 16-byte pieces, read at any alignment.
+#include "fused_common.h"
+#include "fused_load.h"
+
+namespace qg {
+namespace {
+
+constexpr int WAVES = 8, NT = 64 * WAVES, STEP = 128, KB = STEP / 64;
+constexpr uint32_t NOWHERE = 0x80000000u;   // past every buffer's end
+
+template <bool PAIR, int TM, int TN, int NB, bool ANY>
+__global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(2))) void fused_direct_kernel(FusedArgs p) {
+    constexpr int H = PAIR ? 2 : 1, FM = TM / 16, FN = TN / 16;
+    __shared__ __attribute__((aligned(16))) int red[WAVES][H][TM][TN];
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int g = lane >> 4, i16 = lane & 15;
+    const int M = p.e.M, N = p.e.N, K = p.k_bytes;
+    const int tiles_m = (M + TM - 1) / TM;
+    const int tile = xcd_remap(blockIdx.x, gridDim.x);   // an XCD's workgroups share weights
+    const int m0 = tile % tiles_m * TM, n0 = tile / tiles_m * TN;
+    const int rows = M - m0 < TM ? M - m0 : TM, cols = N - n0 < TN ? N - n0 : TN;
+    const int lda = (int)p.lda;
+    const int8_t* const A = p.A[0] + (int64_t)m0 * p.lda;
+    const __amdgpu_buffer_rsrc_t a_rsrc = make_rsrc(A, (uint32_t)((rows - 1) * lda + K));
+    const __amdgpu_buffer_rsrc_t b_rsrc = make_rsrc(p.B[0] + (int64_t)n0 * p.ldb[0], (uint32_t)((cols - 1) * (int)p.ldb[0] + K));
+    const __amdgpu_buffer_rsrc_t b_rsrc2 =
+        PAIR ? make_rsrc(p.B[1] + (int64_t)n0 * p.ldb[1], (uint32_t)((cols - 1) * (int)p.ldb[1] + K)) : b_rsrc;
+
+    const int steps = (K + STEP - 1) / STEP, mine = (steps + WAVES - 1) / WAVES, first = wave * mine;
+    u32x4 av[NB][KB][FM], bv[NB][KB][H][FN];
+    auto fetch = [&](int i, int b) {
+        const int step = first + i;
+        const bool live = i < mine && step < steps;
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            const int k = step * STEP + 64 * kb + 16 * g;
+            if constexpr (ANY) {
+                const int limit = live ? K : 0;
+#pragma unroll
+                for (int a = 0; a < FM; ++a) {
+                    const int r = 16 * a + i16;
+                    av[b][kb][a] = load16_any(A + (int64_t)(r < rows ? r : 0) * p.lda, k, r < rows ? limit : 0);
+                }
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int c = 0; c < FN; ++c) {
+                        const int r = 16 * c + i16;
+                        bv[b][kb][h][c] = load16_any(p.B[h] + (int64_t)(n0 + (r < cols ? r : 0)) * p.ldb[h], k, r < cols ? limit : 0);
+                    }
+            } else {
+                // a piece of A past K gives zeros, and B's there then adds nothing
+                const bool in = live && k < K;
+#pragma unroll
+                for (int h = 0; h < H; ++h)
+#pragma unroll
+                    for (int c = 0; c < FN; ++c)
+                        bv[b][kb][h][c] = buffer_load16(h == 0 ? b_rsrc : b_rsrc2, in ? (uint32_t)((16 * c + i16) * (int)p.ldb[h] + k) : NOWHERE, 0u);
+#pragma unroll
+                for (int a = 0; a < FM; ++a)
+                    av[b][kb][a] = buffer_load16(a_rsrc, in ? (uint32_t)((16 * a + i16) * lda + k) : NOWHERE, 0u);
+            }
+        }
+    };
+    v4i acc[H][FM][FN];
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int a = 0; a < FM; ++a)
+#pragma unroll
+            for (int c = 0; c < FN; ++c) acc[h][a][c] = v4i{0, 0, 0, 0};
+    auto consume = [&](int b) {
+#pragma unroll
+        for (int kb = 0; kb < KB; ++kb)
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int c = 0; c < FN; ++c)
+#pragma unroll
+                    for (int a = 0; a < FM; ++a) acc[h][a][c] = mfma_i8_16x16x64(bv[b][kb][h][c], av[b][kb][a], acc[h][a][c]);
+    };
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+        fetch(b, b);
+        __builtin_amdgcn_sched_barrier(0);
+    }
+
+    // The epilogue's own operands, on their way behind the first steps.  Four columns of a row
+    // to a lane; a checkpoint's eight lanes of a block stay together (TN = 32 then).
+    constexpr int GROUPS = TN / 4, ITEMS = TM * GROUPS;
+    const int item = tid, row = item / GROUPS, c4 = item % GROUPS;
+    const int m = m0 + row, n = n0 + 4 * c4, count = N - n;
+    const bool has = ITEMS >= NT || wave < ITEMS / 64;
+    v4f ws[H], bias = {0.f, 0.f, 0.f, 0.f};
+    Raw4 res = {};
+    float as = 0.f;
+#pragma unroll
+    for (int h = 0; h < H; ++h) ws[h] = v4f{0.f, 0.f, 0.f, 0.f};
+    if (has && m < M) {
+        as = p.e.act_scale[(int64_t)m * p.e.as_stride];
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (i < count) ws[h][i] = p.e.w_scale[h][(int64_t)(n + i) * p.e.ws_stride[h]];
+        if (!PAIR && p.e.bias != nullptr) bias = load4(p.e.bias, n, QG_FP32, count);
+        if (!PAIR && p.e.res != nullptr) res = load_raw4(p.e.res, (int64_t)m * p.e.ldr + n, p.e.out_type, count);
+    }
+
+    int i = 0;
+    for (; i + NB < mine; i += NB) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+            consume(b);
+            __builtin_amdgcn_sched_barrier(0);
+            fetch(i + NB + b, b);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+#pragma unroll
+    for (int b = 0; b < NB; ++b) consume(b);
+
+    // Register r of block (a, c) in lane (g, i): row 16 a + i, column 16 c + 4 g + r.
+#pragma unroll
+    for (int h = 0; h < H; ++h)
+#pragma unroll
+        for (int a = 0; a < FM; ++a)
+#pragma unroll
+            for (int c = 0; c < FN; ++c) *reinterpret_cast<v4i*>(&red[wave][h][16 * a + i16][16 * c + 4 * g]) = acc[h][a][c];
+    __syncthreads();
+    static_assert(ITEMS <= NT && ITEMS % 64 == 0, "an item a lane");
+    if (!has) return;
+    v4f z[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int h = 0; h < H; ++h) {
+        v4i s = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+            const v4i v = *reinterpret_cast<const v4i*>(&red[w][h][row][4 * c4]);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) s[q] = (int)((uint32_t)s[q] + (uint32_t)v[q]);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) z[h][q] = (float)s[q] * as * ws[h][q];
+    }
+    finish4<PAIR>(p.e, m, n, z[0], z[1], bias, res);
+}
+
+template <bool PAIR, int TM, int TN, int NB>
+hipError_t launch_tile(const FusedArgs& a, bool any, hipStream_t s) {
+    const int64_t tiles = (int64_t)((a.e.M + TM - 1) / TM) * ((a.e.N + TN - 1) / TN);
+    if (tiles * NT >= (int64_t)1 << 32) return hipErrorInvalidValue;
+    if (any) hipLaunchKernelGGL((fused_direct_kernel<PAIR, TM, TN, 2, true>), dim3((unsigned)tiles), dim3(NT), 0, s, a);
+    else hipLaunchKernelGGL((fused_direct_kernel<PAIR, TM, TN, NB, false>), dim3((unsigned)tiles), dim3(NT), 0, s, a);
+    return hipGetLastError();
+}
+
+template <bool PAIR>
+hipError_t launch(const FusedArgs& a, int tm, int tn, bool any, hipStream_t s) {
+    if (tn == 16) {
+        if (tm == 16) return launch_tile<PAIR, 16, 16, 4>(a, any, s);
+        if (tm == 32) return launch_tile<PAIR, 32, 16, 4>(a, any, s);
+        return launch_tile<PAIR, 64, 16, 2>(a, any, s);
+    }
+    if (tm == 16) return launch_tile<PAIR, 16, 32, 4>(a, any, s);
+    if (tm == 32) return launch_tile<PAIR, 32, 32, 2>(a, any, s);
+    return launch_tile<PAIR, 64, 32, 2>(a, any, s);
+}
+
+}  // namespace
+
+hipError_t launch_fused_direct(const FusedArgs& a, bool pair, int tm, int tn, bool any, hipStream_t s) {
+    return pair ? launch<true>(a, tm, tn, any, s) : launch<false>(a, tm, tn, any, s);
+}
+
+}  // namespace qg

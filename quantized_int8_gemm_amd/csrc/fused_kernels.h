@@ -32,18 +32,32 @@ struct FusedArgs {
     const int8_t* A[2]; int64_t lda;
     const int8_t* B[2]; int64_t ldb[2];
     int K, branches;
+    // Bytes that the rows along the sum hold, and columns that a [K,N] weight's rows hold: K and
+    // e.N, or up to their padding's end.
+    int k_bytes, b_cols;
     // NULL, or where `splits` workgroups a tile, of split_chunks chunks of 128 each, leave
     // their sums: int32 [splits, 1 or 2 (a pair's or a gradient's), e.M, ld_partial]
     int* partial; int splits, split_chunks; int64_t ld_partial;
 };
-// Rows and columns of sums of a tile, of two LDS stages or more (DEEP); the ANY tiles
-// take operands of any alignment.
-enum FusedTile { FUSED_256x256, FUSED_128x128, FUSED_128x128_DEEP, FUSED_64x128, FUSED_64x128_DEEP,
-                 FUSED_ANY_128x128, FUSED_ANY_64x128, FUSED_TILES };
+// Rows and columns of sums of a tile; DEEP: more than two LDS stages; ANY: operands of any
+// alignment.
+enum FusedTile { FUSED_256x256, FUSED_128x128, FUSED_128x128_DEEP, FUSED_64x128_DEEP, FUSED_ANY_64x128, FUSED_TILES };
 // kmajor: B's rows lie along the sum.
 hipError_t launch_fused_one(const FusedArgs& a, FusedTile tile, bool kmajor, hipStream_t s);
 hipError_t launch_fused_pair(const FusedArgs& a, FusedTile tile, bool kmajor, hipStream_t s);
 hipError_t launch_fused_grad(const FusedArgs& a, FusedTile tile, bool kmajor, hipStream_t s);
+
+// Matrices laid out with rows of whole 16-byte pieces, zeros behind them.
+struct PadArgs {
+    int count;
+    const int8_t* src[3]; int64_t rows[3], cols[3], ld[3];
+    int8_t* dst[3]; int64_t ldd[3];           // a multiple of 16
+};
+hipError_t launch_fused_pad(const PadArgs& a, hipStream_t s);
+
+// Products of tm x tn outputs a workgroup (16, 32 or 64 rows, 16 or 32 columns; 32 with a
+// checkpoint) of weights [N,K]; any: rows of any alignment.
+hipError_t launch_fused_direct(const FusedArgs& a, bool pair, int tm, int tn, bool any, hipStream_t s);
 
 // The second kernel of a divided sum.
 hipError_t launch_fused_join(const FusedArgs& a, int form, hipStream_t s);

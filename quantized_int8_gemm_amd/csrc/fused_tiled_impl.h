@@ -29,6 +29,7 @@
 #pragma once
 #include "fused_common.h"
 #include "fused_kernels.h"
+#include "fused_load.h"
 #include "int8_dma_impl.h"
 
 namespace qg {
@@ -48,33 +49,6 @@ __device__ __forceinline__ int kn_slot_of(int r, int s) {
     else return dma::kn_slot<RB>(r, s);
 }
 
-// 16 bytes from column c of a row of `limit` on, zeros past its end (limit 0: no load).
-// Where they would pass the end, the row's last 16 are read and moved down.
-__device__ __forceinline__ u32x4 load16_any(const int8_t* row, int c, int limit) {
-    const int past = c + 16 - limit;
-    if (past >= 16) return u32x4{0u, 0u, 0u, 0u};
-    if (limit >= 16) {
-        const v4i_any v = *reinterpret_cast<const v4i_any*>(row + (past > 0 ? limit - 16 : c));
-        uint32_t w[5] = {(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3], 0u};
-        if (past > 0) {
-#pragma unroll
-            for (int d = 2; d >= 1; d /= 2)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = past & 4 * d ? (i + d < 4 ? w[i + d] : 0u) : w[i];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = __builtin_amdgcn_alignbyte(w[i + 1], w[i], (uint32_t)past & 3u);
-        }
-        return u32x4{w[0], w[1], w[2], w[3]};
-    }
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    for (int i = 0; c + i < limit; ++i) {
-        const uint32_t b = (uint32_t)(uint8_t)row[c + i] << (8 * (i & 3));
-#pragma unroll
-        for (int q = 0; q < 4; ++q) w[q] |= i / 4 == q ? b : 0u;
-    }
-    return u32x4{w[0], w[1], w[2], w[3]};
-}
-
 template <int MODE, int BM, int BN, int WM, int WN, bool B_KMAJOR, int RING>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel(FusedArgs p) {
     constexpr bool PAIR = MODE == FUSED_PAIR, GRAD = MODE == FUSED_GRAD;
@@ -89,7 +63,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
     constexpr int STAGES = DMA ? RING : 1;
     constexpr int LOADS = A_ROUNDS + B_ROUNDS;                         // per lane and chunk
     constexpr int RB = PAIR ? BN / 2 : BN;                             // row bytes of a [K,N] tile (of each half)
-    static_assert(NT == 256 || NT == 512, "four or eight waves");
+    static_assert(NT == 512, "eight waves");
     static_assert(A_BYTES % ROUND == 0 && B_BYTES % ROUND == 0 && (BK * RB) % ROUND == 0, "whole load rounds");
     static_assert(LOADS * (STAGES - 2) < 64, "vmcnt range");
     static_assert((!GRAD || FM % 2 == 0) && (!PAIR || FN % 2 == 0), "fragments in pairs");
@@ -123,11 +97,11 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
     };
     auto b_words = [&](int h) {
         const int ld = (int)p.ldb[h];
-        return rsrc_words(b_base(h), (uint32_t)(B_KMAJOR ? (cols_b - 1) * ld + K : (K - 1) * ld + (N - n0)));
+        return rsrc_words(b_base(h), (uint32_t)(B_KMAJOR ? (cols_b - 1) * ld + p.k_bytes : (K - 1) * ld + (p.b_cols - n0)));
     };
     v4i a_rsrc = {}, b_rsrc = {}, b_rsrc2 = {};   // b_rsrc2: the second half of a [K,N] pair, or GRAD's second weight
     if constexpr (DMA) {
-        a_rsrc = rsrc_words(A, (uint32_t)((rows_a - 1) * lda + (GRAD ? all * BK : K)));
+        a_rsrc = rsrc_words(A, (uint32_t)((rows_a - 1) * lda + (GRAD ? all * BK : p.k_bytes)));
         b_rsrc = b_words(PAIR && B_KMAJOR ? half : 0);
         if ((PAIR && !B_KMAJOR) || (GRAD && p.branches == 2)) b_rsrc2 = b_words(1);
     }
@@ -163,8 +137,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
         if constexpr (DMA) {
             const uint32_t sbase = lds0 + stage * STAGE + wave * 1024;
             const uint32_t ka = (uint32_t)(kt * BK);
-            if (!GRAD && (kt + 1) * BK > K) {
-                const bool in = kt * BK + kc_col < K;
+            if (!GRAD && (kt + 1) * BK > p.k_bytes) {
+                const bool in = kt * BK + kc_col < p.k_bytes;
 #pragma unroll
                 for (int q = 0; q < A_ROUNDS; ++q) dma16(a_rsrc, in ? a_off[q] + ka : NOWHERE, sbase + q * ROUND);
             } else {
@@ -295,7 +269,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
 
     // Epilogue.  CPT lanes share a row, each with four columns; sums of row rr and columns
     // c .. c + 3 of operand h lie at chunk (c / 4) ^ (rr & 15) of row h * PR + rr.
-    constexpr int PASSES = (BM * BN * 4 + STAGES * STAGE - 1) / (STAGES * STAGE);
+    constexpr int PASSES = BM * BN * 4 <= STAGES * STAGE ? 1 : BM * BN * 2 <= STAGES * STAGE ? 2 : 4;
     static_assert(WAVES_M % PASSES == 0, "passes of whole wave rows");
     constexpr int PW = WAVES_M / PASSES, PR = BMR / PASSES, CPT = BNR / 4, ROWS_AT_ONCE = NT / CPT;
     static_assert(CPT >= 16 && NT % CPT == 0 && PR % ROWS_AT_ONCE == 0, "whole rounds of rows");
@@ -402,12 +376,10 @@ template <int MODE>
 hipError_t launch_form(const FusedArgs& a, FusedTile tile, bool kmajor, hipStream_t s) {
     switch (tile) {
         case FUSED_256x256: return launch_tile<MODE, 256, 256, 128, 64, 2>(a, kmajor, s);
-        case FUSED_128x128: return launch_tile<MODE, 128, 128, 64, 64, 2>(a, kmajor, s);
-        case FUSED_128x128_DEEP: return launch_tile<MODE, 128, 128, 64, 64, 4>(a, kmajor, s);
-        case FUSED_64x128: return launch_tile<MODE, 64, 128, 32, 64, 2>(a, kmajor, s);
-        case FUSED_64x128_DEEP: return launch_tile<MODE, 64, 128, 32, 64, 6>(a, kmajor, s);
-        case FUSED_ANY_128x128: return launch_tile<MODE, 128, 128, 64, 64, 0>(a, kmajor, s);
-        default: return launch_tile<MODE, 64, 128, 32, 64, 0>(a, kmajor, s);
+        case FUSED_128x128: return launch_tile<MODE, 128, 128, 32, 64, 2>(a, kmajor, s);
+        case FUSED_128x128_DEEP: return launch_tile<MODE, 128, 128, 64, 32, 4>(a, kmajor, s);
+        case FUSED_64x128_DEEP: return launch_tile<MODE, 64, 128, 32, 32, 6>(a, kmajor, s);
+        default: return launch_tile<MODE, 64, 128, 32, 32, 0>(a, kmajor, s);
     }
 }
 

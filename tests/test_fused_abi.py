@@ -110,15 +110,15 @@ def test_quantisers_reject_their_own():
 
 
 def test_a_short_workspace_is_refused(monkeypatch):
-    """Products through memory, and a gradient's factors."""
-    monkeypatch.setenv("QGEMM_FUSED_TILE", "5")
-    kw = dict(LINEAR, K=47, lda=47)
-    need = b.lib.qgemm_a8w8_linear_workspace_bytes(4, 40, 47, FAKE, 47, FAKE, 40, 0)
+    """The sums of a divided K, and a gradient's factors."""
+    monkeypatch.setenv("QGEMM_FUSED_SPLITS", "3")
+    kw = dict(LINEAR, K=300, lda=300)
+    need = b.lib.qgemm_a8w8_linear_workspace_bytes(4, 40, 300, FAKE, 300, FAKE, 40, 0)
     assert need > 0
     assert call("qgemm_a8w8_linear", kw, dict(ws=FAKE, wsb=need - 1)) == WS
-    need = b.lib.qgemm_a8w8_gated_workspace_bytes(4, 40, 47, FAKE, 47, FAKE, 40, FAKE, 40, 0)
+    need = b.lib.qgemm_a8w8_gated_workspace_bytes(4, 40, 300, FAKE, 300, FAKE, 40, FAKE, 40, 0)
     assert need > 0
-    assert call("qgemm_a8w8_gated", dict(GATED, K=47, lda=47), dict(ws=FAKE, wsb=need - 1)) == WS
+    assert call("qgemm_a8w8_gated", dict(GATED, K=300, lda=300), dict(ws=FAKE, wsb=need - 1)) == WS
     need = b.lib.qgemm_a8w8_linear_grad_workspace_bytes(4, 40, 48, FAKE, 40, 0, 0)
     assert call("qgemm_a8w8_linear_grad", LINEAR_GRAD, dict(wsb=need - 1)) == WS
     need = b.lib.qgemm_a8w8_gated_grad_workspace_bytes(4, 40, 48, FAKE, 40, FAKE, 40, 0)

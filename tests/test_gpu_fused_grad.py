@@ -7,7 +7,7 @@ import torch
 import fused_reference as ref
 import quantized_int8_gemm_amd as q
 from gpu_util import case, dev, env
-from test_gpu_fused_linear import check, gpu, inputs, laid, padded
+from test_gpu_fused_linear import TILES, check, gpu, inputs, laid, padded
 
 pytestmark = pytest.mark.gpu
 
@@ -194,12 +194,9 @@ def test_the_most_columns():
 
 
 @pytest.mark.parametrize("b_trans", [True, False])
-@pytest.mark.parametrize("tile", range(6))
-def test_every_tile(tile, b_trans):
-    """The tiles' sums are exact, so their bits are the same; the products through memory
-    (5) add four rounded ones."""
-    for m, n, k in ((1, 16, 16), (33, 80, 48), (64, 128, 128), (140, 400, 272), (257, 1040, 528)):
-        case(f"tile {tile} {m} {n} {k} b_trans={b_trans}")
+@pytest.mark.parametrize("tile", range(5))
+def test_every_kernel_gives_the_same_bits(tile, b_trans):
+    for m, n, k in ((1, 16, 16), (33, 80, 48), (64, 128, 128), (140, 400, 272), (257, 1040, 528), (20, 47, 33), (70, 300, 129), (130, 1025, 143)):
         _, ws, _, ss = inputs(m, n, k, m + n, 2)
         ss = [s * np.float32(np.sqrt(k) * 100) for s in ss]
         codes, scale = saved(m, n, 3, 2)
@@ -207,16 +204,17 @@ def test_every_tile(tile, b_trans):
 
         def run():
             d = q.qgemm_a8w8_gated_grad(dy, *(laid(w, b_trans) for w in ws), *map(gpu, ss), (gpu(codes), gpu(scale)), b_trans=b_trans)
+            first = q.last_kernel()
             one = q.qgemm_a8w8_linear_grad(dy, laid(ws[0], b_trans), gpu(ss[0]), (gpu(codes[0]), gpu(scale[0])), "gelu", b_trans=b_trans)
-            return d, one, q.last_kernel()
+            return d, one, first, q.last_kernel()
 
-        with env(QGEMM_FUSED_TILE=4):
+        with env(QGEMM_FUSED_TILE=4, QGEMM_FUSED_SPLITS=1, QGEMM_FUSED_PAD=0):
             want = run()
-        with env(QGEMM_FUSED_TILE=tile):
-            got = run()
-        if tile < 5:
+        for splits, pad in ((1, 0), (2, 1), (4, 0)):
+            case(f"tile {tile} {m} {n} {k} b_trans={b_trans} splits={splits} pad={pad}")
+            with env(QGEMM_FUSED_TILE=tile, QGEMM_FUSED_SPLITS=splits, QGEMM_FUSED_PAD=pad):
+                got = run()
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
-            assert got[2] == "fused_grad_" + ("256x256", "128x128", "64x128", "any_128x128", "any_64x128")[tile]
-        else:
-            for x, y in zip(got[:2], want[:2]):
-                assert ((x.double() - y.double()).abs() <= y.double().abs() * 2.0 ** -10 + y.double().abs().max() * 2.0 ** -18).all()
+            for name, branches in ((got[2], 2), (got[3], 1)):
+                joined = splits > 1 and tile > 0
+                assert (joined and -(-n // 128) * branches < splits) or name == "fused_grad_" + ("joined" if joined else TILES[tile])

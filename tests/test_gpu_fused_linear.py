@@ -187,46 +187,69 @@ def test_outputs_without_elements():
         q.qgemm_a8w8_linear(gpu(a)[:, :0], gpu(w)[:, :0], gpu(sa), gpu(sw), b_trans=True)
 
 
-TILES = {0: "256x256", 1: "128x128", 2: "64x128", 3: "any_128x128", 4: "any_64x128"}
+TILES = ("256x256", "128x128", "128x128_deep", "64x128_deep", "any_64x128", "direct_16x16", "direct_16x32", "direct_32x16",
+         "direct_32x32", "direct_64x16", "direct_64x32")
+
+
+def taken(tile, b_trans, checkpoint):
+    """Whether a forced kind takes the call: the direct ones want [N,K], and 32 columns for a
+    checkpoint's blocks."""
+    return not TILES[tile].startswith("direct") or (b_trans and not (checkpoint and TILES[tile].endswith("x16")))
 
 
 @pytest.mark.parametrize("b_trans", [True, False])
-@pytest.mark.parametrize("tile", range(6))
-def test_every_tile_gives_the_same_bits(tile, b_trans):
-    """Sums are exact and the epilogue is one, so outputs and checkpoints do not depend on
-    the kernel (5: products through memory)."""
-    for m, n, k in ((1, 16, 16), (33, 48, 80), (64, 128, 128), (300, 272, 400), (515, 528, 1040)):
-        case(f"tile {tile} {m} {n} {k} b_trans={b_trans}")
+@pytest.mark.parametrize("tile", range(len(TILES)))
+def test_every_kernel_gives_the_same_bits(tile, b_trans):
+    """Sums are exact and the epilogue is one, so outputs and checkpoints depend neither on
+    the kernel nor on how K is divided, nor on padding."""
+    for i, (m, n, k) in enumerate(((1, 16, 16), (33, 48, 80), (64, 128, 128), (300, 272, 400), (515, 528, 1040), (20, 33, 47), (70, 129, 300),
+                                   (130, 143, 1025))):
         a, (wg, wu), sa, (sg, su) = inputs(m, n, k, m + n, 2)
         args = (gpu(a), laid(wg, b_trans), laid(wu, b_trans), gpu(sa), gpu(sg), gpu(su))
         res = torch.randn(m, n, device=dev()).half()
-        kw = dict(b_trans=b_trans, checkpoint=True)
+        pieces = k % 16 == 0 and (b_trans or n % 16 == 0)
 
-        def run():
-            y = q.qgemm_a8w8_gated(*args, out_dtype=torch.bfloat16, **kw)
+        def run(checkpoint):
+            y = q.qgemm_a8w8_gated(*args, out_dtype=torch.bfloat16, b_trans=b_trans, checkpoint=checkpoint)
             first = q.last_kernel()
-            z = q.qgemm_a8w8_linear(args[0], args[1], args[3], args[4], residual=res, activation="gelu", out_dtype=torch.float16, **kw)
-            return (y[0], *y[1], z[0], *z[1]), first, q.last_kernel()
+            z = q.qgemm_a8w8_linear(args[0], args[1], args[3], args[4], residual=res, activation="gelu", out_dtype=torch.float16,
+                                    b_trans=b_trans, checkpoint=checkpoint)
+            second = q.last_kernel()
+            return (y[0], *y[1], z[0], *z[1]) if checkpoint else (y, z), first, second
 
-        with env(QGEMM_FUSED_TILE=5):
-            want, first, second = run()
-            assert first == second == "a8w8_then_finish"
-        with env(QGEMM_FUSED_TILE=tile):
-            got, first, second = run()
-            if tile < 5:
-                assert first == "fused_pair_" + TILES[tile] and second == "fused_one_" + TILES[tile]
-        for x, y in zip(got, want):
-            assert torch.equal(x, y)
+        with env(QGEMM_FUSED_TILE=4, QGEMM_FUSED_SPLITS=1, QGEMM_FUSED_PAD=0):
+            want, first, _ = run(True)
+            assert first == "fused_pair_any_64x128"
+        for splits in (1, 2, 6):
+            for checkpoint in (True, False):
+                case(f"tile {tile} {m} {n} {k} b_trans={b_trans} splits={splits} checkpoint={checkpoint}")
+                with env(QGEMM_FUSED_TILE=tile, QGEMM_FUSED_SPLITS=splits):
+                    got, first, second = run(checkpoint)
+                can = tile in (1, 2, 3, 4)
+                if taken(tile, b_trans, checkpoint) and (not can or -(-k // 128) >= splits):
+                    joined = can and splits > 1
+                    assert first == "fused_pair_" + ("joined" if joined else TILES[tile])
+                    assert second == "fused_one_" + ("joined" if joined else TILES[tile])
+                for x, y in zip(got, want if checkpoint else (want[0], want[3])):
+                    assert torch.equal(x, y)
+        if not pieces:
+            for pad in (0, 1):
+                with env(QGEMM_FUSED_PAD=pad):
+                    got, _, _ = run(True)
+                for x, y in zip(got, want):
+                    assert torch.equal(x, y)
 
 
-@pytest.mark.parametrize("tile", range(5))
-def test_what_lies_past_k_adds_nothing(tile):
-    """Rows longer than K, with other values behind K, and a K that ends inside a chunk."""
+@pytest.mark.parametrize("pad", [0, 1])
+@pytest.mark.parametrize("tile", range(len(TILES)))
+def test_what_lies_past_k_adds_nothing(tile, pad):
+    """Rows longer than K, with other values behind K, and a K that ends inside a chunk or a
+    16-byte piece."""
     m, n = 70, 144
-    for k in (16, 48, 144, 272):
+    for k in (1, 16, 47, 48, 144, 272, 273):
         a, (w, _), sa, (sw, _) = inputs(m, n, 512, k, 2)
         A, W = gpu(a), gpu(w)
-        with env(QGEMM_FUSED_TILE=tile):
+        with env(QGEMM_FUSED_TILE=tile, QGEMM_FUSED_PAD=pad):
             got = q.qgemm_a8w8_linear(A[:, :k], W[:, :k], gpu(sa), gpu(sw), b_trans=True)
             also = q.qgemm_a8w8_linear(A[:, :k], W.t().contiguous()[:k], gpu(sa), gpu(sw))
         want = ref.z32(ref.accumulate(a[:, :k], w[:, :k], True), sa, sw)
