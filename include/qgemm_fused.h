@@ -60,7 +60,7 @@ typedef enum {
  */
 size_t qgemm_a8w8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K,
                                          const int8_t* A, int64_t lda,
-                                         const int8_t* W, int64_t ldw, int b_trans);
+                                         const int8_t* W, int64_t ldw, int b_trans, int with_checkpoint);
 qg_status qgemm_a8w8_linear(int64_t M, int64_t N, int64_t K,
                             const int8_t* A, int64_t lda,
                             const int8_t* W, int64_t ldw, int b_trans,
@@ -87,7 +87,7 @@ qg_status qgemm_a8w8_linear(int64_t M, int64_t N, int64_t K,
 size_t qgemm_a8w8_gated_workspace_bytes(int64_t M, int64_t N, int64_t K,
                                         const int8_t* A, int64_t lda,
                                         const int8_t* W_gate, int64_t ld_gate,
-                                        const int8_t* W_up, int64_t ld_up, int b_trans);
+                                        const int8_t* W_up, int64_t ld_up, int b_trans, int with_checkpoint);
 qg_status qgemm_a8w8_gated(int64_t M, int64_t N, int64_t K,
                            const int8_t* A, int64_t lda,
                            const int8_t* W_gate, int64_t ld_gate,

@@ -24,10 +24,10 @@ INT8_BLOCK = 32
 
 # C prototypes, in the order of include/qgemm_fused.h.
 PROTOTYPES = {
-    "qgemm_a8w8_linear_workspace_bytes": ([_i64, _i64, _i64, _p, _i64, _p, _i64, _int], _sz),
+    "qgemm_a8w8_linear_workspace_bytes": ([_i64, _i64, _i64, _p, _i64, _p, _i64, _int, _int], _sz),
     "qgemm_a8w8_linear": ([_i64, _i64, _i64, _p, _i64, _p, _i64, _int, _p, _i64, _p, _i64, _p, _int, _p, _i64, _p, _int, _i64,
                            _p, _i64, _p, _i64, _p, _sz, _p], _int),
-    "qgemm_a8w8_gated_workspace_bytes": ([_i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _int], _sz),
+    "qgemm_a8w8_gated_workspace_bytes": ([_i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _int, _int], _sz),
     "qgemm_a8w8_gated": ([_i64, _i64, _i64, _p, _i64, _p, _i64, _p, _i64, _int, _p, _i64, _p, _i64, _p, _i64, _int, _p, _int, _i64,
                           _p, _i64, _p, _i64, _p, _sz, _p], _int),
     "qgemm_a8w8_linear_grad_workspace_bytes": ([_i64, _i64, _i64, _p, _i64, _int, _int], _sz),

@@ -2,6 +2,7 @@
 // plans, kernel choice and launch, with the launch-status convention of api.cpp.
 #include <algorithm>
 #include <cmath>
+#include <cstdio>
 #include <cstdlib>
 
 #include <hip/hip_runtime.h>
@@ -41,10 +42,14 @@ bool span_ok(int64_t K, int64_t lda, int64_t ldw, int b_trans) {
     return 256 * lda + K + 256 < SPAN_LIMIT && (b_trans ? 256 * ldw + K + 256 : (K + 256) * ldw) < SPAN_LIMIT;
 }
 
-int env_int(const char* name, int dflt) {
-    const char* v = std::getenv(name);
-    return v != nullptr && *v ? std::atoi(v) : dflt;
-}
+// QGEMM_FUSED="kind[/parts[/pad]]" forces a kind (its number), a number of parts of K and
+// padding (0: none) where the call allows them, -1 for what is left open; for tests and tuning.
+struct Forced {
+    int kind = -1, parts = -1, pad = -1;
+    Forced() {
+        if (const char* v = std::getenv("QGEMM_FUSED")) std::sscanf(v, "%d/%d/%d", &kind, &parts, &pad);
+    }
+};
 
 // Rows of whole 16-byte pieces.
 bool whole_pieces(const void* p, int64_t ld, int64_t n) { return aligned(p, 16) && ld % 16 == 0 && n % 16 == 0; }
@@ -98,22 +103,23 @@ double time_of(const Shape& s, int tile, int splits, bool pad) {
         default: {
             const double tm = direct_rows(tile), tn = direct_cols(tile);
             const double bytes = (std::min<double>(tm, s.M) + tn * (s.form == qg::FUSED_PAIR ? 2 : 1)) * (double)s.K;
-            t = 1.5 + std::max(1.0, std::ceil(s.M / tm) * std::ceil(s.N / tn) / 256) * (bytes / (s.pieces || pad ? 35e3 : 16e3) + 0.8);
+            t = 1.5 + std::max(1.0, std::ceil((double)s.M / tm) * std::ceil((double)s.N / tn) / 256) * (bytes / (s.pieces || pad ? 35e3 : 16e3) + 0.8);
         }
     }
     if (splits > 1) t += 3 + rows * cols * 8 * splits / 3e6;
     if (pad) t += 3 + 2 * (double)s.pad_bytes / 4e6;
-    // no faster than the operands come from memory
-    const double floor = (rows + cols) * (double)s.K * s.branches / 5e6;
-    return std::max(t, floor) + 0.02 * t;
+    // No faster than the operands come from memory; the rows that every direct workgroup reads
+    // again come from L2, but with the weight's (16 x 14336 x 4096 gated 31 us, tiles 29; one row
+    // 25 and 29).
+    const double floor = tile >= DIRECT ? (cols + std::min<double>(direct_rows(tile), s.M) * std::ceil((double)s.N / direct_cols(tile))) / 5.6e6
+                                        : (rows + cols) / 4.7e6;
+    return std::max(t, floor * (double)s.K * s.branches) + 0.02 * t;
 }
 
-// The kind that takes the least time by this reckoning.  QGEMM_FUSED_TILE, QGEMM_FUSED_SPLITS and
-// QGEMM_FUSED_PAD force a kind, a number of parts of K and padding (0: none), where the call allows
-// them; for tests and tuning.
+// The kind that takes the least time by this reckoning.
 Choice choose(const Shape& s) {
     const int64_t chunks = (s.K + 127) / 128 * s.branches;
-    const int tile = env_int("QGEMM_FUSED_TILE", -1), splits = env_int("QGEMM_FUSED_SPLITS", 0), pad = env_int("QGEMM_FUSED_PAD", -1);
+    const Forced forced;
     Choice best{qg::FUSED_ANY_64x128, 1, 0, false, 0, (s.N + 3) / 4 * 4};
     double least = 1e30;
     static const int parts[] = {1, 2, 3, 4, 6, 8, 12, 16};
@@ -126,8 +132,8 @@ Choice choose(const Shape& s) {
             for (const int p : parts) {
                 if (p > 1 && (direct || k == qg::FUSED_256x256 || p > chunks)) break;
                 // what is forced goes before what is not
-                const double t = time_of(s, k, p, with_pad == 1) + (tile >= 0 && tile < KINDS && k != tile ? 1e12 : 0) +
-                                 (pad >= 0 && with_pad != (pad != 0) ? 1e9 : 0) + (splits > 0 && p != splits ? 1e6 : 0);
+                const double t = time_of(s, k, p, with_pad == 1) + (forced.kind >= 0 && k != forced.kind ? 1e12 : 0) +
+                                 (forced.pad >= 0 && with_pad != forced.pad ? 1e9 : 0) + (forced.parts > 0 && p != forced.parts ? 1e6 : 0);
                 if (t >= least) continue;
                 least = t;
                 best.tile = k;
@@ -244,15 +250,10 @@ bool sizes_bad(int64_t M, int64_t N, int64_t K) {
     return M < 0 || N < 0 || K < 0 || M >= LIM || N >= LIM || K >= LIM;
 }
 
-// With and without a checkpoint: the larger.
-size_t forward_workspace(Forward f) {
+size_t forward_workspace(Forward f, bool blocks) {
     if (sizes_bad(f.M, f.N, f.K) || f.M == 0 || f.N == 0 || f.K == 0) return 0;
-    size_t most = 0;
-    for (const bool blocks : {false, true}) {
-        const Choice c = f.choice(blocks);
-        most = std::max(most, (c.pad ? f.pad_bytes() : 0) + up256(c.bytes));
-    }
-    return most;
+    const Choice c = f.choice(blocks);
+    return (c.pad ? f.pad_bytes() : 0) + up256(c.bytes);
 }
 
 bool checkpoint_ok(const int8_t* c, int64_t ldc, const float* s, int64_t lds, int64_t N) {
@@ -441,8 +442,8 @@ qg_status backward(Backward b, const void* dy, qg_dtype dtype, int64_t ld_dy, co
 extern "C" {
 
 size_t qgemm_a8w8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const int8_t* W,
-                                         int64_t ldw, int b_trans) {
-    return forward_workspace({M, N, K, A, lda, {W, nullptr}, {ldw, 0}, b_trans, 1});
+                                         int64_t ldw, int b_trans, int with_checkpoint) {
+    return forward_workspace({M, N, K, A, lda, {W, nullptr}, {ldw, 0}, b_trans, 1}, with_checkpoint != 0);
 }
 
 qg_status qgemm_a8w8_linear(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const int8_t* W, int64_t ldw,
@@ -458,8 +459,8 @@ qg_status qgemm_a8w8_linear(int64_t M, int64_t N, int64_t K, const int8_t* A, in
 }
 
 size_t qgemm_a8w8_gated_workspace_bytes(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const int8_t* W_gate,
-                                        int64_t ld_gate, const int8_t* W_up, int64_t ld_up, int b_trans) {
-    return forward_workspace({M, N, K, A, lda, {W_gate, W_up}, {ld_gate, ld_up}, b_trans, 2});
+                                        int64_t ld_gate, const int8_t* W_up, int64_t ld_up, int b_trans, int with_checkpoint) {
+    return forward_workspace({M, N, K, A, lda, {W_gate, W_up}, {ld_gate, ld_up}, b_trans, 2}, with_checkpoint != 0);
 }
 
 qg_status qgemm_a8w8_gated(int64_t M, int64_t N, int64_t K, const int8_t* A, int64_t lda, const int8_t* W_gate, int64_t ld_gate,

@@ -166,7 +166,7 @@ PyObject* py_linear(PyObject*, PyObject* const* v, Py_ssize_t argc) {
     if (!out.defined()) out = make({m, w.n}, d, A);
     const Matrix om = matrix(out, "out");
     const Checkpoint c = save ? new_checkpoint(1, m, w.n, A) : Checkpoint{};
-    const size_t need = entry.linear_workspace(m, w.n, k, (const int8_t*)ptr(A), a.ld, (const int8_t*)ptr(w.t), w.ld, b_trans);
+    const size_t need = entry.linear_workspace(m, w.n, k, (const int8_t*)ptr(A), a.ld, (const int8_t*)ptr(w.t), w.ld, b_trans, save);
     const Tensor work = workspace_of(need, A);
     launch(A, "qgemm_a8w8_linear", [&](void* s) {
         return entry.linear(m, w.n, k, (const int8_t*)ptr(A), a.ld, (const int8_t*)ptr(w.t), w.ld, b_trans, (const float*)ptr(as.t),
@@ -201,7 +201,7 @@ PyObject* py_gated(PyObject*, PyObject* const* v, Py_ssize_t argc) {
     const Matrix om = matrix(out, "out");
     const Checkpoint c = save ? new_checkpoint(2, m, g.n, A) : Checkpoint{};
     const size_t need = entry.gated_workspace(m, g.n, k, (const int8_t*)ptr(A), a.ld, (const int8_t*)ptr(g.t), g.ld,
-                                              (const int8_t*)ptr(u.t), u.ld, b_trans);
+                                              (const int8_t*)ptr(u.t), u.ld, b_trans, save);
     const Tensor work = workspace_of(need, A);
     launch(A, "qgemm_a8w8_gated", [&](void* s) {
         return entry.gated(m, g.n, k, (const int8_t*)ptr(A), a.ld, (const int8_t*)ptr(g.t), g.ld, (const int8_t*)ptr(u.t), u.ld,

@@ -111,12 +111,12 @@ def test_quantisers_reject_their_own():
 
 def test_a_short_workspace_is_refused(monkeypatch):
     """The sums of a divided K, and a gradient's factors."""
-    monkeypatch.setenv("QGEMM_FUSED_SPLITS", "3")
+    monkeypatch.setenv("QGEMM_FUSED", "3/3")
     kw = dict(LINEAR, K=300, lda=300)
-    need = b.lib.qgemm_a8w8_linear_workspace_bytes(4, 40, 300, FAKE, 300, FAKE, 40, 0)
+    need = b.lib.qgemm_a8w8_linear_workspace_bytes(4, 40, 300, FAKE, 300, FAKE, 40, 0, 0)
     assert need > 0
     assert call("qgemm_a8w8_linear", kw, dict(ws=FAKE, wsb=need - 1)) == WS
-    need = b.lib.qgemm_a8w8_gated_workspace_bytes(4, 40, 300, FAKE, 300, FAKE, 40, FAKE, 40, 0)
+    need = b.lib.qgemm_a8w8_gated_workspace_bytes(4, 40, 300, FAKE, 300, FAKE, 40, FAKE, 40, 0, 0)
     assert need > 0
     assert call("qgemm_a8w8_gated", dict(GATED, K=300, lda=300), dict(ws=FAKE, wsb=need - 1)) == WS
     need = b.lib.qgemm_a8w8_linear_grad_workspace_bytes(4, 40, 48, FAKE, 40, 0, 0)
@@ -124,7 +124,7 @@ def test_a_short_workspace_is_refused(monkeypatch):
     need = b.lib.qgemm_a8w8_gated_grad_workspace_bytes(4, 40, 48, FAKE, 40, FAKE, 40, 0)
     assert call("qgemm_a8w8_gated_grad", GATED_GRAD, dict(wsb=need - 1)) == WS
     for M, N, K in ((0, 40, 48), (4, 0, 48), (4, 40, 0), (-1, 40, 48), (1 << 30, 40, 48)):
-        assert b.lib.qgemm_a8w8_linear_workspace_bytes(M, N, K, FAKE, 47, FAKE, 40, 0) == 0
+        assert b.lib.qgemm_a8w8_linear_workspace_bytes(M, N, K, FAKE, 47, FAKE, 40, 0, 1) == 0
         assert b.lib.qgemm_a8w8_linear_grad_workspace_bytes(M, N, K, FAKE, 40, 0, 1) == 0
 
 

@@ -208,11 +208,11 @@ def test_every_kernel_gives_the_same_bits(tile, b_trans):
             one = q.qgemm_a8w8_linear_grad(dy, laid(ws[0], b_trans), gpu(ss[0]), (gpu(codes[0]), gpu(scale[0])), "gelu", b_trans=b_trans)
             return d, one, first, q.last_kernel()
 
-        with env(QGEMM_FUSED_TILE=4, QGEMM_FUSED_SPLITS=1, QGEMM_FUSED_PAD=0):
+        with env(QGEMM_FUSED="4/1/0"):
             want = run()
         for splits, pad in ((1, 0), (2, 1), (4, 0)):
             case(f"tile {tile} {m} {n} {k} b_trans={b_trans} splits={splits} pad={pad}")
-            with env(QGEMM_FUSED_TILE=tile, QGEMM_FUSED_SPLITS=splits, QGEMM_FUSED_PAD=pad):
+            with env(QGEMM_FUSED=f"{tile}/{splits}/{pad}"):
                 got = run()
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
             for name, branches in ((got[2], 2), (got[3], 1)):

@@ -217,13 +217,13 @@ def test_every_kernel_gives_the_same_bits(tile, b_trans):
             second = q.last_kernel()
             return (y[0], *y[1], z[0], *z[1]) if checkpoint else (y, z), first, second
 
-        with env(QGEMM_FUSED_TILE=4, QGEMM_FUSED_SPLITS=1, QGEMM_FUSED_PAD=0):
+        with env(QGEMM_FUSED="4/1/0"):
             want, first, _ = run(True)
             assert first == "fused_pair_any_64x128"
         for splits in (1, 2, 6):
             for checkpoint in (True, False):
                 case(f"tile {tile} {m} {n} {k} b_trans={b_trans} splits={splits} checkpoint={checkpoint}")
-                with env(QGEMM_FUSED_TILE=tile, QGEMM_FUSED_SPLITS=splits):
+                with env(QGEMM_FUSED=f"{tile}/{splits}"):
                     got, first, second = run(checkpoint)
                 can = tile in (1, 2, 3, 4)
                 if taken(tile, b_trans, checkpoint) and (not can or -(-k // 128) >= splits):
@@ -234,7 +234,7 @@ def test_every_kernel_gives_the_same_bits(tile, b_trans):
                     assert torch.equal(x, y)
         if not pieces:
             for pad in (0, 1):
-                with env(QGEMM_FUSED_PAD=pad):
+                with env(QGEMM_FUSED=f"-1/-1/{pad}"):
                     got, _, _ = run(True)
                 for x, y in zip(got, want):
                     assert torch.equal(x, y)
@@ -249,7 +249,7 @@ def test_what_lies_past_k_adds_nothing(tile, pad):
     for k in (1, 16, 47, 48, 144, 272, 273):
         a, (w, _), sa, (sw, _) = inputs(m, n, 512, k, 2)
         A, W = gpu(a), gpu(w)
-        with env(QGEMM_FUSED_TILE=tile, QGEMM_FUSED_PAD=pad):
+        with env(QGEMM_FUSED=f"{tile}/-1/{pad}"):
             got = q.qgemm_a8w8_linear(A[:, :k], W[:, :k], gpu(sa), gpu(sw), b_trans=True)
             also = q.qgemm_a8w8_linear(A[:, :k], W.t().contiguous()[:k], gpu(sa), gpu(sw))
         want = ref.z32(ref.accumulate(a[:, :k], w[:, :k], True), sa, sw)
