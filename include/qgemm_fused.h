@@ -57,6 +57,9 @@ typedef enum {
  *   out: QG_FP32, QG_BF16 or QG_FP16, rounded once.
  *   checkpoint: NULL, or int8 [M,N] that receives z in int8 form by blocks of 32,
  *     checkpoint_scale [M, (N + 31) / 32] its scales.
+ * QG_ERR_UNSUPPORTED, here and in the calls below, if operands pass the spans that
+ * qgemm_a8w8 takes, or a leading dimension of an output, residual or checkpoint is 2^22 or
+ * more.
  */
 size_t qgemm_a8w8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K,
                                          const int8_t* A, int64_t lda,

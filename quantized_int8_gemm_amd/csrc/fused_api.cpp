@@ -101,18 +101,19 @@ double time_of(const Shape& s, int tile, int splits, bool pad) {
         case qg::FUSED_64x128_DEEP: t = std::ceil(tiles(64, 128) / 256) * (per * 0.36 + 1.5); break;
         case qg::FUSED_ANY_64x128: t = std::max(1.6, std::ceil(tiles(64, 128) / 256) * 1.04) * per + 2; break;
         default: {
-            const double tm = direct_rows(tile), tn = direct_cols(tile);
+            const double tm = direct_rows(tile), tn = direct_cols(tile), n = std::ceil(s.M / tm) * std::ceil(s.N / tn) / 256;
             const double bytes = (std::min<double>(tm, s.M) + tn * (s.form == qg::FUSED_PAIR ? 2 : 1)) * (double)s.K;
-            t = 1.5 + std::max(1.0, std::ceil((double)s.M / tm) * std::ceil((double)s.N / tn) / 256) * (bytes / (s.pieces || pad ? 35e3 : 16e3) + 0.8);
+            t = 1.3 + std::max(1.0, n) * bytes / (s.pieces || pad ? 37e3 : 16e3) + 0.35 * n;
         }
     }
-    if (splits > 1) t += 3 + rows * cols * 8 * splits / 3e6;
+    if (splits > 1) t += 4.5 + rows * cols * 8 * splits / 3e6;
     if (pad) t += 3 + 2 * (double)s.pad_bytes / 4e6;
-    // No faster than the operands come from memory; the rows that every direct workgroup reads
-    // again come from L2, but with the weight's (16 x 14336 x 4096 gated 31 us, tiles 29; one row
-    // 25 and 29).
-    const double floor = tile >= DIRECT ? (cols + std::min<double>(direct_rows(tile), s.M) * std::ceil((double)s.N / direct_cols(tile))) / 5.6e6
-                                        : (rows + cols) / 4.7e6;
+    // No faster than the operands come from memory, and the rows that every direct workgroup
+    // reads again from L2 (1 and 16 x 14336 x 4096 gated 27 and 34 us, with 32 columns a workgroup 33
+    // and 35, tiles 31).
+    const double floor = tile < DIRECT ? (rows + cols) / 4.7e6
+                                       : cols / (direct_cols(tile) == 16 ? 4.9e6 : 4.1e6) +
+                                             std::min<double>(direct_rows(tile), s.M) * std::ceil((double)s.N / direct_cols(tile)) / 8.5e6;
     return std::max(t, floor * (double)s.K * s.branches) + 0.02 * t;
 }
 
@@ -256,6 +257,9 @@ size_t forward_workspace(Forward f, bool blocks) {
     return (c.pad ? f.pad_bytes() : 0) + up256(c.bytes);
 }
 
+// Rows of an output, residual or checkpoint of which a tile's 256 stay within 32-bit offsets.
+bool rows_ok(int64_t ld) { return ld < (int64_t)1 << 22; }
+
 bool checkpoint_ok(const int8_t* c, int64_t ldc, const float* s, int64_t lds, int64_t N) {
     return c != nullptr && s != nullptr && aligned(s, 4) && ldc >= N && lds >= blocks_of(N);
 }
@@ -278,7 +282,9 @@ qg_status forward(Forward f, const Scales& act, const Scales* ws, const float* b
     if (workspace != nullptr && !aligned(workspace, 256)) return QG_ERR_INVALID_ARGUMENT;
     for (int h = 0; h < f.pair; ++h)
         if (!span_ok(K, f.lda, f.ldw[h], f.b_trans)) return QG_ERR_UNSUPPORTED;
-    if (too_many_tiles(M, N * f.pair)) return QG_ERR_UNSUPPORTED;
+    if (too_many_tiles(M, N * f.pair) || !rows_ok(ldo) || (res != nullptr && !rows_ok(ldr)) ||
+        (ckpt != nullptr && (!rows_ok(ld_ckpt) || !rows_ok(ld_ckpt_scale))))
+        return QG_ERR_UNSUPPORTED;
     const Choice c = f.choice(ckpt != nullptr);
     const size_t pad = c.pad ? f.pad_bytes() : 0, need = pad + up256(c.bytes);
     if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return QG_ERR_WORKSPACE;
@@ -394,7 +400,7 @@ qg_status backward(Backward b, const void* dy, qg_dtype dtype, int64_t ld_dy, co
     const GradPlan p(b);
     for (int h = 0; h < b.pair; ++h)
         if (!span_ok(N, p.ldq, b.ldw[h], !b.b_trans)) return QG_ERR_UNSUPPORTED;
-    if (too_many_tiles(2 * M, K)) return QG_ERR_UNSUPPORTED;
+    if (too_many_tiles(2 * M, K) || !rows_ok(ld_dx)) return QG_ERR_UNSUPPORTED;
     if (workspace == nullptr || workspace_bytes < p.bytes) return QG_ERR_WORKSPACE;
     (void)hipGetLastError();
     const hipStream_t s = (hipStream_t)stream;

@@ -15,25 +15,28 @@ __device__ __forceinline__ float sigmoid(float z) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504f));
 }
 
-// The argument of GELU_TANH's sigmoid (tanh y = 2 sigmoid(2 y) - 1): 2 sqrt(2 / pi) (z +
-// 0.044715 z^3).  Past 32 the sigmoid is 0 or 1 to the last bit, and z^3 could pass
-// fp32's range.
-__device__ __forceinline__ float gelu_tanh_arg(float z, float& square) {
-    const float c = __builtin_amdgcn_fmed3f(z, -32.f, 32.f);
-    square = c * c;
-    return 1.59576912f * c * __builtin_fmaf(0.044715f, square, 1.0f);
+// The normal distribution's Phi(z) = (1 + erf(z / sqrt 2)) / 2 from density = exp(-z^2 / 2): with
+// x = |z| / sqrt 2 and t = 1 / (1 + 0.3275911 x), erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2), to 1.5e-7
+// (Abramowitz and Stegun 7.1.26); 13 instructions where erff takes about 40, which is
+// most of a checkpointed product's epilogue.
+__device__ __forceinline__ float normal_cdf(float z, float density) {
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.23164190f, __builtin_fabsf(z), 1.0f));
+    float q = __builtin_fmaf(t, 0.53070271f, -0.72657601f);
+    q = __builtin_fmaf(t, q, 0.71070687f);
+    q = __builtin_fmaf(t, q, -0.14224837f);
+    q = __builtin_fmaf(t, q, 0.12741480f);
+    q = q * t * density;   // erfc(x) / 2
+    return z < 0.f ? q : 1.0f - q;
 }
 
 template <int KIND>
 __device__ __forceinline__ float activate(float z) {
     if constexpr (KIND == QG_ACT_RELU) return z < 0.f ? 0.f : z;
     else if constexpr (KIND == QG_ACT_SILU) return z * sigmoid(z);
-    else if constexpr (KIND == QG_ACT_GELU) return 0.5f * z * (1.0f + erff(z * 0.70710678f));
-    else if constexpr (KIND == QG_ACT_GELU_TANH) {
-        float sq;
-        const float s = sigmoid(gelu_tanh_arg(z, sq));
-        return z != z ? z : z * s;   // the clamp drops a NaN
-    } else return z;
+    else if constexpr (KIND == QG_ACT_GELU) return z * normal_cdf(z, __builtin_amdgcn_exp2f(z * z * -0.72134752f));
+    // tanh y = 2 sigmoid(2 y) - 1; where z^3 passes fp32's range the sigmoid is 0 or 1 all the same
+    else if constexpr (KIND == QG_ACT_GELU_TANH) return z * sigmoid(1.59576912f * z * __builtin_fmaf(0.044715f, z * z, 1.0f));
+    else return z;
 }
 
 // The activation and its derivative at a checkpoint's value.
@@ -47,18 +50,17 @@ __device__ __forceinline__ void activate_both(float z, float& f, float& slope) {
     } else if constexpr (KIND == QG_ACT_SILU) {
         const float e = sigmoid(z);
         f = z * e;
-        slope = e * (1.0f + z * (1.0f - e));
+        slope = __builtin_fmaf(f, 1.0f - e, e);
     } else if constexpr (KIND == QG_ACT_GELU) {
-        const float c = 0.5f * (1.0f + erff(z * 0.70710678f));
+        const float density = __builtin_amdgcn_exp2f(z * z * -0.72134752f), c = normal_cdf(z, density);
         f = z * c;
-        slope = c + z * 0.39894228f * __builtin_amdgcn_exp2f(z * z * -0.72134752f);
+        slope = __builtin_fmaf(z * 0.39894228f, density, c);
     } else if constexpr (KIND == QG_ACT_GELU_TANH) {
-        float sq;
-        const float e = sigmoid(gelu_tanh_arg(z, sq));
-        const float c = __builtin_amdgcn_fmed3f(z, -32.f, 32.f);
+        const float c = __builtin_amdgcn_fmed3f(z, -32.f, 32.f), sq = c * c;   // past 32 the sigmoid is 0 or 1
+        const float e = sigmoid(1.59576912f * c * __builtin_fmaf(0.044715f, sq, 1.0f));
         f = z * e;
-        slope = e + c * e * (1.0f - e) * 1.59576912f * __builtin_fmaf(0.134145f, sq, 1.0f);
-        if (z != z) slope = z;
+        slope = __builtin_fmaf(c * e * (1.0f - e) * 1.59576912f, __builtin_fmaf(0.134145f, sq, 1.0f), e);
+        if (z != z) slope = z;   // the clamp drops a NaN
     }
 }
 
@@ -93,29 +95,44 @@ __device__ __forceinline__ float over_127(float x) {
     return __builtin_fmaf(__builtin_fmaf(-127.0f, q, x), 0x1.020408p-7f, q);
 }
 
-// From the bits of the largest magnitude: codes are rint((v * up) * inv).
+// The nearest whole number to a |v| < 2^22, ties to even, in the sum's low bits.  v, a product,
+// is rounded first: in one instruction with the sum it would not be, and ties fall otherwise.
+__device__ __forceinline__ uint32_t nearest_bits(float v) {
+#pragma clang fp contract(off)
+    return __float_as_uint(v + 12582912.0f);
+}
+
+// The low bytes of four words (shift 0) or the next ones (shift 1).
+__device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d, int shift = 0) {
+    const uint32_t sel = shift == 0 ? 0x0c0c0400u : 0x0c0c0501u;
+    const uint32_t lo = __builtin_amdgcn_perm(b, a, sel), hi = __builtin_amdgcn_perm(d, c, sel);
+    return __builtin_amdgcn_perm(hi, lo, 0x05040100u);
+}
+
+// From the bits of the largest magnitude: codes are rint((v * up) * inv).  A NaN or an
+// infinity makes inv 0, and its own product with that a NaN, whose low bits are 0.
 struct Int8Form {
-    float up, inv, scale;
-    bool bad;
+    float inv, scale, up = 1.0f;
     __device__ __forceinline__ explicit Int8Form(uint32_t top) {
         const float most = __uint_as_float(top);
-        bad = top >= INF_BITS;
-        up = 1.0f;
         inv = quotient_127(most);
         scale = over_127(most);
-        if (most < 0x1p-100f || most > 0x1p120f) {   // rare: 127 / most would not be finite, or its reciprocal not normal
-            up = most < 1.0f ? 0x1p60f : 1.0f;
-            inv = top == 0u ? 0.f : 127.0f / (most * up);
-            scale = top == 0u ? 1.0f : most / 127.0f;
-        }
-        if (bad) {
-            inv = 0.f;
-            scale = __uint_as_float(0x7fc00000u);
+        // rare: zeros, 127 / most not finite or its reciprocal not normal, most not finite
+        if (top - 0x0d800000u > 0x7b800000u - 0x0d800000u) {   // outside 2^-100 .. 2^120
+            if (most < 1.0f) up = 0x1p60f;
+            inv = top == 0u || top >= INF_BITS ? 0.f : 127.0f / (most * up);
+            scale = top >= INF_BITS ? __uint_as_float(0x7fc00000u) : top == 0u ? 1.0f : most / 127.0f;
         }
     }
-    __device__ __forceinline__ uint32_t code(float v) const {
-        const float t = bad ? 0.f : (v * up) * inv;
-        return (uint32_t)(int)__builtin_rintf(t) & 0xffu;
+    // Codes of four values, in bytes.
+    __device__ __forceinline__ uint32_t codes(float a, float b, float c, float d) const {
+        if (up != 1.0f) {
+            a *= up;
+            b *= up;
+            c *= up;
+            d *= up;
+        }
+        return pack_bytes(nearest_bits(a * inv), nearest_bits(b * inv), nearest_bits(c * inv), nearest_bits(d * inv));
     }
 };
 
@@ -128,10 +145,10 @@ typedef int v2i_any __attribute__((ext_vector_type(2), aligned(1)));
 struct Raw4 { uint32_t w[4]; };
 
 // As they lie in memory, of `count` that exist (the others 0).
-__device__ __forceinline__ Raw4 load_raw4(const void* base, int64_t at, int type, int count) {
+__device__ __forceinline__ Raw4 load_raw4(const void* at, int type, int count) {
     Raw4 r = {};
     if (type == QG_FP32) {
-        const float* p = reinterpret_cast<const float*>(base) + at;
+        const float* p = reinterpret_cast<const float*>(at);
         if (count >= 4) {
             const v4i_any v = *reinterpret_cast<const v4i_any*>(p);
 #pragma unroll
@@ -143,7 +160,7 @@ __device__ __forceinline__ Raw4 load_raw4(const void* base, int64_t at, int type
         }
         return r;
     }
-    const uint16_t* p = reinterpret_cast<const uint16_t*>(base) + at;
+    const uint16_t* p = reinterpret_cast<const uint16_t*>(at);
     if (count >= 4) {
         const v2i_any v = *reinterpret_cast<const v2i_any*>(p);
         r.w[0] = (uint32_t)v[0];
@@ -167,14 +184,12 @@ __device__ __forceinline__ v4f values4(const Raw4& r, int type) {
     return v;
 }
 
-__device__ __forceinline__ v4f load4(const void* base, int64_t at, int type, int count) {
-    return values4(load_raw4(base, at, type, count), type);
-}
+__device__ __forceinline__ v4f load4(const float* at, int count) { return values4(load_raw4(at, QG_FP32, count), QG_FP32); }
 
 // Rounded once to the type; the first `count` of them.
-__device__ __forceinline__ void store4(void* base, int64_t at, int type, int count, v4f v) {
+__device__ __forceinline__ void store4(void* at, int type, int count, v4f v) {
     if (type == QG_FP32) {
-        float* p = reinterpret_cast<float*>(base) + at;
+        float* p = reinterpret_cast<float*>(at);
         if (count >= 4) {
             v4i_any w;
 #pragma unroll
@@ -193,7 +208,7 @@ __device__ __forceinline__ void store4(void* base, int64_t at, int type, int cou
         if (type == QG_BF16) w[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
         else w[i] = __builtin_bit_cast(uint32_t, (v2h){(_Float16)v[2 * i], (_Float16)v[2 * i + 1]});
     }
-    uint16_t* p = reinterpret_cast<uint16_t*>(base) + at;
+    uint16_t* p = reinterpret_cast<uint16_t*>(at);
     if (count >= 4) {
         v2i_any o = {(int)w[0], (int)w[1]};
         *reinterpret_cast<v2i_any*>(p) = o;
@@ -208,16 +223,39 @@ __device__ __forceinline__ void store4(void* base, int64_t at, int type, int cou
 // The epilogue
 // ---------------------------------------------------------------------------
 
-// Four columns n .. n + 3 of row m, z0 (and z1 of a pair) the scaled products, res the
-// residual as it lies.  With a
-// checkpoint, eight lanes in a row from a multiple of eight hold one block of 32
+// Where four columns of a row go.
+struct Goes {
+    void* out;
+    int8_t* code[2];
+    float* scale[2];   // of the block that starts here
+    bool starts;
+};
+
+__device__ __forceinline__ int size_of(int type) { return type == QG_FP32 ? 4 : 2; }
+
+// From row m and column n of the output.
+template <bool PAIR>
+__device__ __forceinline__ Goes goes_to(const Epilogue& e, int64_t m, int n) {
+    Goes g{};
+    g.out = reinterpret_cast<char*>(e.out) + (m * e.ldo + n) * size_of(e.out_type);
+    g.starts = n % INT8_BLOCK == 0;
+#pragma unroll
+    for (int h = 0; h < (PAIR ? 2 : 1); ++h) {
+        g.code[h] = e.ckpt[h] + (m * e.ld_ckpt + n);
+        g.scale[h] = e.ckpt_scale[h] + (m * e.ld_ckpt_scale + n / INT8_BLOCK);
+    }
+    return g;
+}
+
+// Four columns of a row, `count` of them there (none or less: a row or columns outside): z0
+// (and z1 of a pair) the scaled products, res the residual as it lies.  FULL: all four are.
+// With a checkpoint, eight lanes in a row from a multiple of eight hold one block of 32
 // columns, and all lanes of a wave have to be here, those outside the matrix too.
 // Each step rounds by itself: the checkpoint's codes are defined by these steps.
-template <bool PAIR>
-__device__ __forceinline__ void finish4(const Epilogue& e, int m, int n, v4f z0, v4f z1, v4f bias, const Raw4& res) {
+template <bool PAIR, bool FULL>
+__device__ __forceinline__ void finish4(const Epilogue& e, const Goes& to, int count, v4f z0, v4f z1, v4f bias, const Raw4& res) {
 #pragma clang fp contract(off)
-    const bool live = m < e.M && n < e.N;
-    const int count = live ? e.N - n : 0;
+    if constexpr (FULL) count = 4;
     if (!PAIR && e.bias != nullptr) z0 = z0 + bias;
     if (e.ckpt[0] != nullptr) {
 #pragma unroll
@@ -225,27 +263,22 @@ __device__ __forceinline__ void finish4(const Epilogue& e, int m, int n, v4f z0,
             const v4f z = h == 0 ? z0 : z1;
             uint32_t top = 0u;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = umax(top, i < count ? abs_bits(z[i]) : 0u);
+            for (int i = 0; i < 4; ++i) top = umax(top, FULL || i < count ? abs_bits(z[i]) : 0u);
             top = quad_max(top);
             top = umax(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0x141, 0xF, 0xF, true));   // the other four of eight
             const Int8Form f(top);
-            uint32_t w = 0u;
+            const uint32_t w = f.codes(z[0], z[1], z[2], z[3]);
+            if (count >= 4) {
+                __builtin_memcpy(to.code[h], &w, 4);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w |= f.code(z[i]) << (8 * i);
-            if (live) {
-                int8_t* p = e.ckpt[h] + (int64_t)m * e.ld_ckpt + n;
-                if (count >= 4) {
-                    __builtin_memcpy(p, &w, 4);
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 3; ++i)
-                        if (i < count) p[i] = (int8_t)(w >> (8 * i));
-                }
-                if (n % INT8_BLOCK == 0) e.ckpt_scale[h][(int64_t)m * e.ld_ckpt_scale + n / INT8_BLOCK] = f.scale;
+                for (int i = 0; i < 3; ++i)
+                    if (i < count) to.code[h][i] = (int8_t)(w >> (8 * i));
             }
+            if (to.starts && count > 0) *to.scale[h] = f.scale;
         }
     }
-    if (!live) return;
+    if (count <= 0) return;
     v4f y;
     with_activation(e.activation, [&](auto kind) {
 #pragma unroll
@@ -253,7 +286,7 @@ __device__ __forceinline__ void finish4(const Epilogue& e, int m, int n, v4f z0,
     });
     if constexpr (PAIR) y = y * z1;
     if (!PAIR && e.res != nullptr) y = y + values4(res, e.out_type);
-    store4(e.out, (int64_t)m * e.ldo + n, e.out_type, count, y);
+    store4(to.out, e.out_type, count, y);
 }
 
 }  // namespace qg

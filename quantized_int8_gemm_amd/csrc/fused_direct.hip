@@ -113,8 +113,8 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(2))) void fu
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (i < count) ws[h][i] = p.e.w_scale[h][(int64_t)(n + i) * p.e.ws_stride[h]];
-        if (!PAIR && p.e.bias != nullptr) bias = load4(p.e.bias, n, QG_FP32, count);
-        if (!PAIR && p.e.res != nullptr) res = load_raw4(p.e.res, (int64_t)m * p.e.ldr + n, p.e.out_type, count);
+        if (!PAIR && p.e.bias != nullptr) bias = load4(p.e.bias + n, count);
+        if (!PAIR && p.e.res != nullptr) res = load_raw4((const char*)p.e.res + ((int64_t)m * p.e.ldr + n) * size_of(p.e.out_type), p.e.out_type, count);
     }
 
     int i = 0;
@@ -153,7 +153,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(2))) void fu
 #pragma unroll
         for (int q = 0; q < 4; ++q) z[h][q] = (float)s[q] * as * ws[h][q];
     }
-    finish4<PAIR>(p.e, m, n, z[0], z[1], bias, res);
+    finish4<PAIR, false>(p.e, goes_to<PAIR>(p.e, m, n), m < M ? count : 0, z[0], z[1], bias, res);
 }
 
 template <bool PAIR, int TM, int TN, int NB>

@@ -69,10 +69,11 @@ __device__ __forceinline__ void load_scales(const float* w, int stride, int c, i
     }
 }
 
-// G lanes a row, ITER groups of eight columns a lane.  With BIAS a workgroup walks
-// rows and keeps the sums of p of its columns.  HOLD, up to two groups a lane: the
-// factors stay in registers between the row's maximum and their codes; wider rows
-// keep what they were read from and compute them again.
+// G lanes a row, ITER groups of eight columns a lane; a workgroup walks rows.  HOLD, up to
+// two groups a lane: the factors stay in registers between the row's maximum and their
+// codes, the weights' scales, which every row needs again, lie in LDS, and the next row is on
+// its way meanwhile (4096 x 14336 gated 232 us with none of that, a row a workgroup).  Wider
+// rows are read, and their factors computed, again for the codes.
 template <typename T, int G, int ITER, bool PAIR, bool BIAS>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void grad_rows_kernel(GradRowsArgs a) {
     constexpr int RPW = G < 256 ? 256 / G : 1;
@@ -80,105 +81,159 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void grad_rows_kernel(GradRowsAr
     constexpr bool HOLD = ITER <= 2;
     __shared__ uint32_t red[2][G < 64 ? 1 : G / 64];
     __shared__ float part[BIAS && RPW > 1 ? (RPW - 1) * G * ITER * 8 : 1];
+    // a lane's own scales, four to a place: each lane reads what it wrote
+    __shared__ __attribute__((aligned(16))) float ws[HOLD ? RPW * H * ITER * 2 * G * 4 : 1];
     const int t = threadIdx.x % G, group = threadIdx.x / G;
     const int N = a.N;
+    auto place = [&](int h, int i, int half) { return ws + ((((group * H + h) * ITER + i) * 2 + half) * G + t) * 4; };
+    if constexpr (HOLD) {
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int i = 0; i < ITER; ++i) {
+                float s[8];
+                load_scales(a.w_scale[h], a.ws_stride[h], (i * G + t) * 8, N, s);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) *reinterpret_cast<v4f*>(place(h, i, half)) = v4f{s[4 * half], s[4 * half + 1], s[4 * half + 2], s[4 * half + 3]};
+            }
+    }
     float db[BIAS ? ITER : 1][8];
 #pragma unroll
     for (int i = 0; i < (BIAS ? ITER : 1); ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) db[i][e] = 0.f;
 
-    int turn = 0;
-    for (int64_t row0 = (int64_t)blockIdx.x * RPW; row0 < a.M; row0 += (int64_t)gridDim.x * RPW, turn ^= 1) {
-        const int64_t row = row0 + group;
-        const bool live = row < a.M;                   // whole groups; no barrier where a workgroup has several
-        const int64_t r = live ? row : a.M - 1;
-        Pack8<T> yv[ITER];
-        uint2 cv[H][ITER];
-        float cs[H][ITER];
+    constexpr int WI = HOLD ? ITER : 1;
+    struct Row {
+        Pack8<T> y[WI];
+        uint2 c[H][WI];
+        float s[H][WI];
+    };
+    auto fetch_group = [&](int64_t r, Row& v, int i) {
+        const int c = (i * G + t) * 8, w = HOLD ? i : 0;
+        if (c + 8 <= N) load8<false>(reinterpret_cast<const T*>(a.dy) + r * a.ldy, c, N, v.y[w]);
+        else load8<true>(reinterpret_cast<const T*>(a.dy) + r * a.ldy, c, N, v.y[w]);
 #pragma unroll
-        for (int i = 0; i < ITER; ++i) {
-            const int c = (i * G + t) * 8;
-            if (c + 8 <= N) load8<false>(reinterpret_cast<const T*>(a.dy) + r * a.ldy, c, N, yv[i]);
-            else load8<true>(reinterpret_cast<const T*>(a.dy) + r * a.ldy, c, N, yv[i]);
+        for (int h = 0; h < H; ++h) {
+            if (a.ckpt[h] == nullptr) continue;
+            v.c[h][w] = load_codes(a.ckpt[h] + r * a.ld_ckpt, c, N);
+            v.s[h][w] = c < N ? a.ckpt_scale[h][r * a.ld_ckpt_scale + c / INT8_BLOCK] : 0.f;
+        }
+    };
+    auto fetch = [&](int64_t r, Row& v) {
+        if constexpr (HOLD) {
 #pragma unroll
-            for (int h = 0; h < H; ++h) {
-                if (a.ckpt[h] == nullptr) continue;
-                cv[h][i] = load_codes(a.ckpt[h] + r * a.ld_ckpt, c, N);
-                cs[h][i] = c < N ? a.ckpt_scale[h][r * a.ld_ckpt_scale + c / INT8_BLOCK] : 0.f;
+            for (int i = 0; i < ITER; ++i) fetch_group(r, v, i);
+        }
+    };
+    // The factors of group i with the weight's scales; dy is 0 past the last column.
+    auto factors = [&](const Row& row, int i, float (*v)[8], bool add) {
+        const int w = HOLD ? i : 0;
+        if (a.ckpt[0] == nullptr) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[0][e] = value(row.y[w], e);
+        } else {
+            with_activation(a.activation, [&](auto kind) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float f, slope;
+                    activate_both<decltype(kind)::value>(code_at(row.c[0][w], e) * row.s[0][w], f, slope);
+                    const float y = value(row.y[w], e);
+                    if constexpr (PAIR) {
+                        v[0][e] = y * (code_at(row.c[1][w], e) * row.s[1][w]) * slope;
+                        v[1][e] = y * f;
+                    } else {
+                        v[0][e] = y * slope;
+                    }
+                }
+            });
+        }
+        if constexpr (BIAS) {
+            if (add) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) db[i][e] += v[0][e];
             }
         }
-        // The factors of group i with the weight's scales; dy is 0 past the last column.
-        auto factors = [&](int i, float (*v)[8], bool first) {
-            if (a.ckpt[0] == nullptr) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) v[0][e] = value(yv[i], e);
-            } else {
-                with_activation(a.activation, [&](auto kind) {
+        for (int h = 0; h < H; ++h) {
+            float s[8];
+            if constexpr (HOLD) {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        float f, slope;
-                        activate_both<decltype(kind)::value>(code_at(cv[0][i], e) * cs[0][i], f, slope);
-                        const float y = value(yv[i], e);
-                        if constexpr (PAIR) {
-                            v[0][e] = y * (code_at(cv[1][i], e) * cs[1][i]) * slope;
-                            v[1][e] = y * f;
-                        } else {
-                            v[0][e] = y * slope;
-                        }
-                    }
-                });
-            }
-            if constexpr (BIAS) {
-                if (first) {
+                for (int half = 0; half < 2; ++half) {
+                    const v4f q = *reinterpret_cast<const v4f*>(place(h, i, half));
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) db[i][e] += live ? v[0][e] : 0.f;
+                    for (int e = 0; e < 4; ++e) s[4 * half + e] = q[e];
                 }
-            }
-#pragma unroll
-            for (int h = 0; h < H; ++h) {
-                float s[8];
+            } else {
                 load_scales(a.w_scale[h], a.ws_stride[h], (i * G + t) * 8, N, s);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) v[h][e] *= s[e];
             }
-        };
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[h][e] *= s[e];
+        }
+    };
+    // red: two in turn, since a wave may be one row ahead of the others' reads
+    auto finish = [&](int64_t row, bool live, Row& v, int turn) {
         float held[HOLD ? ITER : 1][H][8];
         uint32_t top = 0u;
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
-            float (*v)[8] = held[HOLD ? i : 0];
-            factors(i, v, true);
+            float (*f)[8] = held[HOLD ? i : 0];
+            if constexpr (!HOLD) fetch_group(live ? row : a.M - 1, v, i);
+            factors(v, i, f, live);
 #pragma unroll
             for (int h = 0; h < H; ++h)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) top = umax(top, abs_bits(v[h][e]));
+                for (int e = 0; e < 8; ++e) top = umax(top, abs_bits(f[h][e]));
+            if constexpr (!HOLD) __builtin_amdgcn_sched_barrier(0);   // one group at a time
         }
         top = row_max<G>(top, red[turn]);
-        const bool bad = top >= INF_BITS;
+        if (!live) return;
+        // a NaN or an infinity makes inv 0, and its own product a NaN, whose low bits are 0
         const float most = __uint_as_float(top), up = most < 0x1p-90f ? 0x1p60f : 1.0f;   // STEPS / most stays finite
-        const float inv = bad || top == 0u ? 0.f : STEPS / (most * up);
-        if (!live) continue;
-        if (t == 0) a.row_scale[row] = bad ? __uint_as_float(0x7fc00000u) : most / STEPS;
+        const float inv = top >= INF_BITS || top == 0u ? 0.f : STEPS / (most * up);
+        if (t == 0) a.row_scale[row] = top >= INF_BITS ? __uint_as_float(0x7fc00000u) : most / STEPS;
 #pragma unroll
         for (int i = 0; i < ITER; ++i) {
             const int c = (i * G + t) * 8;
             if (c >= a.np) continue;
-            float (*v)[8] = held[HOLD ? i : 0];
-            if constexpr (!HOLD) factors(i, v, false);
+            float (*f)[8] = held[HOLD ? i : 0];
+            if constexpr (!HOLD) {
+                __builtin_amdgcn_sched_barrier(0);
+                fetch_group(row, v, i);
+                factors(v, i, f, false);
+            }
 #pragma unroll
             for (int h = 0; h < H; ++h) {
-                uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+                uint32_t b[8], hi[2], lo[2];
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int code = bad ? 0 : (int)__builtin_rintf((v[h][e] * up) * inv);
-                    hi[e / 4] |= ((uint32_t)((code + 128) >> 8) & 0xffu) << (8 * (e & 3));
-                    lo[e / 4] |= ((uint32_t)code & 0xffu) << (8 * (e & 3));
+                for (int e = 0; e < 8; ++e) b[e] = nearest_bits((f[h][e] * up) * inv);
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    lo[q] = pack_bytes(b[4 * q], b[4 * q + 1], b[4 * q + 2], b[4 * q + 3]);
+                    hi[q] = pack_bytes(b[4 * q] + 128u, b[4 * q + 1] + 128u, b[4 * q + 2] + 128u, b[4 * q + 3] + 128u, 1);
                 }
                 const int64_t at = row * a.ldq + (int64_t)h * a.np + c;
                 *reinterpret_cast<uint2*>(a.hi + at) = make_uint2(hi[0], hi[1]);
                 *reinterpret_cast<uint2*>(a.lo + at) = make_uint2(lo[0], lo[1]);
             }
+        }
+    };
+    const int64_t step = (int64_t)gridDim.x * RPW, M = a.M;
+    int64_t row = (int64_t)blockIdx.x * RPW + group;   // whole groups; no barrier where a workgroup has several
+    if constexpr (HOLD && RPW == 1) {
+        Row now, next;
+        fetch(row, now);
+        for (int turn = 0; row < M; row += step, turn ^= 1) {
+            if (row + step < M) fetch(row + step, next);
+            finish(row, true, now, turn);
+            now = next;
+        }
+    } else {
+        for (int turn = 0; row - group < M; row += step, turn ^= 1) {
+            const bool live = row < M;
+            Row now;
+            fetch(live ? row : M - 1, now);
+            finish(row, live, now, turn);
         }
     }
     if constexpr (BIAS) {
@@ -234,8 +289,8 @@ hipError_t by_width(const GradRowsArgs& a, hipStream_t s) {
 #define QG_ROWS(G, ITER, LIMIT)                                                                                     \
     if (!done && a.N <= LIMIT) {                                                                                    \
         constexpr int RPW = G < 256 ? 256 / G : 1;                                                                  \
-        const int64_t groups = ((int64_t)a.M + RPW - 1) / RPW;                                                      \
-        const unsigned grid = (unsigned)(BIAS ? a.parts : groups < (1 << 20) ? groups : (1 << 20));                 \
+        const int64_t groups = ((int64_t)a.M + RPW - 1) / RPW, most = G >= 1024 ? 256 : G == 512 ? 512 : 1024;      \
+        const unsigned grid = (unsigned)(BIAS ? a.parts : groups < most ? groups : most);                           \
         hipLaunchKernelGGL((grad_rows_kernel<T, G, ITER, PAIR, BIAS>), dim3(grid), dim3(G < 256 ? 256 : G), 0, s, a); \
         done = true;                                                                                                \
     }
@@ -264,8 +319,8 @@ hipError_t by_form(const GradRowsArgs& a, bool pair, hipStream_t s) {
 
 // Workgroups of the row kernel where each leaves partial sums of dbias.
 int grad_rows_parts(int64_t M, int64_t N) {
-    const int64_t rows = N <= 512 ? 4 : 1, groups = (M + rows - 1) / rows;
-    return (int)(groups < 512 ? groups : 512);
+    const int64_t rows = N <= 512 ? 4 : 1, groups = (M + rows - 1) / rows, most = N > 8192 ? 256 : 512;
+    return (int)(groups < most ? groups : most);
 }
 
 hipError_t launch_grad_rows(const GradRowsArgs& a, bool pair, bool bf16, hipStream_t s) {

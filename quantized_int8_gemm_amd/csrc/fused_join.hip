@@ -17,7 +17,7 @@ __global__ __launch_bounds__(NT) void fused_join_kernel(FusedArgs p, int gpr) {
     const int64_t row = t / gpr;
     const int n = (int)(t - row * gpr) * 4;
     const bool live = row < e.M && n < e.N;
-    const int m = live ? (int)row : e.M, count = live ? e.N - n : 0;
+    const int count = live ? e.N - n : 0;
     v4i s[H];
     v4f ws[H], bias = {0.f, 0.f, 0.f, 0.f};
     Raw4 res = {};
@@ -35,15 +35,15 @@ __global__ __launch_bounds__(NT) void fused_join_kernel(FusedArgs p, int gpr) {
 #pragma unroll
                 for (int q = 0; q < 4; ++q) s[h][q] = (int)((uint32_t)s[h][q] + (uint32_t)v[q]);
             }
-        as = e.act_scale[(int64_t)m * e.as_stride];
-        if (FORM == FUSED_ONE && e.res != nullptr) res = load_raw4(e.res, row * e.ldr + n, e.out_type, count);
-        if (FORM == FUSED_ONE && e.bias != nullptr) bias = load4(e.bias, n, QG_FP32, count);
+        as = e.act_scale[row * e.as_stride];
+        if (FORM == FUSED_ONE && e.res != nullptr) res = load_raw4((const char*)e.res + (row * e.ldr + n) * size_of(e.out_type), e.out_type, count);
+        if (FORM == FUSED_ONE && e.bias != nullptr) bias = load4(e.bias + n, count);
     }
     if constexpr (FORM == FUSED_GRAD) {
         v4f v;
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf((float)s[0][i], 256.f, (float)s[1][i]) * as;
-        if (live) store4(e.out, row * e.ldo + n, e.out_type, count, v);
+        if (live) store4((char*)e.out + (row * e.ldo + n) * size_of(e.out_type), e.out_type, count, v);
     } else {
         v4f z[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
@@ -53,7 +53,7 @@ __global__ __launch_bounds__(NT) void fused_join_kernel(FusedArgs p, int gpr) {
                 ws[h][i] = i < count ? e.w_scale[h][(int64_t)(n + i) * e.ws_stride[h]] : 0.f;
                 z[h][i] = (float)s[h][i] * as * ws[h][i];
             }
-        finish4<FORM == FUSED_PAIR>(e, m, n, z[0], z[1], bias, res);
+        finish4<FORM == FUSED_PAIR, false>(e, goes_to<FORM == FUSED_PAIR>(e, row, n), count, z[0], z[1], bias, res);
     }
 }
 

@@ -274,28 +274,36 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
     constexpr int PW = WAVES_M / PASSES, PR = BMR / PASSES, CPT = BNR / 4, ROWS_AT_ONCE = NT / CPT;
     static_assert(CPT >= 16 && NT % CPT == 0 && PR % ROWS_AT_ONCE == 0, "whole rounds of rows");
     const int c4 = tid % CPT, n = n0 + 4 * c4, count = N - n;
+    const bool whole = rows_a == BMR && cols_b == BNR;   // no row or column outside
     v4f ws[H], bias = {0.f, 0.f, 0.f, 0.f};
     if constexpr (!GRAD) {
 #pragma unroll
         for (int h = 0; h < H; ++h)
 #pragma unroll
             for (int i = 0; i < 4; ++i) ws[h][i] = i < count ? p.e.w_scale[h][(int64_t)(n + i) * p.e.ws_stride[h]] : 0.f;
-        if (!PAIR && p.e.bias != nullptr) bias = load4(p.e.bias, n, QG_FP32, count);
+        if (!PAIR && p.e.bias != nullptr) bias = load4(p.e.bias + n, count);
     }
+    // Places of a lane's four columns, from the tile's corner (one address in scalar registers)
+    // by 32 bits, which the host has checked, a row at a time.
+    const int size = size_of(p.e.out_type);
+    const int64_t corner = (int64_t)m0;
+    char* const out0 = reinterpret_cast<char*>(p.e.out) + (corner * p.e.ldo + n0) * size;
+    const char* const res0 = reinterpret_cast<const char*>(p.e.res) + (corner * p.e.ldr + n0) * size;
     // What a row needs beside its sums, U rows ahead: a residual read where it is used would
     // cost a memory latency a row, which nothing covers (8192 x 8192 x 8192, bf16: 547 us).
-    constexpr int TURNS = PR / ROWS_AT_ONCE, U = TURNS < 4 ? TURNS : 4;
+    constexpr int TURNS = PR / ROWS_AT_ONCE, U = BM == 256 ? 2 : TURNS < 4 ? TURNS : 4;   // of 256 x 256, 4 spill
     Raw4 res_next[U];
     float as_next[U];
     auto fetch = [&](int pass, int q0) {
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int m = m0 + pass * PR + (q0 + u) * ROWS_AT_ONCE + tid / CPT;
+            const int rr = pass * PR + (q0 + u) * ROWS_AT_ONCE + tid / CPT;
             res_next[u] = Raw4{};
             as_next[u] = 0.f;
-            if (m >= M || p.partial != nullptr) continue;
-            as_next[u] = p.e.act_scale[(int64_t)m * p.e.as_stride];
-            if (MODE == FUSED_ONE && p.e.res != nullptr) res_next[u] = load_raw4(p.e.res, (int64_t)m * p.e.ldr + n, p.e.out_type, count);
+            if (rr >= rows_a || p.partial != nullptr) continue;
+            as_next[u] = p.e.act_scale[(int64_t)(m0 + rr) * p.e.as_stride];
+            if (MODE == FUSED_ONE && p.e.res != nullptr)
+                res_next[u] = load_raw4(res0 + ((uint32_t)rr * (uint32_t)p.e.ldr + 4 * c4) * size, p.e.out_type, count);
         }
     };
     fetch(0, 0);
@@ -316,46 +324,73 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
                 }
         }
         __syncthreads();
+        // `full`: no lane has anything outside
+        auto turns = [&](auto full) {
+            constexpr bool FULL = decltype(full)::value;
+            const uint32_t r0 = pass * PR + tid / CPT;
+            uint32_t at_out = (r0 * (uint32_t)p.e.ldo + 4 * c4) * size;
+            uint32_t at_code = r0 * (uint32_t)p.e.ld_ckpt + 4 * c4, at_block = (r0 * (uint32_t)p.e.ld_ckpt_scale + c4 / 8) * 4;
 #pragma unroll 1
-        for (int q0 = 0; q0 < TURNS; q0 += U) {
-            Raw4 res[U];
-            float as[U];
+            for (int q0 = 0; q0 < TURNS; q0 += U) {
+                Raw4 res[U];
+                float as[U];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                res[u] = res_next[u];
-                as[u] = as_next[u];
-            }
-            if (q0 + U < TURNS) fetch(pass, q0 + U);
-            else if (pass + 1 < PASSES) fetch(pass + 1, 0);
+                for (int u = 0; u < U; ++u) {
+                    res[u] = res_next[u];
+                    as[u] = as_next[u];
+                }
+                if (q0 + U < TURNS) fetch(pass, q0 + U);
+                else if (pass + 1 < PASSES) fetch(pass + 1, 0);
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int rr = (q0 + u) * ROWS_AT_ONCE + tid / CPT, m = m0 + pass * PR + rr;
-                const int at = rr * BNR + ((c4 ^ (rr & 15)) << 2);
-                const v4i s0 = *reinterpret_cast<const v4i*>(stage + at);
-                if (p.partial != nullptr) {
-                    if (m < M && count > 0) {
-                        int* to = p.partial + ((int64_t)blockIdx.y * H * M + m) * p.ld_partial + n;
-                        *reinterpret_cast<v4i*>(to) = s0;
-                        if constexpr (H == 2) *reinterpret_cast<v4i*>(to + (int64_t)M * p.ld_partial) = *reinterpret_cast<const v4i*>(stage + PR * BNR + at);
-                    }
-                } else if constexpr (GRAD) {
-                    const v4i s1 = *reinterpret_cast<const v4i*>(stage + PR * BNR + at);
-                    v4f v;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf((float)s0[i], 256.f, (float)s1[i]) * as[u];
-                    if (m < M && count > 0) store4(p.e.out, (int64_t)m * p.e.ldo + n, p.e.out_type, count, v);
-                } else {
-                    v4f z0, z1 = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) z0[i] = (float)s0[i] * as[u] * ws[0][i];
-                    if constexpr (PAIR) {
+                for (int u = 0; u < U; ++u) {
+                    const int rr = (q0 + u) * ROWS_AT_ONCE + tid / CPT;
+                    const int live = FULL ? 4 : pass * PR + rr < rows_a ? count : 0;
+                    const int at = rr * BNR + ((c4 ^ (rr & 15)) << 2);
+                    const v4i s0 = *reinterpret_cast<const v4i*>(stage + at);
+                    if constexpr (GRAD) {
                         const v4i s1 = *reinterpret_cast<const v4i*>(stage + PR * BNR + at);
+                        v4f v;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) z1[i] = (float)s1[i] * as[u] * ws[1][i];
+                        for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf((float)s0[i], 256.f, (float)s1[i]) * as[u];
+                        if (live > 0) store4(out0 + at_out, p.e.out_type, live, v);
+                    } else {
+                        v4f z0, z1 = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) z0[i] = (float)s0[i] * as[u] * ws[0][i];
+                        if constexpr (PAIR) {
+                            const v4i s1 = *reinterpret_cast<const v4i*>(stage + PR * BNR + at);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) z1[i] = (float)s1[i] * as[u] * ws[1][i];
+                        }
+                        Goes to{};
+                        to.out = out0 + at_out;
+                        to.starts = c4 % 8 == 0;
+#pragma unroll
+                        for (int h = 0; h < H; ++h) {
+                            to.code[h] = p.e.ckpt[h] + (corner * p.e.ld_ckpt + n0) + at_code;
+                            to.scale[h] = reinterpret_cast<float*>(reinterpret_cast<char*>(p.e.ckpt_scale[h] + (corner * p.e.ld_ckpt_scale + n0 / INT8_BLOCK)) + at_block);
+                        }
+                        finish4<PAIR, FULL>(p.e, to, live, z0, z1, bias, res[u]);
                     }
-                    finish4<PAIR>(p.e, m, n, z0, z1, bias, res[u]);
+                    at_out += (uint32_t)(ROWS_AT_ONCE * p.e.ldo) * size;
+                    at_code += (uint32_t)(ROWS_AT_ONCE * p.e.ld_ckpt);
+                    at_block += (uint32_t)(ROWS_AT_ONCE * p.e.ld_ckpt_scale) * 4;
                 }
             }
+        };
+        if (p.partial != nullptr) {
+            for (int q = 0; q < TURNS; ++q) {
+                const int rr = q * ROWS_AT_ONCE + tid / CPT, m = pass * PR + rr;
+                const int at = rr * BNR + ((c4 ^ (rr & 15)) << 2);
+                if (m >= rows_a || count <= 0) continue;
+                int* to = p.partial + ((int64_t)blockIdx.y * H * M + m0 + m) * p.ld_partial + n;
+                *reinterpret_cast<v4i*>(to) = *reinterpret_cast<const v4i*>(stage + at);
+                if constexpr (H == 2) *reinterpret_cast<v4i*>(to + (int64_t)M * p.ld_partial) = *reinterpret_cast<const v4i*>(stage + PR * BNR + at);
+            }
+        } else if (whole) {
+            turns(std::integral_constant<bool, true>());
+        } else {
+            turns(std::integral_constant<bool, false>());
         }
     }
 }

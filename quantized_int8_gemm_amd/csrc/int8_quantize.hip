@@ -44,7 +44,8 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void int8_rows_kernel(Int8Args a
         const int c = (i * G + t) * 8;
         Pack8<int8_t> q = {};
 #pragma unroll
-        for (int e = 0; e < 8; ++e) q.w[e / 4] |= f.code(value(v[i], e)) << (8 * (e & 3));
+        for (int h = 0; h < 2; ++h)
+            q.w[h] = f.codes(value(v[i], 4 * h), value(v[i], 4 * h + 1), value(v[i], 4 * h + 2), value(v[i], 4 * h + 3));
         if (c < n) store8(dst, c, n, q);
     }
 }
@@ -64,7 +65,7 @@ __global__ __launch_bounds__(NT) void int8_blocks_kernel(Int8Args a, int64_t gpr
     const Int8Form f(quad_max(top));
     Pack8<int8_t> q = {};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) q.w[e / 4] |= f.code(value(v, e)) << (8 * (e & 3));
+    for (int h = 0; h < 2; ++h) q.w[h] = f.codes(value(v, 4 * h), value(v, 4 * h + 1), value(v, 4 * h + 2), value(v, 4 * h + 3));
     if (!live || c >= n) return;
     store8(a.codes + row * a.ldc, c, n, q);
     if (c % INT8_BLOCK == 0) a.scale[row * a.lds + c / INT8_BLOCK] = f.scale;
