@@ -188,6 +188,31 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
         }
     };
 
+    // The epilogue's own operands, on their way before everything else: the column scales of
+    // this lane's four columns, and a row's scale for the others by LDS (a load between the
+    // epilogue's stores would wait for those before it: 29 us of a 256 x 256 tile were that).
+    // CPT lanes share a row; sums of row rr and columns c .. c + 3 of operand h lie at chunk
+    // (c / 4) ^ (rr & 15) of row h * PR + rr.
+    constexpr int PASSES = BM * BN * 4 <= STAGES * STAGE ? 1 : BM * BN * 2 <= STAGES * STAGE ? 2 : 4;
+    static_assert(WAVES_M % PASSES == 0 && BM * BN * 4 / PASSES <= STAGES * STAGE, "passes of whole wave rows");
+    constexpr int PW = WAVES_M / PASSES, PR = BMR / PASSES, CPT = BNR / 4, ROWS_AT_ONCE = NT / CPT;
+    static_assert(CPT >= 16 && NT % CPT == 0 && PR % ROWS_AT_ONCE == 0 && BMR <= NT, "whole rounds of rows");
+    __shared__ float as_rows[BMR];
+    const int c4 = tid % CPT, n = n0 + 4 * c4, count = N - n;
+    const bool whole = rows_a == BMR && cols_b == BNR;   // no row or column outside
+    float as_mine = 0.f;
+    v4f ws[H], bias = {0.f, 0.f, 0.f, 0.f};
+    if (p.partial == nullptr) {
+        if (tid < rows_a) as_mine = p.e.act_scale[(int64_t)(m0 + tid) * p.e.as_stride];
+        if constexpr (!GRAD) {
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ws[h][i] = i < count ? p.e.w_scale[h][(int64_t)(n + i) * p.e.ws_stride[h]] : 0.f;
+            if (!PAIR && p.e.bias != nullptr) bias = load4(p.e.bias + n, count);
+        }
+    }
+
     v4i acc[FM][FN];
 #pragma unroll
     for (int a = 0; a < FM; ++a)
@@ -267,46 +292,30 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
         }
     }
 
-    // Epilogue.  CPT lanes share a row, each with four columns; sums of row rr and columns
-    // c .. c + 3 of operand h lie at chunk (c / 4) ^ (rr & 15) of row h * PR + rr.
-    constexpr int PASSES = BM * BN * 4 <= STAGES * STAGE ? 1 : BM * BN * 2 <= STAGES * STAGE ? 2 : 4;
-    static_assert(WAVES_M % PASSES == 0, "passes of whole wave rows");
-    constexpr int PW = WAVES_M / PASSES, PR = BMR / PASSES, CPT = BNR / 4, ROWS_AT_ONCE = NT / CPT;
-    static_assert(CPT >= 16 && NT % CPT == 0 && PR % ROWS_AT_ONCE == 0, "whole rounds of rows");
-    const int c4 = tid % CPT, n = n0 + 4 * c4, count = N - n;
-    const bool whole = rows_a == BMR && cols_b == BNR;   // no row or column outside
-    v4f ws[H], bias = {0.f, 0.f, 0.f, 0.f};
-    if constexpr (!GRAD) {
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) ws[h][i] = i < count ? p.e.w_scale[h][(int64_t)(n + i) * p.e.ws_stride[h]] : 0.f;
-        if (!PAIR && p.e.bias != nullptr) bias = load4(p.e.bias + n, count);
-    }
     // Places of a lane's four columns, from the tile's corner (one address in scalar registers)
     // by 32 bits, which the host has checked, a row at a time.
     const int size = size_of(p.e.out_type);
     const int64_t corner = (int64_t)m0;
     char* const out0 = reinterpret_cast<char*>(p.e.out) + (corner * p.e.ldo + n0) * size;
     const char* const res0 = reinterpret_cast<const char*>(p.e.res) + (corner * p.e.ldr + n0) * size;
-    // What a row needs beside its sums, U rows ahead: a residual read where it is used would
-    // cost a memory latency a row, which nothing covers (8192 x 8192 x 8192, bf16: 547 us).
-    constexpr int TURNS = PR / ROWS_AT_ONCE, U = BM == 256 ? 2 : TURNS < 4 ? TURNS : 4;   // of 256 x 256, 4 spill
-    Raw4 res_next[U];
-    float as_next[U];
+    // Residuals, U turns ahead: one read where it is used would cost a memory latency, and
+    // each wait for them is also one for the stores before (8192 x 8192 x 8192, bf16: 547 us so).
+    // Of 256 x 256 tiles more than two spill.
+    constexpr int TURNS = PR / ROWS_AT_ONCE, U = BM == 256 ? 2 : TURNS < 4 ? TURNS : 4;
+    Raw4 next[U];
     auto fetch = [&](int pass, int q0) {
+        if (MODE != FUSED_ONE || p.e.res == nullptr) return;
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int rr = pass * PR + (q0 + u) * ROWS_AT_ONCE + tid / CPT;
-            res_next[u] = Raw4{};
-            as_next[u] = 0.f;
-            if (rr >= rows_a || p.partial != nullptr) continue;
-            as_next[u] = p.e.act_scale[(int64_t)(m0 + rr) * p.e.as_stride];
-            if (MODE == FUSED_ONE && p.e.res != nullptr)
-                res_next[u] = load_raw4(res0 + ((uint32_t)rr * (uint32_t)p.e.ldr + 4 * c4) * size, p.e.out_type, count);
+            next[u] = Raw4{};
+            if (rr < rows_a) next[u] = load_raw4(res0 + ((uint32_t)rr * (uint32_t)p.e.ldr + 4 * c4) * size, p.e.out_type, count);
         }
     };
-    fetch(0, 0);
+    if (p.partial == nullptr) {
+        if (BMR == NT || tid < BMR) as_rows[tid] = as_mine;
+        fetch(0, 0);
+    }
     int* const stage = reinterpret_cast<int*>(smem);
     __syncthreads();   // every wave has read the last chunk
 #pragma unroll
@@ -333,12 +342,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
 #pragma unroll 1
             for (int q0 = 0; q0 < TURNS; q0 += U) {
                 Raw4 res[U];
-                float as[U];
 #pragma unroll
-                for (int u = 0; u < U; ++u) {
-                    res[u] = res_next[u];
-                    as[u] = as_next[u];
-                }
+                for (int u = 0; u < U; ++u) res[u] = next[u];
                 if (q0 + U < TURNS) fetch(pass, q0 + U);
                 else if (pass + 1 < PASSES) fetch(pass + 1, 0);
 #pragma unroll
@@ -347,20 +352,21 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
                     const int live = FULL ? 4 : pass * PR + rr < rows_a ? count : 0;
                     const int at = rr * BNR + ((c4 ^ (rr & 15)) << 2);
                     const v4i s0 = *reinterpret_cast<const v4i*>(stage + at);
+                    const float as = as_rows[pass * PR + rr];
                     if constexpr (GRAD) {
                         const v4i s1 = *reinterpret_cast<const v4i*>(stage + PR * BNR + at);
                         v4f v;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf((float)s0[i], 256.f, (float)s1[i]) * as[u];
+                        for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf((float)s0[i], 256.f, (float)s1[i]) * as;
                         if (live > 0) store4(out0 + at_out, p.e.out_type, live, v);
                     } else {
                         v4f z0, z1 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) z0[i] = (float)s0[i] * as[u] * ws[0][i];
+                        for (int i = 0; i < 4; ++i) z0[i] = (float)s0[i] * as * ws[0][i];
                         if constexpr (PAIR) {
                             const v4i s1 = *reinterpret_cast<const v4i*>(stage + PR * BNR + at);
 #pragma unroll
-                            for (int i = 0; i < 4; ++i) z1[i] = (float)s1[i] * as[u] * ws[1][i];
+                            for (int i = 0; i < 4; ++i) z1[i] = (float)s1[i] * as * ws[1][i];
                         }
                         Goes to{};
                         to.out = out0 + at_out;
