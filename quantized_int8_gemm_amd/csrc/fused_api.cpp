@@ -117,6 +117,12 @@ double time_of(const Shape& s, int tile, int splits, bool pad) {
     return std::max(t, floor * (double)s.K * s.branches) + 0.02 * t;
 }
 
+int64_t tiles_of(const Shape& s, int tile) {
+    const int64_t rows = s.form == qg::FUSED_GRAD ? 2 * s.M : s.M, cols = s.form == qg::FUSED_PAIR ? 2 * s.N : s.N;
+    const int64_t bm = tile == qg::FUSED_256x256 ? 256 : tile == qg::FUSED_128x128 || tile == qg::FUSED_128x128_DEEP ? 128 : 64;
+    return ((rows + bm - 1) / bm) * ((cols + (bm == 256 ? 255 : 127)) / (bm == 256 ? 256 : 128));
+}
+
 // The kind that takes the least time by this reckoning.
 Choice choose(const Shape& s) {
     const int64_t chunks = (s.K + 127) / 128 * s.branches;
@@ -132,6 +138,8 @@ Choice choose(const Shape& s) {
             if (k < qg::FUSED_ANY_64x128 && !s.pieces && with_pad == 0) continue;
             for (const int p : parts) {
                 if (p > 1 && (direct || k == qg::FUSED_256x256 || p > chunks)) break;
+                // K is divided where workgroups would be missing
+                if (p > 1 && forced.parts < 0 && tiles_of(s, k) * p > 384) break;
                 // what is forced goes before what is not
                 const double t = time_of(s, k, p, with_pad == 1) + (forced.kind >= 0 && k != forced.kind ? 1e12 : 0) +
                                  (forced.pad >= 0 && with_pad != forced.pad ? 1e9 : 0) + (forced.parts > 0 && p != forced.parts ? 1e6 : 0);
@@ -385,10 +393,7 @@ qg_status backward(Backward b, const void* dy, qg_dtype dtype, int64_t ld_dy, co
     if (M == 0) {
         if (dbias == nullptr || N == 0) return nothing();
         (void)hipGetLastError();
-        qg::GradRowsArgs a{};
-        a.N = (int)N;
-        a.dbias = dbias;
-        return done(qg::launch_grad_rows(a, false, true, (hipStream_t)stream), "grad_rows");
+        return done(qg::launch_clear(dbias, N, (hipStream_t)stream), "fused_clear");
     }
     if (N == 0 || K == 0 || dy == nullptr || dx == nullptr || ld_dy < N || ld_dx < K) return QG_ERR_INVALID_ARGUMENT;
     if (!aligned_for(dy, dtype) || !aligned_for(dx, dtype)) return QG_ERR_INVALID_ARGUMENT;
@@ -421,8 +426,7 @@ qg_status backward(Backward b, const void* dy, qg_dtype dtype, int64_t ld_dy, co
     a.activation = activation;
     a.hi = (int8_t*)(w + p.hi); a.lo = (int8_t*)(w + p.lo); a.ldq = p.ldq;
     a.row_scale = (float*)(w + p.row_scale);
-    a.part = (float*)(w + p.part); a.parts = p.parts;
-    a.dbias = dbias;
+    a.part = dbias != nullptr ? (float*)(w + p.part) : nullptr; a.parts = p.parts;
     QG_TRY_HIP(qg::launch_grad_rows(a, b.pair == 2, dtype == QG_BF16, s));
 
     qg::FusedArgs f{};
@@ -440,6 +444,7 @@ qg_status backward(Backward b, const void* dy, qg_dtype dtype, int64_t ld_dy, co
         ops[h].p = &f.B[h]; ops[h].ld = &f.ldb[h];
     }
     f.K = (int)N; f.branches = b.pair;
+    f.part = a.part; f.parts = p.parts; f.dbias = dbias; f.bias_n = (int)N;
     return run(qg::FUSED_GRAD, f, p.c, b.b_trans == 0, any, ops, count, w + p.pad, w + p.sums, s);
 }
 

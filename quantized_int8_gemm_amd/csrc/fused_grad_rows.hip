@@ -86,17 +86,6 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void grad_rows_kernel(GradRowsAr
     const int t = threadIdx.x % G, group = threadIdx.x / G;
     const int N = a.N;
     auto place = [&](int h, int i, int half) { return ws + ((((group * H + h) * ITER + i) * 2 + half) * G + t) * 4; };
-    if constexpr (HOLD) {
-#pragma unroll
-        for (int h = 0; h < H; ++h)
-#pragma unroll
-            for (int i = 0; i < ITER; ++i) {
-                float s[8];
-                load_scales(a.w_scale[h], a.ws_stride[h], (i * G + t) * 8, N, s);
-#pragma unroll
-                for (int half = 0; half < 2; ++half) *reinterpret_cast<v4f*>(place(h, i, half)) = v4f{s[4 * half], s[4 * half + 1], s[4 * half + 2], s[4 * half + 3]};
-            }
-    }
     float db[BIAS ? ITER : 1][8];
 #pragma unroll
     for (int i = 0; i < (BIAS ? ITER : 1); ++i)
@@ -220,19 +209,27 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void grad_rows_kernel(GradRowsAr
     };
     const int64_t step = (int64_t)gridDim.x * RPW, M = a.M;
     int64_t row = (int64_t)blockIdx.x * RPW + group;   // whole groups; no barrier where a workgroup has several
-    if constexpr (HOLD && RPW == 1) {
+    if constexpr (HOLD) {
         Row now, next;
-        fetch(row, now);
-        for (int turn = 0; row < M; row += step, turn ^= 1) {
+        fetch(row < M ? row : M - 1, now);
+#pragma unroll
+        for (int h = 0; h < H; ++h)
+#pragma unroll
+            for (int i = 0; i < ITER; ++i) {
+                float s[8];
+                load_scales(a.w_scale[h], a.ws_stride[h], (i * G + t) * 8, N, s);
+#pragma unroll
+                for (int half = 0; half < 2; ++half) *reinterpret_cast<v4f*>(place(h, i, half)) = v4f{s[4 * half], s[4 * half + 1], s[4 * half + 2], s[4 * half + 3]};
+            }
+        for (int turn = 0; row - group < M; row += step, turn ^= 1) {
             if (row + step < M) fetch(row + step, next);
-            finish(row, true, now, turn);
+            finish(row, row < M, now, turn);
             now = next;
         }
     } else {
         for (int turn = 0; row - group < M; row += step, turn ^= 1) {
             const bool live = row < M;
             Row now;
-            fetch(live ? row : M - 1, now);
             finish(row, live, now, turn);
         }
     }
@@ -263,29 +260,14 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void grad_rows_kernel(GradRowsAr
     }
 }
 
-// dbias[n] = sum of the partial rows: 32 columns a workgroup, 32 lanes a column,
-// joined through LDS in a fixed order.
-constexpr int SUM_ROWS = 32;
-__global__ __launch_bounds__(32 * SUM_ROWS) void grad_bias_sum(const float* __restrict__ part, int parts, int n, float* __restrict__ db) {
-    __shared__ float red[SUM_ROWS][33];
-    const int cl = threadIdx.x & 31, q = threadIdx.x >> 5, c = blockIdx.x * 32 + cl;
-    float s = 0.f;
-    if (c < n) {
-#pragma unroll 8
-        for (int p = q; p < parts; p += SUM_ROWS) s += part[(int64_t)p * n + c];
-    }
-    red[q][cl] = s;
-    __syncthreads();
-    if (q == 0 && c < n) {
-#pragma unroll
-        for (int i = 1; i < SUM_ROWS; ++i) s += red[i][cl];
-        db[c] = s;
-    }
+__global__ __launch_bounds__(256) void clear_kernel(float* x, int64_t n) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < n) x[i] = 0.f;
 }
 
 template <typename T, bool PAIR, bool BIAS>
 hipError_t by_width(const GradRowsArgs& a, hipStream_t s) {
-    bool done = a.M == 0;
+    bool done = false;
 #define QG_ROWS(G, ITER, LIMIT)                                                                                     \
     if (!done && a.N <= LIMIT) {                                                                                    \
         constexpr int RPW = G < 256 ? 256 / G : 1;                                                                  \
@@ -303,24 +285,27 @@ hipError_t by_width(const GradRowsArgs& a, hipStream_t s) {
     QG_ROWS(1024, 8, 65536)
 #undef QG_ROWS
     if (!done) return hipErrorInvalidValue;
-    if constexpr (BIAS)
-        hipLaunchKernelGGL(grad_bias_sum, dim3((unsigned)((a.N + 31) / 32)), dim3(32 * SUM_ROWS), 0, s, a.part, a.M == 0 ? 0 : a.parts,
-                           a.N, a.dbias);
     return hipGetLastError();
 }
 
 template <typename T>
 hipError_t by_form(const GradRowsArgs& a, bool pair, hipStream_t s) {
     if (pair) return by_width<T, true, false>(a, s);
-    return a.dbias != nullptr ? by_width<T, false, true>(a, s) : by_width<T, false, false>(a, s);
+    return a.part != nullptr ? by_width<T, false, true>(a, s) : by_width<T, false, false>(a, s);
 }
 
 }  // namespace
 
 // Workgroups of the row kernel where each leaves partial sums of dbias.
 int grad_rows_parts(int64_t M, int64_t N) {
-    const int64_t rows = N <= 512 ? 4 : 1, groups = (M + rows - 1) / rows, most = N > 8192 ? 256 : 512;
+    // (few rows: one a compute unit and its partial sums fewer; 515 x 2816: 5.8 MB of them with 512)
+    const int64_t rows = N <= 512 ? 4 : 1, groups = (M + rows - 1) / rows, most = N > 8192 || M <= 1024 * rows ? 256 : 512;
     return (int)(groups < most ? groups : most);
+}
+
+hipError_t launch_clear(float* x, int64_t n, hipStream_t s) {
+    hipLaunchKernelGGL(clear_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, x, n);
+    return hipGetLastError();
 }
 
 hipError_t launch_grad_rows(const GradRowsArgs& a, bool pair, bool bf16, hipStream_t s) {

@@ -38,6 +38,9 @@ struct FusedArgs {
     // NULL, or where `splits` workgroups a tile, of split_chunks chunks of 128 each, leave
     // their sums: int32 [splits, 1 or 2 (a pair's or a gradient's), e.M, ld_partial]
     int* partial; int splits, split_chunks; int64_t ld_partial;
+    // Of a gradient: NULL, or partial sums [parts, bias_n], that workgroups behind the tiles' add
+    // up to dbias.
+    const float* part; int parts, bias_n; float* dbias;
 };
 // Rows and columns of sums of a tile; DEEP: more than two LDS stages; ANY: operands of any
 // alignment.
@@ -74,8 +77,9 @@ struct GradRowsArgs {
     int8_t* hi; int8_t* lo; int64_t ldq;
     float* row_scale;                         // [M]
     float* part; int parts;                   // NULL, or [parts,N] partial sums of dbias
-    float* dbias;
 };
+// Zeros.
+hipError_t launch_clear(float* x, int64_t n, hipStream_t s);
 int grad_rows_parts(int64_t M, int64_t N);
 hipError_t launch_grad_rows(const GradRowsArgs& a, bool pair, bool bf16, hipStream_t s);
 struct Int8Args {
