@@ -108,12 +108,13 @@ double time_of(const Shape& s, int tile, int splits, bool pad) {
     }
     if (splits > 1) t += 4.5 + rows * cols * 8 * splits / 3e6;
     if (pad) t += 3 + 2 * (double)s.pad_bytes / 4e6;
-    // No faster than the operands come from memory, and the rows that every direct workgroup
-    // reads again from L2 (1 and 16 x 14336 x 4096 gated 27 and 34 us, with 32 columns a workgroup 33
-    // and 35, tiles 31).
+    // No faster than the operands come from memory, and what direct workgroups read again from
+    // L2 (1 and 16 x 14336 x 4096 gated 27 and 34 us, with 32 columns a workgroup 33 and 35, tiles 31;
+    // 30 x 4096 x 4096 gated 10.8 with 32 x 16, 12.6 with 16 x 32).
+    const double tm = direct_rows(tile), tn = direct_cols(tile);
     const double floor = tile < DIRECT ? (rows + cols) / 4.7e6
-                                       : cols / (direct_cols(tile) == 16 ? 4.9e6 : 4.1e6) +
-                                             std::min<double>(direct_rows(tile), s.M) * std::ceil((double)s.N / direct_cols(tile)) / 8.5e6;
+                                       : cols / (tn == 16 ? 4.9e6 : 4.1e6) +
+                                             (s.M * std::ceil(s.N / tn) + cols * (std::ceil(s.M / tm) - 1)) / 8.5e6;
     return std::max(t, floor * (double)s.K * s.branches) + 0.02 * t;
 }
 

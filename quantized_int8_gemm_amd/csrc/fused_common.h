@@ -113,12 +113,14 @@ __device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t 
 // infinity makes inv 0, and its own product with that a NaN, whose low bits are 0.
 struct Int8Form {
     float inv, scale, up = 1.0f;
+    // 2^-100 .. 2^120; outside: zeros, 127 / most not finite or its reciprocal not normal, most not
+    // finite.
+    __device__ __forceinline__ static bool ordinary(uint32_t top) { return top - 0x0d800000u <= 0x7b800000u - 0x0d800000u; }
     __device__ __forceinline__ explicit Int8Form(uint32_t top) {
         const float most = __uint_as_float(top);
         inv = quotient_127(most);
         scale = over_127(most);
-        // rare: zeros, 127 / most not finite or its reciprocal not normal, most not finite
-        if (top - 0x0d800000u > 0x7b800000u - 0x0d800000u) {   // outside 2^-100 .. 2^120
+        if (!ordinary(top)) {
             if (most < 1.0f) up = 0x1p60f;
             inv = top == 0u || top >= INF_BITS ? 0.f : 127.0f / (most * up);
             scale = top >= INF_BITS ? __uint_as_float(0x7fc00000u) : top == 0u ? 1.0f : most / 127.0f;
@@ -247,46 +249,88 @@ __device__ __forceinline__ Goes goes_to(const Epilogue& e, int64_t m, int n) {
     return g;
 }
 
-// Four columns of a row, `count` of them there (none or less: a row or columns outside): z0
-// (and z1 of a pair) the scaled products, res the residual as it lies.  FULL: all four are.
-// With a checkpoint, eight lanes in a row from a multiple of eight hold one block of 32
-// columns, and all lanes of a wave have to be here, those outside the matrix too.
-// Each step rounds by itself: the checkpoint's codes are defined by these steps.
-template <bool PAIR, bool FULL>
-__device__ __forceinline__ void finish4(const Epilogue& e, const Goes& to, int count, v4f z0, v4f z1, v4f bias, const Raw4& res) {
+// U times four columns of a row, `count` of them there (none or less: a row or columns
+// outside): z0 (and z1 of a pair) the scaled products, res the residual as it lies.  FULL: all
+// four are.  Several at once hide each other's latencies (one a time, the epilogue of a
+// 4096 x 8192 x 2048 product with GELU and a checkpoint took 50 of 108 us).  With a checkpoint,
+// eight lanes in a row from a multiple of eight hold one block of 32 columns, and all lanes of
+// a wave have to be here, those outside the matrix too.  Each step rounds by itself: the
+// checkpoint's codes are defined by these steps.
+template <bool PAIR, bool FULL, int U>
+__device__ __forceinline__ void finish(const Epilogue& e, const Goes* to, const int* counts, v4f* z0, const v4f* z1, v4f bias, const Raw4* res) {
 #pragma clang fp contract(off)
-    if constexpr (FULL) count = 4;
-    if (!PAIR && e.bias != nullptr) z0 = z0 + bias;
+    if (!PAIR && e.bias != nullptr) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) z0[u] = z0[u] + bias;
+    }
     if (e.ckpt[0] != nullptr) {
 #pragma unroll
         for (int h = 0; h < (PAIR ? 2 : 1); ++h) {
-            const v4f z = h == 0 ? z0 : z1;
-            uint32_t top = 0u;
+            uint32_t top[U], w[U];
+            float scale[U];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = umax(top, FULL || i < count ? abs_bits(z[i]) : 0u);
-            top = quad_max(top);
-            top = umax(top, (uint32_t)__builtin_amdgcn_mov_dpp((int)top, 0x141, 0xF, 0xF, true));   // the other four of eight
-            const Int8Form f(top);
-            const uint32_t w = f.codes(z[0], z[1], z[2], z[3]);
-            if (count >= 4) {
-                __builtin_memcpy(to.code[h], &w, 4);
+            for (int u = 0; u < U; ++u) {
+                const v4f z = h == 0 ? z0[u] : z1[u];
+                top[u] = 0u;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top[u] = umax(top[u], FULL || i < counts[u] ? abs_bits(z[i]) : 0u);
+                top[u] = quad_max(top[u]);
+                top[u] = umax(top[u], (uint32_t)__builtin_amdgcn_mov_dpp((int)top[u], 0x141, 0xF, 0xF, true));   // the other four of eight
+            }
+            bool plain = true;
+#pragma unroll
+            for (int u = 0; u < U; ++u) plain = plain && Int8Form::ordinary(top[u]);
+            if (__builtin_amdgcn_ballot_w64(!plain) == 0ull) {
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    const v4f z = h == 0 ? z0[u] : z1[u];
+                    const float inv = quotient_127(__uint_as_float(top[u]));
+                    scale[u] = over_127(__uint_as_float(top[u]));
+                    w[u] = pack_bytes(nearest_bits(z[0] * inv), nearest_bits(z[1] * inv), nearest_bits(z[2] * inv), nearest_bits(z[3] * inv));
+                }
             } else {
 #pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    if (i < count) to.code[h][i] = (int8_t)(w >> (8 * i));
+                for (int u = 0; u < U; ++u) {
+                    const v4f z = h == 0 ? z0[u] : z1[u];
+                    const Int8Form f(top[u]);
+                    scale[u] = f.scale;
+                    w[u] = f.codes(z[0], z[1], z[2], z[3]);
+                }
             }
-            if (to.starts && count > 0) *to.scale[h] = f.scale;
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (FULL || counts[u] >= 4) {
+                    __builtin_memcpy(to[u].code[h], &w[u], 4);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 3; ++i)
+                        if (i < counts[u]) to[u].code[h][i] = (int8_t)(w[u] >> (8 * i));
+                }
+            }
+            if (to[0].starts) {
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (FULL || counts[u] > 0) *to[u].scale[h] = scale[u];
+            }
         }
     }
-    if (count <= 0) return;
-    v4f y;
+    v4f y[U];
     with_activation(e.activation, [&](auto kind) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = activate<decltype(kind)::value>(z0[i]);
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) y[u][i] = activate<decltype(kind)::value>(z0[u][i]);
     });
-    if constexpr (PAIR) y = y * z1;
-    if (!PAIR && e.res != nullptr) y = y + values4(res, e.out_type);
-    store4(to.out, e.out_type, count, y);
+    if constexpr (PAIR) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) y[u] = y[u] * z1[u];
+    } else if (e.res != nullptr) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) y[u] = y[u] + values4(res[u], e.out_type);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (FULL || counts[u] > 0) store4(to[u].out, e.out_type, FULL ? 4 : counts[u], y[u]);
 }
 
 }  // namespace qg

@@ -153,7 +153,9 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(2))) void fu
 #pragma unroll
         for (int q = 0; q < 4; ++q) z[h][q] = (float)s[q] * as * ws[h][q];
     }
-    finish4<PAIR, false>(p.e, goes_to<PAIR>(p.e, m, n), m < M ? count : 0, z[0], z[1], bias, res);
+    const Goes to = goes_to<PAIR>(p.e, m, n);
+    const int there = m < M ? count : 0;
+    finish<PAIR, false, 1>(p.e, &to, &there, &z[0], &z[1], bias, &res);
 }
 
 template <bool PAIR, int TM, int TN, int NB>

@@ -53,7 +53,8 @@ __global__ __launch_bounds__(NT) void fused_join_kernel(FusedArgs p, int gpr) {
                 ws[h][i] = i < count ? e.w_scale[h][(int64_t)(n + i) * e.ws_stride[h]] : 0.f;
                 z[h][i] = (float)s[h][i] * as * ws[h][i];
             }
-        finish4<FORM == FUSED_PAIR, false>(e, goes_to<FORM == FUSED_PAIR>(e, row, n), count, z[0], z[1], bias, res);
+        const Goes to = goes_to<FORM == FUSED_PAIR>(e, row, n);
+        finish<FORM == FUSED_PAIR, false, 1>(e, &to, &count, &z[0], &z[1], bias, &res);
     }
 }
 

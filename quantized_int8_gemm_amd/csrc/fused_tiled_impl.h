@@ -69,8 +69,9 @@ __device__ __forceinline__ void sum_bias(const FusedArgs& p, int block, float* r
     }
 }
 
+// 128 x 128 tiles on two stages, two workgroups to a CU: four waves a SIMD asked for.
 template <int MODE, int BM, int BN, int WM, int WN, bool B_KMAJOR, int RING>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel(FusedArgs p) {
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, (BM == 128 && RING == 2 ? 4 : 2)) void fused_tiled_kernel(FusedArgs p) {
     constexpr bool PAIR = MODE == FUSED_PAIR, GRAD = MODE == FUSED_GRAD;
     constexpr int H = MODE == FUSED_ONE ? 1 : 2;
     constexpr int BMR = GRAD ? BM / 2 : BM, BNR = PAIR ? BN / 2 : BN;   // rows and columns of the output
@@ -326,8 +327,8 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
     const char* const res0 = reinterpret_cast<const char*>(p.e.res) + (corner * p.e.ldr + n0) * size;
     // Residuals, U turns ahead: one read where it is used would cost a memory latency, and
     // each wait for them is also one for the stores before (8192 x 8192 x 8192, bf16: 547 us so).
-    // Of 256 x 256 tiles more than two spill.
-    constexpr int TURNS = PR / ROWS_AT_ONCE, U = BM == 256 ? 2 : TURNS < 4 ? TURNS : 4;
+    // Where registers are few, two.
+    constexpr int TURNS = PR / ROWS_AT_ONCE, U = BM == 256 || RING == 2 ? 2 : TURNS < 4 ? TURNS : 4;
     Raw4 next[U];
     auto fetch = [&](int pass, int q0) {
         if (MODE != FUSED_ONE || p.e.res == nullptr) return;
@@ -372,41 +373,44 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void fused_tiled_kernel
                 for (int u = 0; u < U; ++u) res[u] = next[u];
                 if (q0 + U < TURNS) fetch(pass, q0 + U);
                 else if (pass + 1 < PASSES) fetch(pass + 1, 0);
+                v4f z0[U], z1[U];
+                Goes to[U];
+                int live[U];
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     const int rr = (q0 + u) * ROWS_AT_ONCE + tid / CPT;
-                    const int live = FULL ? 4 : pass * PR + rr < rows_a ? count : 0;
+                    live[u] = FULL ? 4 : pass * PR + rr < rows_a ? count : 0;
                     const int at = rr * BNR + ((c4 ^ (rr & 15)) << 2);
                     const v4i s0 = *reinterpret_cast<const v4i*>(stage + at);
+                    v4i s1 = {0, 0, 0, 0};
+                    if constexpr (H == 2) s1 = *reinterpret_cast<const v4i*>(stage + PR * BNR + at);
                     const float as = as_rows[pass * PR + rr];
-                    if constexpr (GRAD) {
-                        const v4i s1 = *reinterpret_cast<const v4i*>(stage + PR * BNR + at);
-                        v4f v;
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf((float)s0[i], 256.f, (float)s1[i]) * as;
-                        if (live > 0) store4(out0 + at_out, p.e.out_type, live, v);
-                    } else {
-                        v4f z0, z1 = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) z0[i] = (float)s0[i] * as * ws[0][i];
-                        if constexpr (PAIR) {
-                            const v4i s1 = *reinterpret_cast<const v4i*>(stage + PR * BNR + at);
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) z1[i] = (float)s1[i] * as * ws[1][i];
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (GRAD) {
+                            z0[u][i] = __builtin_fmaf((float)s0[i], 256.f, (float)s1[i]) * as;
+                        } else {
+                            z0[u][i] = (float)s0[i] * as * ws[0][i];
+                            if constexpr (PAIR) z1[u][i] = (float)s1[i] * as * ws[1][i];
                         }
-                        Goes to{};
-                        to.out = out0 + at_out;
-                        to.starts = c4 % 8 == 0;
+                    }
+                    to[u].out = out0 + at_out;
+                    to[u].starts = c4 % 8 == 0;
 #pragma unroll
-                        for (int h = 0; h < H; ++h) {
-                            to.code[h] = p.e.ckpt[h] + (corner * p.e.ld_ckpt + n0) + at_code;
-                            to.scale[h] = reinterpret_cast<float*>(reinterpret_cast<char*>(p.e.ckpt_scale[h] + (corner * p.e.ld_ckpt_scale + n0 / INT8_BLOCK)) + at_block);
-                        }
-                        finish4<PAIR, FULL>(p.e, to, live, z0, z1, bias, res[u]);
+                    for (int h = 0; h < (GRAD ? 0 : H); ++h) {
+                        to[u].code[h] = p.e.ckpt[h] + (corner * p.e.ld_ckpt + n0) + at_code;
+                        to[u].scale[h] = reinterpret_cast<float*>(reinterpret_cast<char*>(p.e.ckpt_scale[h] + (corner * p.e.ld_ckpt_scale + n0 / INT8_BLOCK)) + at_block);
                     }
                     at_out += (uint32_t)(ROWS_AT_ONCE * p.e.ldo) * size;
                     at_code += (uint32_t)(ROWS_AT_ONCE * p.e.ld_ckpt);
                     at_block += (uint32_t)(ROWS_AT_ONCE * p.e.ld_ckpt_scale) * 4;
+                }
+                if constexpr (GRAD) {
+#pragma unroll
+                    for (int u = 0; u < U; ++u)
+                        if (live[u] > 0) store4(to[u].out, p.e.out_type, live[u], z0[u]);
+                } else {
+                    finish<PAIR, FULL, U>(p.e, to, live, z0, z1, bias, res);
                 }
             }
         };
