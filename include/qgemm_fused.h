@@ -58,8 +58,9 @@ typedef enum {
  *   checkpoint: NULL, or int8 [M,N] that receives z in int8 form by blocks of 32,
  *     checkpoint_scale [M, (N + 31) / 32] its scales.
  * QG_ERR_UNSUPPORTED, here and in the calls below, if operands pass the spans that
- * qgemm_a8w8 takes, or a leading dimension of an output, residual or checkpoint is 2^22 or
- * more.
+ * qgemm_a8w8 takes, a leading dimension of an output, residual or checkpoint is 2^22 or
+ * more, or there are about 2^23 tiles of 64 x 128 sums (2 N columns of a pair, 2 M rows of a
+ * gradient).
  */
 size_t qgemm_a8w8_linear_workspace_bytes(int64_t M, int64_t N, int64_t K,
                                          const int8_t* A, int64_t lda,
@@ -117,7 +118,7 @@ qg_status qgemm_a8w8_gated(int64_t M, int64_t N, int64_t K,
  * form p's and q's together, are held in 16-bit fixed point for each row: with
  * a = the largest magnitude among the row's, t = rint(value * 32639 / a).  Sums over n
  * are exact; an error of a factor is at most a / 65278 (and four roundings in
- * fp32 on the way).  A row that holds a NaN or an infinity among its factors gives
+ * fp32 on the way; more where a is below 2^-110, whose scale is no normal number).  A row that holds a NaN or an infinity among its factors gives
  * a dx row of NaN.
  *   dy: QG_BF16 or QG_FP16 [M,N]; dx: [M,K] of that type.
  *   checkpoint, checkpoint_scale: as the forward call left them.  For the linear

@@ -135,10 +135,12 @@ Choice choose(const Shape& s) {
         if (with_pad == 1 && (s.pieces || s.pad_bytes < 0)) continue;
         for (int k = 0; k < KINDS; ++k) {
             const bool direct = k >= DIRECT;
-            if (direct && (!s.kmajor || s.form == qg::FUSED_GRAD || (s.blocks && direct_cols(k) == 16))) continue;
+            if (direct && (!s.kmajor || s.form == qg::FUSED_GRAD || (s.blocks && direct_cols(k) == 16) ||
+                           ((s.M + 15) / direct_rows(k) + 1) * ((s.N + 15) / direct_cols(k) + 1) >= (int64_t)1 << 23))
+                continue;   // the last: threads of a launch
             if (k < qg::FUSED_ANY_64x128 && !s.pieces && with_pad == 0) continue;
             for (const int p : parts) {
-                if (p > 1 && (direct || k == qg::FUSED_256x256 || p > chunks)) break;
+                if (p > 1 && (direct || k == qg::FUSED_256x256 || p > chunks || s.M * ((s.N + 31) / 32) >= (int64_t)1 << 28)) break;
                 // K is divided where workgroups would be missing
                 if (p > 1 && forced.parts < 0 && tiles_of(s, k) * p > 384) break;
                 // what is forced goes before what is not
@@ -223,8 +225,8 @@ qg_status run(int form, qg::FusedArgs& a, const Choice& c, bool kmajor, bool any
     return done(hipSuccess, kernel_name(form, c));
 }
 
-// A launch holds fewer than 2^32 threads: of the smallest tile's 256.
-bool too_many_tiles(int64_t rows, int64_t cols) { return ((rows + 63) / 64) * ((cols + 127) / 128) >= (int64_t)1 << 24; }
+// A launch holds fewer than 2^32 threads: 512 to a tile of 64 x 128, and to 32 columns of a bias.
+bool too_many_tiles(int64_t rows, int64_t cols) { return ((rows + 63) / 64) * ((cols + 127) / 128) >= ((int64_t)1 << 23) - 2048; }
 
 struct Scales { const float* p; int64_t len; };
 
@@ -252,7 +254,8 @@ struct Forward {
     Choice choice(bool blocks) {
         const size_t pad = pad_bytes();
         return choose({pair == 2 ? qg::FUSED_PAIR : qg::FUSED_ONE, M, N, K, 1, b_trans != 0, pad == 0, blocks,
-                       span_ok(K, up16(lda), std::max(up16(ldw[0]), up16(ldw[pair - 1])), b_trans) ? (int64_t)pad : -1});
+                       span_ok(K, up16(lda), std::max(up16(ldw[0]), up16(ldw[pair - 1])), b_trans) && M * (up16(K) / 16) < (int64_t)1 << 32
+                           ? (int64_t)pad : -1});
     }
 };
 

@@ -45,12 +45,14 @@ BOTH = [
     (dict(type=I8), INV), (dict(type=QG_MXFP8), INV), (dict(out=ODD), INV), (dict(act=-1), INV), (dict(act=5), INV),
     (dict(ck=FAKE, ldc=40), INV), (dict(cs=FAKE, lds=2), INV), (dict(ck=FAKE, ldc=39, cs=FAKE, lds=2), INV),
     (dict(ck=FAKE, ldc=40, cs=FAKE, lds=1), INV), (dict(ck=FAKE, ldc=40, cs=ODD, lds=2), INV), (dict(ws=ODD, wsb=1 << 30), INV),
-    (dict(lda=1 << 23), UNS), (dict(ldw=1 << 23), UNS), (dict(trans=1, ldw=1 << 23), UNS),
+    (dict(lda=1 << 23), UNS), (dict(ldw=1 << 23), UNS), (dict(trans=1, ldw=1 << 23), UNS), (dict(ldo=1 << 22), UNS),
+    (dict(ck=FAKE, ldc=1 << 22, cs=FAKE, lds=2), UNS), (dict(ck=FAKE, ldc=40, cs=FAKE, lds=1 << 22), UNS),
+    (dict(M=(1 << 30) - 1, nsa=1), UNS),
 ]
 
 
 @pytest.mark.parametrize("kw,code", BOTH + [
-    (dict(bias=ODD), INV), (dict(res=FAKE, ldr=39), INV), (dict(res=ODD, ldr=40), INV)])
+    (dict(bias=ODD), INV), (dict(res=FAKE, ldr=39), INV), (dict(res=FAKE, ldr=1 << 22), UNS), (dict(res=ODD, ldr=40), INV)])
 def test_linear_rejects(kw, code):
     assert call("qgemm_a8w8_linear", LINEAR, kw) == code
 
@@ -72,7 +74,8 @@ BOTH_GRADS = [
     (dict(nsw=39), INV), (dict(type=F32), INV), (dict(type=I8), INV), (dict(ldy=39), INV), (dict(ldx=47), INV), (dict(ldw=39), INV),
     (dict(trans=1, ldw=47), INV), (dict(trans=-1), INV), (dict(dy=ODD), INV), (dict(dx=ODD), INV), (dict(act=5), INV),
     (dict(ck=None), INV), (dict(cs=None), INV), (dict(ldc=39), INV), (dict(lds=1), INV), (dict(cs=ODD), INV),
-    (dict(ck=None, cs=None), INV), (dict(ws=ODD), INV), (dict(ws=None), WS), (dict(wsb=0), WS), (dict(ldw=1 << 23), UNS),
+    (dict(ck=None, cs=None), INV), (dict(ws=ODD), INV), (dict(ws=None), WS), (dict(wsb=0), WS), (dict(ldw=1 << 23), UNS), (dict(ldx=1 << 22), UNS),
+    (dict(M=1 << 29), UNS),
 ]
 
 
