@@ -57,6 +57,7 @@ SOURCES = [
     "fused_tiled_pair.hip",
     "fused_tiled_grad.hip",
     "fused_direct.hip",
+    "fused_direct_kn.hip",
     "fused_pad.hip",
     "fused_join.hip",
     "fused_grad_rows.hip",

@@ -54,11 +54,11 @@ struct Forced {
 // Rows of whole 16-byte pieces.
 bool whole_pieces(const void* p, int64_t ld, int64_t n) { return aligned(p, 16) && ld % 16 == 0 && n % 16 == 0; }
 
-// How a product runs.  tile: a FusedTile, or DIRECT + 0 .. 5 for workgroups of 16, 32 or 64
-// rows by 16 or 32 columns.
-constexpr int DIRECT = qg::FUSED_TILES, KINDS = DIRECT + 6;
-int direct_rows(int tile) { return 16 << (tile - DIRECT) / 2; }
-int direct_cols(int tile) { return (tile - DIRECT) % 2 == 0 ? 16 : 32; }
+// How a product runs.  tile: a FusedTile; DIRECT + 0 .. 5 for workgroups of 16, 32 or 64 rows by
+// 16 or 32 columns; DIRECT_KN + 0, 1 for 16 or 32 rows by 64 columns of sums.
+constexpr int DIRECT = qg::FUSED_TILES, DIRECT_KN = DIRECT + 6, KINDS = DIRECT_KN + 2;
+int direct_rows(int tile) { return 16 << (tile >= DIRECT_KN ? tile - DIRECT_KN : (tile - DIRECT) / 2); }
+int direct_cols(int tile) { return tile >= DIRECT_KN ? 64 : (tile - DIRECT) % 2 == 0 ? 16 : 32; }
 
 struct Choice {
     int tile, splits, split_chunks;
@@ -101,9 +101,13 @@ double time_of(const Shape& s, int tile, int splits, bool pad) {
         case qg::FUSED_64x128_DEEP: t = std::ceil(tiles(64, 128) / 256) * (per * 0.36 + 1.5); break;
         case qg::FUSED_ANY_64x128: t = std::max(1.6, std::ceil(tiles(64, 128) / 256) * 1.04) * per + 2; break;
         default: {
-            const double tm = direct_rows(tile), tn = direct_cols(tile), n = std::ceil(s.M / tm) * std::ceil(s.N / tn) / 256;
-            const double bytes = (std::min<double>(tm, s.M) + tn * (s.form == qg::FUSED_PAIR ? 2 : 1)) * (double)s.K;
-            t = 1.3 + std::max(1.0, n) * bytes / (s.pieces || pad ? 37e3 : 16e3) + 0.35 * n;
+            // rows of A and of the weights that a workgroup reads, and how many there are
+            const double tm = direct_rows(tile), tn = direct_cols(tile);
+            const double a_rows = std::min<double>(tm, s.M) * (s.form == qg::FUSED_GRAD ? 2 : 1);
+            const bool kn = tile >= DIRECT_KN, pair = s.form == qg::FUSED_PAIR;
+            const double w_rows = pair && !kn ? 2 * tn : tn, out_cols = pair && kn ? tn / 2 : tn;
+            const double n = std::ceil(s.M / tm) * std::ceil(s.N / out_cols) / 256;
+            t = 1.3 + std::max(1.0, n) * (a_rows + w_rows) * (double)s.K * s.branches / (s.pieces || pad ? 37e3 : 16e3) + 0.35 * n;
         }
     }
     if (splits > 1) t += 4.5 + rows * cols * 8 * splits / 3e6;
@@ -114,7 +118,7 @@ double time_of(const Shape& s, int tile, int splits, bool pad) {
     const double tm = direct_rows(tile), tn = direct_cols(tile);
     const double floor = tile < DIRECT ? (rows + cols) / 4.7e6
                                        : cols / (tn == 16 ? 4.9e6 : 4.1e6) +
-                                             (s.M * std::ceil(s.N / tn) + cols * (std::ceil(s.M / tm) - 1)) / 8.5e6;
+                                             (rows * std::ceil(s.N / tn) + cols * (std::ceil(s.M / tm) - 1)) / 8.5e6;
     return std::max(t, floor * (double)s.K * s.branches) + 0.02 * t;
 }
 
@@ -135,9 +139,10 @@ Choice choose(const Shape& s) {
         if (with_pad == 1 && (s.pieces || s.pad_bytes < 0)) continue;
         for (int k = 0; k < KINDS; ++k) {
             const bool direct = k >= DIRECT;
-            if (direct && (!s.kmajor || s.form == qg::FUSED_GRAD || (s.blocks && direct_cols(k) == 16) ||
-                           ((s.M + 15) / direct_rows(k) + 1) * ((s.N + 15) / direct_cols(k) + 1) >= (int64_t)1 << 23))
+            if (direct && ((k < DIRECT_KN) != s.kmajor || (s.blocks && direct_cols(k) == 16) ||
+                           ((s.M + 15) / direct_rows(k) + 1) * ((s.N + 15) / 16 + 1) >= (int64_t)1 << 23))
                 continue;   // the last: threads of a launch
+            if (k >= DIRECT_KN && !s.pieces && with_pad == 0) continue;
             if (k < qg::FUSED_ANY_64x128 && !s.pieces && with_pad == 0) continue;
             for (const int p : parts) {
                 if (p > 1 && (direct || k == qg::FUSED_256x256 || p > chunks || s.M * ((s.N + 31) / 32) >= (int64_t)1 << 28)) break;
@@ -163,7 +168,8 @@ Choice choose(const Shape& s) {
 }
 
 hipError_t launch_fused(int form, const qg::FusedArgs& a, int tile, bool kmajor, bool any, hipStream_t s) {
-    if (tile >= DIRECT) return qg::launch_fused_direct(a, form == qg::FUSED_PAIR, direct_rows(tile), direct_cols(tile), any, s);
+    if (tile >= DIRECT_KN) return qg::launch_fused_direct_kn(a, form, direct_rows(tile), s);
+    if (tile >= DIRECT) return qg::launch_fused_direct(a, form, direct_rows(tile), direct_cols(tile), any, s);
     const qg::FusedTile t = (qg::FusedTile)tile;
     return form == qg::FUSED_ONE ? qg::launch_fused_one(a, t, kmajor, s)
            : form == qg::FUSED_PAIR ? qg::launch_fused_pair(a, t, kmajor, s) : qg::launch_fused_grad(a, t, kmajor, s);
@@ -171,14 +177,18 @@ hipError_t launch_fused(int form, const qg::FusedArgs& a, int tile, bool kmajor,
 
 const char* kernel_name(int form, const Choice& c) {
     static const char* const names[3][KINDS] = {
-        {"fused_one_256x256", "fused_one_128x128", "fused_one_128x128_deep", "fused_one_64x128_deep", "fused_one_any_64x128",
-         "fused_one_direct_16x16", "fused_one_direct_16x32", "fused_one_direct_32x16", "fused_one_direct_32x32",
-         "fused_one_direct_64x16", "fused_one_direct_64x32"},
-        {"fused_pair_256x256", "fused_pair_128x128", "fused_pair_128x128_deep", "fused_pair_64x128_deep", "fused_pair_any_64x128",
-         "fused_pair_direct_16x16", "fused_pair_direct_16x32", "fused_pair_direct_32x16", "fused_pair_direct_32x32",
-         "fused_pair_direct_64x16", "fused_pair_direct_64x32"},
-        {"fused_grad_256x256", "fused_grad_128x128", "fused_grad_128x128_deep", "fused_grad_64x128_deep", "fused_grad_any_64x128",
-         "", "", "", "", "", ""}};
+        {"fused_one_256x256", "fused_one_128x128", "fused_one_128x128_deep", "fused_one_64x128_deep",
+         "fused_one_any_64x128", "fused_one_direct_16x16", "fused_one_direct_16x32", "fused_one_direct_32x16",
+         "fused_one_direct_32x32", "fused_one_direct_64x16", "fused_one_direct_64x32", "fused_one_direct_kn_16",
+         "fused_one_direct_kn_32"},
+        {"fused_pair_256x256", "fused_pair_128x128", "fused_pair_128x128_deep", "fused_pair_64x128_deep",
+         "fused_pair_any_64x128", "fused_pair_direct_16x16", "fused_pair_direct_16x32",
+         "fused_pair_direct_32x16", "fused_pair_direct_32x32", "fused_pair_direct_64x16",
+         "fused_pair_direct_64x32", "fused_pair_direct_kn_16", "fused_pair_direct_kn_32"},
+        {"fused_grad_256x256", "fused_grad_128x128", "fused_grad_128x128_deep", "fused_grad_64x128_deep",
+         "fused_grad_any_64x128", "fused_grad_direct_16x16", "fused_grad_direct_16x32",
+         "fused_grad_direct_32x16", "fused_grad_direct_32x32", "fused_grad_direct_64x16",
+         "fused_grad_direct_64x32", "fused_grad_direct_kn_16", "fused_grad_direct_kn_32"}};
     static const char* const joined[3] = {"fused_one_joined", "fused_pair_joined", "fused_grad_joined"};
     return c.splits > 1 ? joined[form] : names[form][c.tile];
 }

@@ -333,4 +333,25 @@ __device__ __forceinline__ void finish(const Epilogue& e, const Goes* to, const 
         if (FULL || counts[u] > 0) store4(to[u].out, e.out_type, FULL ? 4 : counts[u], y[u]);
 }
 
+// The same from the int32 sums of row m, columns n .. n + 3, for kernels whose lanes have one item
+// each; sums of a gradient's planes hi and lo give its value.
+template <int FORM>
+__device__ __forceinline__ void finish_sums(const Epilogue& e, int m, int n, int count, const v4i* s, float as, const v4f* ws, v4f bias,
+                                            const Raw4& res) {
+    constexpr bool PAIR = FORM == FUSED_PAIR;
+    const Goes to = goes_to<PAIR>(e, m, n);
+    v4f z[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    if constexpr (FORM == FUSED_GRAD) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) z[0][i] = __builtin_fmaf((float)s[0][i], 256.f, (float)s[1][i]) * as;
+        if (count > 0) store4(to.out, e.out_type, count, z[0]);
+    } else {
+#pragma unroll
+        for (int h = 0; h < (PAIR ? 2 : 1); ++h)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) z[h][i] = (float)s[h][i] * as * ws[h][i];
+        finish<PAIR, false, 1>(e, &to, &count, &z[0], &z[1], bias, &res);
+    }
+}
+
 }  // namespace qg

@@ -11,64 +11,82 @@
 // ANY: rows that are not whole 16-byte pieces, read at any alignment.
 #include "fused_common.h"
 #include "fused_load.h"
+#include "fused_stage.h"
 
 namespace qg {
 namespace {
 
+using fused::NOWHERE;
 constexpr int WAVES = 8, NT = 64 * WAVES, STEP = 128, KB = STEP / 64;
-constexpr uint32_t NOWHERE = 0x80000000u;   // past every buffer's end
 
-template <bool PAIR, int TM, int TN, int NB, bool ANY>
+// GRAD: A is the two planes of the factors, B the branches' weights one behind the other.
+template <int FORM, int TM, int TN, int NB, bool ANY>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(2))) void fused_direct_kernel(FusedArgs p) {
-    constexpr int H = PAIR ? 2 : 1, FM = TM / 16, FN = TN / 16;
+    constexpr bool PAIR = FORM == FUSED_PAIR, GRAD = FORM == FUSED_GRAD;
+    constexpr int H = FORM == FUSED_ONE ? 1 : 2, AH = GRAD ? 2 : 1, BH = PAIR ? 2 : 1, FM = TM / 16, FN = TN / 16;
     __shared__ __attribute__((aligned(16))) int red[WAVES][H][TM][TN];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, i16 = lane & 15;
     const int M = p.e.M, N = p.e.N, K = p.k_bytes;
     const int tiles_m = (M + TM - 1) / TM;
-    const int tile = xcd_remap(blockIdx.x, gridDim.x);   // an XCD's workgroups share weights
+    const int tiles = tiles_m * ((N + TN - 1) / TN);
+    if (GRAD && (int)blockIdx.x >= tiles) {
+        fused::sum_bias<NT>(p, (int)blockIdx.x - tiles, reinterpret_cast<float*>(red));
+        return;
+    }
+    const int tile = xcd_remap(blockIdx.x, tiles);   // an XCD's workgroups share weights
     const int m0 = tile % tiles_m * TM, n0 = tile / tiles_m * TN;
     const int rows = M - m0 < TM ? M - m0 : TM, cols = N - n0 < TN ? N - n0 : TN;
     const int lda = (int)p.lda;
-    const int8_t* const A = p.A[0] + (int64_t)m0 * p.lda;
-    const __amdgpu_buffer_rsrc_t a_rsrc = make_rsrc(A, (uint32_t)((rows - 1) * lda + K));
+    const int nkb = (p.K + STEP - 1) / STEP, steps = GRAD ? nkb * p.branches : nkb;
+    const int a_row = GRAD ? steps * STEP : K;   // bytes of A's rows
+    auto a_base = [&](int h) { return p.A[h] + (int64_t)m0 * p.lda; };
+    const __amdgpu_buffer_rsrc_t a_rsrc = make_rsrc(a_base(0), (uint32_t)((rows - 1) * lda + a_row));
+    const __amdgpu_buffer_rsrc_t a_rsrc2 = GRAD ? make_rsrc(a_base(1), (uint32_t)((rows - 1) * lda + a_row)) : a_rsrc;
     const __amdgpu_buffer_rsrc_t b_rsrc = make_rsrc(p.B[0] + (int64_t)n0 * p.ldb[0], (uint32_t)((cols - 1) * (int)p.ldb[0] + K));
     const __amdgpu_buffer_rsrc_t b_rsrc2 =
-        PAIR ? make_rsrc(p.B[1] + (int64_t)n0 * p.ldb[1], (uint32_t)((cols - 1) * (int)p.ldb[1] + K)) : b_rsrc;
+        PAIR || (GRAD && p.branches == 2) ? make_rsrc(p.B[1] + (int64_t)n0 * p.ldb[1], (uint32_t)((cols - 1) * (int)p.ldb[1] + K)) : b_rsrc;
 
-    const int steps = (K + STEP - 1) / STEP, mine = (steps + WAVES - 1) / WAVES, first = wave * mine;
-    u32x4 av[NB][KB][FM], bv[NB][KB][H][FN];
+    const int mine = (steps + WAVES - 1) / WAVES, first = wave * mine;
+    u32x4 av[NB][KB][AH][FM], bv[NB][KB][BH][FN];
     auto fetch = [&](int i, int b) {
         const int step = first + i;
         const bool live = i < mine && step < steps;
+        const int branch = GRAD && step >= nkb ? 1 : 0;
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
-            const int k = step * STEP + 64 * kb + 16 * g;
+            const int k = step * STEP + 64 * kb + 16 * g, kw = k - branch * nkb * STEP;   // of A's row and the weight's
             if constexpr (ANY) {
-                const int limit = live ? K : 0;
 #pragma unroll
-                for (int a = 0; a < FM; ++a) {
-                    const int r = 16 * a + i16;
-                    av[b][kb][a] = load16_any(A + (int64_t)(r < rows ? r : 0) * p.lda, k, r < rows ? limit : 0);
-                }
+                for (int h = 0; h < AH; ++h)
 #pragma unroll
-                for (int h = 0; h < H; ++h)
+                    for (int a = 0; a < FM; ++a) {
+                        const int r = 16 * a + i16;
+                        av[b][kb][h][a] = load16_any(a_base(h) + (int64_t)(r < rows ? r : 0) * p.lda, k, live && r < rows ? a_row : 0);
+                    }
+#pragma unroll
+                for (int h = 0; h < BH; ++h)
 #pragma unroll
                     for (int c = 0; c < FN; ++c) {
-                        const int r = 16 * c + i16;
-                        bv[b][kb][h][c] = load16_any(p.B[h] + (int64_t)(n0 + (r < cols ? r : 0)) * p.ldb[h], k, r < cols ? limit : 0);
+                        const int r = 16 * c + i16, w = PAIR ? h : branch;
+                        bv[b][kb][h][c] = load16_any(p.B[w] + (int64_t)(n0 + (r < cols ? r : 0)) * p.ldb[w], kw, live && r < cols ? K : 0);
                     }
             } else {
                 // a piece of A past K gives zeros, and B's there then adds nothing
-                const bool in = live && k < K;
+                const bool in = live && k < a_row;
 #pragma unroll
-                for (int h = 0; h < H; ++h)
+                for (int h = 0; h < BH; ++h)
 #pragma unroll
-                    for (int c = 0; c < FN; ++c)
-                        bv[b][kb][h][c] = buffer_load16(h == 0 ? b_rsrc : b_rsrc2, in ? (uint32_t)((16 * c + i16) * (int)p.ldb[h] + k) : NOWHERE, 0u);
+                    for (int c = 0; c < FN; ++c) {
+                        const bool second = PAIR ? h == 1 : branch == 1;
+                        bv[b][kb][h][c] = buffer_load16(second ? b_rsrc2 : b_rsrc,
+                                                        in ? (uint32_t)((16 * c + i16) * (int)p.ldb[second ? 1 : 0] + kw) : NOWHERE, 0u);
+                    }
 #pragma unroll
-                for (int a = 0; a < FM; ++a)
-                    av[b][kb][a] = buffer_load16(a_rsrc, in ? (uint32_t)((16 * a + i16) * lda + k) : NOWHERE, 0u);
+                for (int h = 0; h < AH; ++h)
+#pragma unroll
+                    for (int a = 0; a < FM; ++a)
+                        av[b][kb][h][a] = buffer_load16(h == 0 ? a_rsrc : a_rsrc2, in ? (uint32_t)((16 * a + i16) * lda + k) : NOWHERE, 0u);
             }
         }
     };
@@ -87,7 +105,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(2))) void fu
 #pragma unroll
                 for (int c = 0; c < FN; ++c)
 #pragma unroll
-                    for (int a = 0; a < FM; ++a) acc[h][a][c] = mfma_i8_16x16x64(bv[b][kb][h][c], av[b][kb][a], acc[h][a][c]);
+                    for (int a = 0; a < FM; ++a) acc[h][a][c] = mfma_i8_16x16x64(bv[b][kb][PAIR ? h : 0][c], av[b][kb][GRAD ? h : 0][a], acc[h][a][c]);
     };
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -109,12 +127,12 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(2))) void fu
     if (has && m < M) {
         as = p.e.act_scale[(int64_t)m * p.e.as_stride];
 #pragma unroll
-        for (int h = 0; h < H; ++h)
+        for (int h = 0; h < (GRAD ? 0 : H); ++h)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 if (i < count) ws[h][i] = p.e.w_scale[h][(int64_t)(n + i) * p.e.ws_stride[h]];
-        if (!PAIR && p.e.bias != nullptr) bias = load4(p.e.bias + n, count);
-        if (!PAIR && p.e.res != nullptr) res = load_raw4((const char*)p.e.res + ((int64_t)m * p.e.ldr + n) * size_of(p.e.out_type), p.e.out_type, count);
+        if (FORM == FUSED_ONE && p.e.bias != nullptr) bias = load4(p.e.bias + n, count);
+        if (FORM == FUSED_ONE && p.e.res != nullptr) res = load_raw4((const char*)p.e.res + ((int64_t)m * p.e.ldr + n) * size_of(p.e.out_type), p.e.out_type, count);
     }
 
     int i = 0;
@@ -140,49 +158,45 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(2))) void fu
     __syncthreads();
     static_assert(ITEMS <= NT && ITEMS % 64 == 0, "an item a lane");
     if (!has) return;
-    v4f z[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    v4i s[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
-        v4i s = {0, 0, 0, 0};
+    for (int h = 0; h < H; ++h)
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) {
             const v4i v = *reinterpret_cast<const v4i*>(&red[w][h][row][4 * c4]);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) s[q] = (int)((uint32_t)s[q] + (uint32_t)v[q]);
+            for (int q = 0; q < 4; ++q) s[h][q] = (int)((uint32_t)s[h][q] + (uint32_t)v[q]);
         }
-#pragma unroll
-        for (int q = 0; q < 4; ++q) z[h][q] = (float)s[q] * as * ws[h][q];
-    }
-    const Goes to = goes_to<PAIR>(p.e, m, n);
-    const int there = m < M ? count : 0;
-    finish<PAIR, false, 1>(p.e, &to, &there, &z[0], &z[1], bias, &res);
+    finish_sums<FORM>(p.e, m, n, m < M ? count : 0, s, as, ws, bias, res);
 }
 
-template <bool PAIR, int TM, int TN, int NB>
+template <int FORM, int TM, int TN, int NB>
 hipError_t launch_tile(const FusedArgs& a, bool any, hipStream_t s) {
     const int64_t tiles = (int64_t)((a.e.M + TM - 1) / TM) * ((a.e.N + TN - 1) / TN);
-    if (tiles * NT >= (int64_t)1 << 32) return hipErrorInvalidValue;
-    if (any) hipLaunchKernelGGL((fused_direct_kernel<PAIR, TM, TN, 2, true>), dim3((unsigned)tiles), dim3(NT), 0, s, a);
-    else hipLaunchKernelGGL((fused_direct_kernel<PAIR, TM, TN, NB, false>), dim3((unsigned)tiles), dim3(NT), 0, s, a);
+    const int64_t grid = tiles + (FORM == FUSED_GRAD && a.dbias != nullptr ? (a.bias_n + 31) / 32 : 0);
+    if (grid * NT >= (int64_t)1 << 32) return hipErrorInvalidValue;
+    if (any) hipLaunchKernelGGL((fused_direct_kernel<FORM, TM, TN, 2, true>), dim3((unsigned)grid), dim3(NT), 0, s, a);
+    else hipLaunchKernelGGL((fused_direct_kernel<FORM, TM, TN, NB, false>), dim3((unsigned)grid), dim3(NT), 0, s, a);
     return hipGetLastError();
 }
 
-template <bool PAIR>
+template <int FORM>
 hipError_t launch(const FusedArgs& a, int tm, int tn, bool any, hipStream_t s) {
     if (tn == 16) {
-        if (tm == 16) return launch_tile<PAIR, 16, 16, 4>(a, any, s);
-        if (tm == 32) return launch_tile<PAIR, 32, 16, 4>(a, any, s);
-        return launch_tile<PAIR, 64, 16, 2>(a, any, s);
+        if (tm == 16) return launch_tile<FORM, 16, 16, 4>(a, any, s);
+        if (tm == 32) return launch_tile<FORM, 32, 16, 4>(a, any, s);
+        return launch_tile<FORM, 64, 16, 2>(a, any, s);
     }
-    if (tm == 16) return launch_tile<PAIR, 16, 32, 4>(a, any, s);
-    if (tm == 32) return launch_tile<PAIR, 32, 32, 2>(a, any, s);
-    return launch_tile<PAIR, 64, 32, 2>(a, any, s);
+    if (tm == 16) return launch_tile<FORM, 16, 32, 4>(a, any, s);
+    if (tm == 32) return launch_tile<FORM, 32, 32, 2>(a, any, s);
+    return launch_tile<FORM, 64, 32, 2>(a, any, s);
 }
 
 }  // namespace
 
-hipError_t launch_fused_direct(const FusedArgs& a, bool pair, int tm, int tn, bool any, hipStream_t s) {
-    return pair ? launch<true>(a, tm, tn, any, s) : launch<false>(a, tm, tn, any, s);
+hipError_t launch_fused_direct(const FusedArgs& a, int form, int tm, int tn, bool any, hipStream_t s) {
+    return form == FUSED_ONE ? launch<FUSED_ONE>(a, tm, tn, any, s)
+           : form == FUSED_PAIR ? launch<FUSED_PAIR>(a, tm, tn, any, s) : launch<FUSED_GRAD>(a, tm, tn, any, s);
 }
 
 }  // namespace qg

@@ -39,23 +39,13 @@ __global__ __launch_bounds__(NT) void fused_join_kernel(FusedArgs p, int gpr) {
         if (FORM == FUSED_ONE && e.res != nullptr) res = load_raw4((const char*)e.res + (row * e.ldr + n) * size_of(e.out_type), e.out_type, count);
         if (FORM == FUSED_ONE && e.bias != nullptr) bias = load4(e.bias + n, count);
     }
-    if constexpr (FORM == FUSED_GRAD) {
-        v4f v;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf((float)s[0][i], 256.f, (float)s[1][i]) * as;
-        if (live) store4((char*)e.out + (row * e.ldo + n) * size_of(e.out_type), e.out_type, count, v);
-    } else {
-        v4f z[2] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+    if constexpr (FORM != FUSED_GRAD) {
 #pragma unroll
         for (int h = 0; h < H; ++h)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                ws[h][i] = i < count ? e.w_scale[h][(int64_t)(n + i) * e.ws_stride[h]] : 0.f;
-                z[h][i] = (float)s[h][i] * as * ws[h][i];
-            }
-        const Goes to = goes_to<FORM == FUSED_PAIR>(e, row, n);
-        finish<FORM == FUSED_PAIR, false, 1>(e, &to, &count, &z[0], &z[1], bias, &res);
+            for (int i = 0; i < 4; ++i) ws[h][i] = i < count ? e.w_scale[h][(int64_t)(n + i) * e.ws_stride[h]] : 0.f;
     }
+    finish_sums<FORM>(e, (int)row, n, count, s, as, ws, bias, res);
 }
 
 }  // namespace

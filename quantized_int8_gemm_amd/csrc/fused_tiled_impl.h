@@ -30,6 +30,7 @@
 #include "fused_common.h"
 #include "fused_kernels.h"
 #include "fused_load.h"
+#include "fused_stage.h"
 #include "int8_dma_impl.h"
 
 namespace qg {
@@ -38,36 +39,6 @@ namespace fused {
 constexpr int BK = 128;          // bytes of K per chunk
 constexpr int KB = BK / 64;      // matrix instructions along it
 constexpr int GROUP_M = 8;
-constexpr uint32_t NOWHERE = 0x80000000u;   // past every buffer's end
-
-// Slot of segment s of k-row r of a [K,N] tile whose rows are RB bytes.  For RB = 64: the
-// 16 rows that a transposed read touches (8 of two groups 16 rows apart) lie four to
-// 256 bytes, and bits 2 and 4 of r tell those that would share a slot apart.
-template <int RB>
-__device__ __forceinline__ int kn_slot_of(int r, int s) {
-    if constexpr (RB == 64) return s ^ (((r >> 2) & 1) | ((r >> 3) & 2));
-    else return dma::kn_slot<RB>(r, s);
-}
-
-// dbias[n] = sum of the partial rows, for 32 columns a workgroup: NT / 32 lanes a column, joined
-// in a fixed order.  Behind the tiles in one launch: on their own they took 3 us more.
-template <int NT>
-__device__ __forceinline__ void sum_bias(const FusedArgs& p, int block, float* red) {
-    constexpr int ROWS = NT / 32;
-    const int cl = threadIdx.x & 31, q = threadIdx.x >> 5, c = block * 32 + cl;
-    float s = 0.f;
-    if (c < p.bias_n) {
-#pragma unroll 8
-        for (int i = q; i < p.parts; i += ROWS) s += p.part[(int64_t)i * p.bias_n + c];
-    }
-    red[q * 33 + cl] = s;
-    __syncthreads();
-    if (q == 0 && c < p.bias_n) {
-#pragma unroll
-        for (int i = 1; i < ROWS; ++i) s += red[i * 33 + cl];
-        p.dbias[c] = s;
-    }
-}
 
 // 128 x 128 tiles on two stages, two workgroups to a CU: four waves a SIMD asked for.
 template <int MODE, int BM, int BN, int WM, int WN, bool B_KMAJOR, int RING>

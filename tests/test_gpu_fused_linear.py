@@ -188,12 +188,14 @@ def test_outputs_without_elements():
 
 
 TILES = ("256x256", "128x128", "128x128_deep", "64x128_deep", "any_64x128", "direct_16x16", "direct_16x32", "direct_32x16",
-         "direct_32x32", "direct_64x16", "direct_64x32")
+         "direct_32x32", "direct_64x16", "direct_64x32", "direct_kn_16", "direct_kn_32")
 
 
 def taken(tile, b_trans, checkpoint):
     """Whether a forced kind takes the call: the direct ones want [N,K], and 32 columns for a
-    checkpoint's blocks."""
+    checkpoint's blocks, or [K,N]."""
+    if "kn" in TILES[tile]:
+        return not b_trans
     return not TILES[tile].startswith("direct") or (b_trans and not (checkpoint and TILES[tile].endswith("x16")))
 
 
