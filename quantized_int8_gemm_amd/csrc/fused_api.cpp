@@ -78,12 +78,15 @@ struct Shape {
 
 // Microseconds that a kind takes, about, fitted to measured calls (those in parentheses).  A
 // chunk of 128 of K costs a tile what its CU needs with the workgroups that run there at
-// once: 1.75 for 256 x 256 (4000 x 4096 x 4096 71 us, 8192^3 446), 0.75 and 1.1 for one and two of
+// once: 1.7 for 256 x 256 (4000 x 4096 x 4096 71 us, 8192^3 446), 0.75 and 1.1 for one and two of
 // 128 x 128 on two stages (1000 and 2000 x 4096 x 4096 29 and 40), 0.58 on four (24, 48; 1000 x
-// 4096 x 14336 70, two stages 111), 0.36 for 64 x 128 on six (300 x 4096 x 14336 51, 90 x 1008 x 1008
+// 4096 x 14336 70, two stages 111), 0.4 for 64 x 128 on six (300 x 4096 x 14336 51, 90 x 1008 x 1008
 // 7.9), 0.52 through registers (1000 x 4095 x 4095 71).  A direct workgroup takes its operands at
-// 35 bytes a nanosecond (64 x 4096 x 4096 gated 15 us, 64 x 4096 x 14336 34; 300 x 1008 x 1008 6.6), 16
-// unaligned ones (4 x 4095 x 4095 gated 20).
+// 37 bytes a nanosecond (64 x 4096 x 4096 gated 15 us, 64 x 4096 x 14336 34; 300 x 1008 x 1008 6.6), 35
+// transposed ones (202 x 1904 x 3024 12), 16 unaligned ones (4 x 4095 x 4095 gated 20), and faster
+// where few run (30 workgroups, 151 x 96 x 4576 gated, [K,N], 8); a 257th takes as long as a second
+// round (55 x 2064 x 384 gated, [K,N], 260 of 16 x 32 8.0, 130 of 32 x 32 5.6); what it adds up through LDS
+// bounds short sums (1024 x 2816 x 64 gated 30 with 64 x 32, 33 with 32 x 32, tiles of 64 x 128 12).
 double time_of(const Shape& s, int tile, int splits, bool pad) {
     const double chunks = (double)((s.K + 127) / 128 * s.branches);
     const double rows = (double)s.M * (s.form == qg::FUSED_GRAD ? 2 : 1), cols = (double)s.N * (s.form == qg::FUSED_PAIR ? 2 : 1);
@@ -91,26 +94,29 @@ double time_of(const Shape& s, int tile, int splits, bool pad) {
     auto tiles = [&](double bm, double bn) { return std::ceil(rows / bm) * std::ceil(cols / bn) * splits; };
     double t;
     switch (tile) {
-        case qg::FUSED_256x256: t = std::ceil(tiles(256, 256) / 256) * (per * 1.75 + 6); break;
+        case qg::FUSED_256x256: t = std::ceil(tiles(256, 256) / 256) * (per * 1.7 + 10); break;
         case qg::FUSED_128x128: {
             const double n = tiles(128, 128), full = std::floor(n / 512), rest = n - 512 * full;
             t = full * (per * 1.1 + 4) + (rest > 256 ? per * 1.1 + 4 : rest > 0 ? per * 0.75 + 3 : 0);
             break;
         }
-        case qg::FUSED_128x128_DEEP: t = std::ceil(tiles(128, 128) / 256) * (per * 0.58 + 2.5); break;
-        case qg::FUSED_64x128_DEEP: t = std::ceil(tiles(64, 128) / 256) * (per * 0.36 + 1.5); break;
-        case qg::FUSED_ANY_64x128: t = std::max(1.6, std::ceil(tiles(64, 128) / 256) * 1.04) * per + 2; break;
+        case qg::FUSED_128x128_DEEP: t = std::ceil(tiles(128, 128) / 256) * (per * 0.58 + 3.2); break;
+        case qg::FUSED_64x128_DEEP: t = std::ceil(tiles(64, 128) / 256) * (per * 0.4 + 2.2); break;
+        case qg::FUSED_ANY_64x128: { const double n = std::ceil(tiles(64, 128) / 256); t = std::max(1.6, n * 1.04) * per + 1 + 1.2 * n; break; }
         default: {
             // rows of A and of the weights that a workgroup reads, and how many there are
             const double tm = direct_rows(tile), tn = direct_cols(tile);
             const double a_rows = std::min<double>(tm, s.M) * (s.form == qg::FUSED_GRAD ? 2 : 1);
             const bool kn = tile >= DIRECT_KN, pair = s.form == qg::FUSED_PAIR;
             const double w_rows = pair && !kn ? 2 * tn : tn, out_cols = pair && kn ? tn / 2 : tn;
-            const double n = std::ceil(s.M / tm) * std::ceil(s.N / out_cols) / 256;
-            t = 1.3 + std::max(1.0, n) * (a_rows + w_rows) * (double)s.K * s.branches / (s.pieces || pad ? 37e3 : 16e3) + 0.35 * n;
+            const double n = std::ceil(s.M / tm) * std::ceil(s.N / out_cols) / 256, alone = std::max(0.0, 1 - n);
+            const double rate = !s.pieces && !pad ? 16e3 : kn ? 35e3 + (s.form == qg::FUSED_GRAD ? 0 : 25e3) * alone : 37e3 + 20e3 * alone;
+            const double each = (a_rows + w_rows) * (double)s.K * s.branches / rate + 0.35;
+            const double sums = tm * out_cols * (s.form == qg::FUSED_ONE ? 1 : 2);
+            t = 1.2 + 4e-4 * sums + each + (std::ceil(n) - 1) * std::max({each, kn ? 2.5 : 1.5, 1.3e-3 * sums});
         }
     }
-    if (splits > 1) t += 4.5 + rows * cols * 8 * splits / 3e6;
+    if (splits > 1) t += 5 + rows * cols * 8 * splits / 3e6;
     if (pad) t += 3 + 2 * (double)s.pad_bytes / 4e6;
     // No faster than the operands come from memory, and what direct workgroups read again from
     // L2 (1 and 16 x 14336 x 4096 gated 27 and 34 us, with 32 columns a workgroup 33 and 35, tiles 31;

@@ -354,4 +354,12 @@ __device__ __forceinline__ void finish_sums(const Epilogue& e, int m, int n, int
     }
 }
 
+// Where columns 4 c4 .. of a row lie in a tile of sums with C columns in LDS: the 16 rows that a
+// fragment's store touches, 64 / C to 256 bytes, take distinct places (64 x 32 gated workgroups
+// lost 5 us where they did not).
+template <int C>
+__device__ __forceinline__ int sums_at(int row, int c4) {
+    return row * C + ((c4 ^ ((row / (64 / C)) & (C / 4 - 1))) << 2);
+}
+
 }  // namespace qg

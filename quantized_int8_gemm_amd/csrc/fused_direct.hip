@@ -24,7 +24,7 @@ template <int FORM, int TM, int TN, int NB, bool ANY>
 __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(2))) void fused_direct_kernel(FusedArgs p) {
     constexpr bool PAIR = FORM == FUSED_PAIR, GRAD = FORM == FUSED_GRAD;
     constexpr int H = FORM == FUSED_ONE ? 1 : 2, AH = GRAD ? 2 : 1, BH = PAIR ? 2 : 1, FM = TM / 16, FN = TN / 16;
-    __shared__ __attribute__((aligned(16))) int red[WAVES][H][TM][TN];
+    __shared__ __attribute__((aligned(16))) int red[WAVES][H][TM * TN];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int g = lane >> 4, i16 = lane & 15;
     const int M = p.e.M, N = p.e.N, K = p.k_bytes;
@@ -154,7 +154,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(2))) void fu
 #pragma unroll
         for (int a = 0; a < FM; ++a)
 #pragma unroll
-            for (int c = 0; c < FN; ++c) *reinterpret_cast<v4i*>(&red[wave][h][16 * a + i16][16 * c + 4 * g]) = acc[h][a][c];
+            for (int c = 0; c < FN; ++c) *reinterpret_cast<v4i*>(&red[wave][h][sums_at<TN>(16 * a + i16, 4 * c + g)]) = acc[h][a][c];
     __syncthreads();
     static_assert(ITEMS <= NT && ITEMS % 64 == 0, "an item a lane");
     if (!has) return;
@@ -163,7 +163,7 @@ __global__ __launch_bounds__(NT) __attribute__((amdgpu_waves_per_eu(2))) void fu
     for (int h = 0; h < H; ++h)
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) {
-            const v4i v = *reinterpret_cast<const v4i*>(&red[w][h][row][4 * c4]);
+            const v4i v = *reinterpret_cast<const v4i*>(&red[w][h][sums_at<TN>(row, c4)]);
 #pragma unroll
             for (int q = 0; q < 4; ++q) s[h][q] = (int)((uint32_t)s[h][q] + (uint32_t)v[q]);
         }

@@ -148,8 +148,8 @@ __global__ __launch_bounds__(NT, 2) void fused_direct_kn_kernel(FusedArgs p) {
 #pragma unroll
         for (int b = 0; b < FB; ++b) {
             const int h = GRAD ? a & 1 : PAIR ? b / (FB / 2) : 0;
-            const int rr = (GRAD ? a >> 1 : a) * 16 + i16, c = (PAIR ? b % (FB / 2) : b) * 16 + 4 * g;
-            *reinterpret_cast<v4i*>(red + ((wave * H + h) * TM + rr) * C + c) = acc[a][b];
+            const int rr = (GRAD ? a >> 1 : a) * 16 + i16, c = (PAIR ? b % (FB / 2) : b) * 4 + g;
+            *reinterpret_cast<v4i*>(red + (wave * H + h) * TM * C + sums_at<C>(rr, c)) = acc[a][b];
         }
     __syncthreads();
     if (!has) return;
@@ -158,7 +158,7 @@ __global__ __launch_bounds__(NT, 2) void fused_direct_kn_kernel(FusedArgs p) {
     for (int h = 0; h < H; ++h)
 #pragma unroll
         for (int w = 0; w < WAVES; ++w) {
-            const v4i v = *reinterpret_cast<const v4i*>(red + ((w * H + h) * TM + row) * C + 4 * c4);
+            const v4i v = *reinterpret_cast<const v4i*>(red + (w * H + h) * TM * C + sums_at<C>(row, c4));
 #pragma unroll
             for (int q = 0; q < 4; ++q) s[h][q] = (int)((uint32_t)s[h][q] + (uint32_t)v[q]);
         }
