@@ -118,8 +118,9 @@ qg_status qgemm_a8w8_gated(int64_t M, int64_t N, int64_t K,
  * form p's and q's together, are held in 16-bit fixed point for each row: with
  * a = the largest magnitude among the row's, t = rint(value * 32639 / a).  Sums over n
  * are exact; an error of a factor is at most a / 65278 (and four roundings in
- * fp32 on the way; more where a is below 2^-110, whose scale is no normal number).  A row that holds a NaN or an infinity among its factors gives
- * a dx row of NaN.
+ * fp32 on the way; more where a is below 2^-110, whose scale is no normal
+ * number).  A row that holds a NaN or an infinity among its factors gives a dx
+ * row of NaN.
  *   dy: QG_BF16 or QG_FP16 [M,N]; dx: [M,K] of that type.
  *   checkpoint, checkpoint_scale: as the forward call left them.  For the linear
  *     form with QG_ACT_NONE both may be NULL.

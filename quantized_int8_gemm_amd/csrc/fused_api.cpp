@@ -146,6 +146,7 @@ Choice choose(const Shape& s) {
         for (int k = 0; k < KINDS; ++k) {
             const bool direct = k >= DIRECT;
             if (direct && ((k < DIRECT_KN) != s.kmajor || (s.blocks && direct_cols(k) == 16) ||
+                           (k == DIRECT_KN + 1 && s.form == qg::FUSED_GRAD) ||
                            ((s.M + 15) / direct_rows(k) + 1) * ((s.N + 15) / 16 + 1) >= (int64_t)1 << 23))
                 continue;   // the last: threads of a launch
             if (k >= DIRECT_KN && !s.pieces && with_pad == 0) continue;
@@ -194,7 +195,7 @@ const char* kernel_name(int form, const Choice& c) {
         {"fused_grad_256x256", "fused_grad_128x128", "fused_grad_128x128_deep", "fused_grad_64x128_deep",
          "fused_grad_any_64x128", "fused_grad_direct_16x16", "fused_grad_direct_16x32",
          "fused_grad_direct_32x16", "fused_grad_direct_32x32", "fused_grad_direct_64x16",
-         "fused_grad_direct_64x32", "fused_grad_direct_kn_16", "fused_grad_direct_kn_32"}};
+         "fused_grad_direct_64x32", "fused_grad_direct_kn_16", ""}};
     static const char* const joined[3] = {"fused_one_joined", "fused_pair_joined", "fused_grad_joined"};
     return c.splits > 1 ? joined[form] : names[form][c.tile];
 }

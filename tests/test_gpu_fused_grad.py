@@ -218,7 +218,8 @@ def test_every_kernel_gives_the_same_bits(tile, b_trans):
                 got = run()
             assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
             for name, branches in ((got[2], 2), (got[3], 1)):
-                if tile > 4 and ("kn" in TILES[tile]) != b_trans:   # the gradient reads the weight the other way
+                # the gradient reads the weight the other way, and 32 rows of [N,K] are no kind of its
+                if tile > 4 and ("kn" in TILES[tile]) != b_trans or TILES[tile] == "direct_kn_32":
                     continue
                 joined = splits > 1 and 0 < tile < 5
                 assert (joined and -(-n // 128) * branches < splits) or name == "fused_grad_" + ("joined" if joined else TILES[tile])
