@@ -81,12 +81,13 @@ struct Shape {
 // once: 1.7 for 256 x 256 (4000 x 4096 x 4096 71 us, 8192^3 446), 0.75 and 1.1 for one and two of
 // 128 x 128 on two stages (1000 and 2000 x 4096 x 4096 29 and 40), 0.58 on four (24, 48; 1000 x
 // 4096 x 14336 70, two stages 111), 0.4 for 64 x 128 on six (300 x 4096 x 14336 51, 90 x 1008 x 1008
-// 7.9), 0.52 through registers (1000 x 4095 x 4095 71).  A direct workgroup takes its operands at
-// 37 bytes a nanosecond (64 x 4096 x 4096 gated 15 us, 64 x 4096 x 14336 34; 300 x 1008 x 1008 6.6), 35
-// transposed ones (202 x 1904 x 3024 12), 16 unaligned ones (4 x 4095 x 4095 gated 20), and faster
-// where few run (30 workgroups, 151 x 96 x 4576 gated, [K,N], 8); a 257th takes as long as a second
-// round (55 x 2064 x 384 gated, [K,N], 260 of 16 x 32 8.0, 130 of 32 x 32 5.6); what it adds up through LDS
-// bounds short sums (1024 x 2816 x 64 gated 30 with 64 x 32, 33 with 32 x 32, tiles of 64 x 128 12).
+// 7.9), 1.04 to 1.5 through registers (1000 x 4095 x 4095 71; 1 x 4095 x 4095 gated 54).  A direct
+// workgroup takes its operands at 37 bytes a nanosecond (64 x 4096 x 4096 gated 15 us, 64 x 4096 x
+// 14336 34; 300 x 1008 x 1008 6.6), 35 transposed ones (202 x 1904 x 3024 12), 16 unaligned ones (4 x 4095
+// x 4095 gated 20; 27 of one [K,N] weight, 30 x 4095 x 4095 16), and faster where few run (30
+// workgroups, 151 x 96 x 4576 gated, [K,N], 8); a 257th takes as long as a second round (55 x 2064 x
+// 384 gated, [K,N], 260 of 16 x 32 8.0, 130 of 32 x 32 5.6); what it adds up through LDS bounds short
+// sums (1024 x 2816 x 64 gated 30 with 64 x 32, 33 with 32 x 32, tiles of 64 x 128 12).
 double time_of(const Shape& s, int tile, int splits, bool pad) {
     const double chunks = (double)((s.K + 127) / 128 * s.branches);
     const double rows = (double)s.M * (s.form == qg::FUSED_GRAD ? 2 : 1), cols = (double)s.N * (s.form == qg::FUSED_PAIR ? 2 : 1);
@@ -102,7 +103,7 @@ double time_of(const Shape& s, int tile, int splits, bool pad) {
         }
         case qg::FUSED_128x128_DEEP: t = std::ceil(tiles(128, 128) / 256) * (per * 0.58 + 3.2); break;
         case qg::FUSED_64x128_DEEP: t = std::ceil(tiles(64, 128) / 256) * (per * 0.4 + 2.2); break;
-        case qg::FUSED_ANY_64x128: { const double n = std::ceil(tiles(64, 128) / 256); t = std::max(1.6, n * 1.04) * per + 1 + 1.2 * n; break; }
+        case qg::FUSED_ANY_64x128: { const double n = std::ceil(tiles(64, 128) / 256); t = std::max(1.25, n * 1.04) * per + 1 + 1.2 * n; break; }
         default: {
             // rows of A and of the weights that a workgroup reads, and how many there are
             const double tm = direct_rows(tile), tn = direct_cols(tile);
@@ -110,7 +111,7 @@ double time_of(const Shape& s, int tile, int splits, bool pad) {
             const bool kn = tile >= DIRECT_KN, pair = s.form == qg::FUSED_PAIR;
             const double w_rows = pair && !kn ? 2 * tn : tn, out_cols = pair && kn ? tn / 2 : tn;
             const double n = std::ceil(s.M / tm) * std::ceil(s.N / out_cols) / 256, alone = std::max(0.0, 1 - n);
-            const double rate = !s.pieces && !pad ? 16e3 : kn ? 35e3 + (s.form == qg::FUSED_GRAD ? 0 : 25e3) * alone : 37e3 + 20e3 * alone;
+            const double rate = !s.pieces && !pad ? (!kn || s.form == qg::FUSED_GRAD ? 16e3 : s.form == qg::FUSED_ONE ? 27e3 : 16e3 + 10e3 * alone) : kn ? 35e3 + (s.form == qg::FUSED_GRAD ? 0 : 25e3) * alone : 37e3 + 20e3 * alone;
             const double each = (a_rows + w_rows) * (double)s.K * s.branches / rate + 0.35;
             const double sums = tm * out_cols * (s.form == qg::FUSED_ONE ? 1 : 2);
             t = 1.2 + 4e-4 * sums + each + (std::ceil(n) - 1) * std::max({each, kn ? 2.5 : 1.5, 1.3e-3 * sums});
@@ -149,7 +150,6 @@ Choice choose(const Shape& s) {
                            (k == DIRECT_KN + 1 && s.form == qg::FUSED_GRAD) ||
                            ((s.M + 15) / direct_rows(k) + 1) * ((s.N + 15) / 16 + 1) >= (int64_t)1 << 23))
                 continue;   // the last: threads of a launch
-            if (k >= DIRECT_KN && !s.pieces && with_pad == 0) continue;
             if (k < qg::FUSED_ANY_64x128 && !s.pieces && with_pad == 0) continue;
             for (const int p : parts) {
                 if (p > 1 && (direct || k == qg::FUSED_256x256 || p > chunks || s.M * ((s.N + 31) / 32) >= (int64_t)1 << 28)) break;
@@ -175,7 +175,7 @@ Choice choose(const Shape& s) {
 }
 
 hipError_t launch_fused(int form, const qg::FusedArgs& a, int tile, bool kmajor, bool any, hipStream_t s) {
-    if (tile >= DIRECT_KN) return qg::launch_fused_direct_kn(a, form, direct_rows(tile), s);
+    if (tile >= DIRECT_KN) return qg::launch_fused_direct_kn(a, form, direct_rows(tile), any, s);
     if (tile >= DIRECT) return qg::launch_fused_direct(a, form, direct_rows(tile), direct_cols(tile), any, s);
     const qg::FusedTile t = (qg::FusedTile)tile;
     return form == qg::FUSED_ONE ? qg::launch_fused_one(a, t, kmajor, s)

@@ -4,8 +4,11 @@
 // meet in LDS.  A [K,N] weight's fragments are not as they lie in memory, so each wave stages
 // 64 rows of K by 64 bytes in LDS of its own, by loads that go there directly, and reads them
 // transposed; A's 64-byte pieces of rows go the same way.  A wave waits for its own loads only,
-// without a barrier.  One launch; a tiled kernel's workgroup walks eight times as much of K.
+// without a barrier.  Rows that are not whole 16-byte pieces (ANY) come through registers, the
+// next step's while one is multiplied: 130 x 1000 x 512 6 us, where laying the weight out again first
+// takes 3 and the product 5.  One launch; a tiled kernel's workgroup walks eight times as much of K.
 #include "fused_common.h"
+#include "fused_load.h"
 #include "fused_stage.h"
 
 namespace qg {
@@ -20,7 +23,7 @@ __device__ __forceinline__ void wait_own_loads() {
     asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
 }
 
-template <int FORM, int TM>
+template <int FORM, int TM, bool ANY>
 __global__ __launch_bounds__(NT, 2) void fused_direct_kn_kernel(FusedArgs p) {
     constexpr bool PAIR = FORM == FUSED_PAIR, GRAD = FORM == FUSED_GRAD;
     constexpr int H = FORM == FUSED_ONE ? 1 : 2;
@@ -28,7 +31,7 @@ __global__ __launch_bounds__(NT, 2) void fused_direct_kn_kernel(FusedArgs p) {
     constexpr int C = PAIR ? COLS / 2 : COLS, RB = C;                // columns of the output; bytes of a weight's staged row
     constexpr int B_LOADS = STEP * COLS / 1024, LOADS = FA + B_LOADS;
     constexpr int STAGE = LOADS * 1024;                              // of a wave
-    constexpr int STAGES = STAGE * WAVES * 3 <= 128 * 1024 ? 3 : 2;
+    constexpr int STAGES = ANY ? 1 : STAGE * WAVES * 3 <= 128 * 1024 ? 3 : 2;
     constexpr int RED = WAVES * H * TM * C * 4, LDS = STAGES * STAGE * WAVES > RED ? STAGES * STAGE * WAVES : RED;
     __shared__ __attribute__((aligned(1024))) uint8_t smem[LDS];
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -50,7 +53,7 @@ __global__ __launch_bounds__(NT, 2) void fused_direct_kn_kernel(FusedArgs p) {
     const v4i a_rsrc = a_words(0), a_rsrc2 = GRAD ? a_words(1) : a_rsrc;
     const v4i b_rsrc = b_words(0), b_rsrc2 = PAIR || (GRAD && p.branches == 2) ? b_words(1) : b_rsrc;
     const uint32_t lds0 = (uint32_t)(uintptr_t)smem + wave * (STAGES * STAGE);
-    const uint8_t* const own = smem + wave * (STAGES * STAGE);
+    uint8_t* const own = smem + wave * (STAGES * STAGE);
 
     // A load moves 16 rows of A by 64 bytes, or 1024 / RB rows of a weight.
     const int ar = lane >> 2, a_col = 16 * dma::kc_slot<STEP>(ar, lane & 3);
@@ -129,18 +132,52 @@ __global__ __launch_bounds__(NT, 2) void fused_direct_kn_kernel(FusedArgs p) {
             res = load_raw4((const char*)p.e.res + ((int64_t)m * p.e.ldr + n) * size_of(p.e.out_type), p.e.out_type, count);
     }
 
+    if constexpr (ANY) {
+        u32x4 ra[FA], rb[B_LOADS];
+        auto fetch = [&](int i) {
+            const int step = first + i;
+            const bool live = i < mine && step < steps, second = GRAD && step >= nkb;
+            const int k = step * STEP, kw = second ? k - nkb * STEP : k;
 #pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) issue(i, i);
-    int at = 0;
-    for (int i = 0; i < mine; ++i) {
-        // the stage that is filled now was read in the last turn, and those reads are done
-        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-        issue(i + STAGES - 1, at == 0 ? STAGES - 1 : at - 1);
-        wait_own_loads<LOADS * (STAGES - 1)>();   // all but the later stages' are there
-        compute(at);
-        at = at + 1 == STAGES ? 0 : at + 1;
+            for (int a = 0; a < FA; ++a) {
+                const int r = (GRAD ? a >> 1 : a) * 16 + ar;
+                const int8_t* base = p.A[GRAD ? a & 1 : 0] + (int64_t)(m0 + (r < rows ? r : 0)) * p.lda;
+                ra[a] = load16_any(base, k + a_col, live && r < rows ? a_row : 0);
+            }
+#pragma unroll
+            for (int q = 0; q < B_LOADS; ++q) {
+                const int half = PAIR ? q / (B_LOADS / 2) : 0, r = (PAIR ? q % (B_LOADS / 2) : q) * (1024 / RB) + br, row = kw + r;
+                const int w = PAIR ? half : second ? 1 : 0;
+                rb[q] = load16_any(p.B[w] + (int64_t)(row < p.K ? row : 0) * p.ldb[w], n0 + 16 * kn_slot_of<RB>(r, lane % (RB / 16)),
+                                   live && row < p.K ? N : 0);
+            }
+        };
+        fetch(0);
+        for (int i = 0; i < mine; ++i) {
+            // a wave's LDS accesses are in order: these follow the last turn's reads
+#pragma unroll
+            for (int a = 0; a < FA; ++a) *reinterpret_cast<u32x4*>(own + a * 1024 + lane * 16) = ra[a];
+#pragma unroll
+            for (int q = 0; q < B_LOADS; ++q) *reinterpret_cast<u32x4*>(own + (FA + q) * 1024 + lane * 16) = rb[q];
+            asm volatile("" ::: "memory");
+            fetch(i + 1);
+            compute(0);
+            asm volatile("" ::: "memory");
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i) issue(i, i);
+        int at = 0;
+        for (int i = 0; i < mine; ++i) {
+            // the stage that is filled now was read in the last turn, and those reads are done
+            asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+            issue(i + STAGES - 1, at == 0 ? STAGES - 1 : at - 1);
+            wait_own_loads<LOADS * (STAGES - 1)>();   // all but the later stages' are there
+            compute(at);
+            at = at + 1 == STAGES ? 0 : at + 1;
+        }
+        wait_own_loads<0>();
     }
-    wait_own_loads<0>();
     __syncthreads();   // every wave is done with its stages
     int* const red = reinterpret_cast<int*>(smem);
 #pragma unroll
@@ -165,29 +202,35 @@ __global__ __launch_bounds__(NT, 2) void fused_direct_kn_kernel(FusedArgs p) {
     finish_sums<FORM>(p.e, m, n, m < M ? count : 0, s, as, ws, bias, res);
 }
 
-template <int FORM, int TM>
+template <int FORM, int TM, bool ANY>
 hipError_t launch_tile(const FusedArgs& a, hipStream_t s) {
     constexpr int C = FORM == FUSED_PAIR ? COLS / 2 : COLS;
     const int64_t tiles = (int64_t)((a.e.M + TM - 1) / TM) * ((a.e.N + C - 1) / C);
     const int64_t grid = tiles + (FORM == FUSED_GRAD && a.dbias != nullptr ? (a.bias_n + 31) / 32 : 0);
     if (grid * NT >= (int64_t)1 << 32) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((fused_direct_kn_kernel<FORM, TM>), dim3((unsigned)grid), dim3(NT), 0, s, a);
+    hipLaunchKernelGGL((fused_direct_kn_kernel<FORM, TM, ANY>), dim3((unsigned)grid), dim3(NT), 0, s, a);
     return hipGetLastError();
 }
 
 // A gradient's 32 rows, two fragments each, gained nothing over 16 or over tiles (500 and 1000 x 512 over 4000
 // 29 and 39 us, tiles of 64 x 128 28 and 35).
-template <int FORM>
+template <int FORM, bool ANY>
 hipError_t launch(const FusedArgs& a, int tm, hipStream_t s) {
-    if (tm == 16) return launch_tile<FORM, 16>(a, s);
+    if (tm == 16) return launch_tile<FORM, 16, ANY>(a, s);
     if constexpr (FORM == FUSED_GRAD) return hipErrorInvalidValue;
-    else return launch_tile<FORM, 32>(a, s);
+    else return launch_tile<FORM, 32, ANY>(a, s);
+}
+
+template <int FORM>
+hipError_t launch(const FusedArgs& a, int tm, bool any, hipStream_t s) {
+    return any ? launch<FORM, true>(a, tm, s) : launch<FORM, false>(a, tm, s);
 }
 
 }  // namespace
 
-hipError_t launch_fused_direct_kn(const FusedArgs& a, int form, int tm, hipStream_t s) {
-    return form == FUSED_ONE ? launch<FUSED_ONE>(a, tm, s) : form == FUSED_PAIR ? launch<FUSED_PAIR>(a, tm, s) : launch<FUSED_GRAD>(a, tm, s);
+hipError_t launch_fused_direct_kn(const FusedArgs& a, int form, int tm, bool any, hipStream_t s) {
+    return form == FUSED_ONE ? launch<FUSED_ONE>(a, tm, any, s)
+           : form == FUSED_PAIR ? launch<FUSED_PAIR>(a, tm, any, s) : launch<FUSED_GRAD>(a, tm, any, s);
 }
 
 }  // namespace qg

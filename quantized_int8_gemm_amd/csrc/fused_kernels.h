@@ -62,7 +62,7 @@ hipError_t launch_fused_pad(const PadArgs& a, hipStream_t s);
 // checkpoint) of weights whose rows lie along the sum; any: rows of any alignment.
 hipError_t launch_fused_direct(const FusedArgs& a, int form, int tm, int tn, bool any, hipStream_t s);
 // Products of tm (16 or 32) rows by 64 columns of sums a workgroup of weights whose rows do not.
-hipError_t launch_fused_direct_kn(const FusedArgs& a, int form, int tm, hipStream_t s);
+hipError_t launch_fused_direct_kn(const FusedArgs& a, int form, int tm, bool any, hipStream_t s);
 
 // The second kernel of a divided sum.
 hipError_t launch_fused_join(const FusedArgs& a, int form, hipStream_t s);
