@@ -84,10 +84,11 @@ struct Shape {
 // 7.9), 1.04 to 1.5 through registers (1000 x 4095 x 4095 71; 1 x 4095 x 4095 gated 54).  A direct
 // workgroup takes its operands at 37 bytes a nanosecond (64 x 4096 x 4096 gated 15 us, 64 x 4096 x
 // 14336 34; 300 x 1008 x 1008 6.6), 35 transposed ones (202 x 1904 x 3024 12), 16 unaligned ones (4 x 4095
-// x 4095 gated 20; 27 of one [K,N] weight, 30 x 4095 x 4095 16), and faster where few run (30
-// workgroups, 151 x 96 x 4576 gated, [K,N], 8); a 257th takes as long as a second round (55 x 2064 x
-// 384 gated, [K,N], 260 of 16 x 32 8.0, 130 of 32 x 32 5.6); what it adds up through LDS bounds short
-// sums (1024 x 2816 x 64 gated 30 with 64 x 32, 33 with 32 x 32, tiles of 64 x 128 12).
+// x 4095 gated 20; 27 of one [K,N] weight, 30 x 4095 x 4095 16), and faster where few run
+// and L2 holds the weights (30 workgroups, 151 x 96 x 4576 gated, [K,N], 8; 49, 16 x 1552 x 5264, 18);
+// a 257th takes as long as a second round (55 x 2064 x 384 gated, [K,N], 260 of 16 x 32 8.0, 130 of
+// 32 x 32 5.6); what it adds up through LDS bounds short sums (1024 x 2816 x 64 gated 30 with 64 x
+// 32, 33 with 32 x 32, tiles of 64 x 128 12).
 double time_of(const Shape& s, int tile, int splits, bool pad) {
     const double chunks = (double)((s.K + 127) / 128 * s.branches);
     const double rows = (double)s.M * (s.form == qg::FUSED_GRAD ? 2 : 1), cols = (double)s.N * (s.form == qg::FUSED_PAIR ? 2 : 1);
@@ -95,7 +96,11 @@ double time_of(const Shape& s, int tile, int splits, bool pad) {
     auto tiles = [&](double bm, double bn) { return std::ceil(rows / bm) * std::ceil(cols / bn) * splits; };
     double t;
     switch (tile) {
-        case qg::FUSED_256x256: t = std::ceil(tiles(256, 256) / 256) * (per * 1.7 + 10); break;
+        case qg::FUSED_256x256: {   // the epilogues: 4096 x 8192 x 1024 with GELU 62 us, 56 with 128 x 128; gated 4096 x 14336 x 1024 184, 198
+            const double last = s.form == qg::FUSED_ONE ? 12.5 : s.form == qg::FUSED_PAIR ? 10 : 8;
+            t = std::ceil(tiles(256, 256) / 256) * (per * 1.7 + last);
+            break;
+        }
         case qg::FUSED_128x128: {
             const double n = tiles(128, 128), full = std::floor(n / 512), rest = n - 512 * full;
             t = full * (per * 1.1 + 4) + (rest > 256 ? per * 1.1 + 4 : rest > 0 ? per * 0.75 + 3 : 0);
@@ -110,7 +115,8 @@ double time_of(const Shape& s, int tile, int splits, bool pad) {
             const double a_rows = std::min<double>(tm, s.M) * (s.form == qg::FUSED_GRAD ? 2 : 1);
             const bool kn = tile >= DIRECT_KN, pair = s.form == qg::FUSED_PAIR;
             const double w_rows = pair && !kn ? 2 * tn : tn, out_cols = pair && kn ? tn / 2 : tn;
-            const double n = std::ceil(s.M / tm) * std::ceil(s.N / out_cols) / 256, alone = std::max(0.0, 1 - n);
+            const double n = std::ceil(s.M / tm) * std::ceil(s.N / out_cols) / 256;
+            const double alone = cols * (double)s.K * s.branches < 8e6 ? std::max(0.0, 1 - n) : 0;
             const double rate = !s.pieces && !pad ? (!kn || s.form == qg::FUSED_GRAD ? 16e3 : s.form == qg::FUSED_ONE ? 27e3 : 16e3 + 10e3 * alone) : kn ? 35e3 + (s.form == qg::FUSED_GRAD ? 0 : 25e3) * alone : 37e3 + 20e3 * alone;
             const double each = (a_rows + w_rows) * (double)s.K * s.branches / rate + 0.35;
             const double sums = tm * out_cols * (s.form == qg::FUSED_ONE ? 1 : 2);
