@@ -73,12 +73,15 @@ __device__ __forceinline__ void load_scales(const float* w, int stride, int c, i
 // two groups a lane: the factors stay in registers between the row's maximum and their
 // codes, the weights' scales, which every row needs again, lie in LDS, and the next row is on
 // its way meanwhile (4096 x 14336 gated 232 us with none of that, a row a workgroup).  Wider
-// rows are read, and their factors computed, again for the codes.
+// rows are read, and their factors computed, again for the codes, one group at a time, and
+// their sums for dbias lie in memory (300 x 60000 gated 361 us where the loops over groups were
+// unrolled and spilled, 101 so).
 template <typename T, int G, int ITER, bool PAIR, bool BIAS>
 __global__ __launch_bounds__(G < 256 ? 256 : G) void grad_rows_kernel(GradRowsArgs a) {
     constexpr int RPW = G < 256 ? 256 / G : 1;
     constexpr int H = PAIR ? 2 : 1;
     constexpr bool HOLD = ITER <= 2;
+    constexpr int TURNS = HOLD ? ITER : 1;   // unrolled where registers hold every group
     __shared__ uint32_t red[2][G < 64 ? 1 : G / 64];
     __shared__ float part[BIAS && RPW > 1 ? (RPW - 1) * G * ITER * 8 : 1];
     // a lane's own scales, four to a place: each lane reads what it wrote
@@ -86,9 +89,9 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void grad_rows_kernel(GradRowsAr
     const int t = threadIdx.x % G, group = threadIdx.x / G;
     const int N = a.N;
     auto place = [&](int h, int i, int half) { return ws + ((((group * H + h) * ITER + i) * 2 + half) * G + t) * 4; };
-    float db[BIAS ? ITER : 1][8];
+    float db[BIAS && HOLD ? ITER : 1][8];
 #pragma unroll
-    for (int i = 0; i < (BIAS ? ITER : 1); ++i)
+    for (int i = 0; i < (BIAS && HOLD ? ITER : 1); ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) db[i][e] = 0.f;
 
@@ -116,7 +119,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void grad_rows_kernel(GradRowsAr
         }
     };
     // The factors of group i with the weight's scales; dy is 0 past the last column.
-    auto factors = [&](const Row& row, int i, float (*v)[8], bool add) {
+    auto factors = [&](const Row& row, int i, float (*v)[8], bool add, bool first) {
         const int w = HOLD ? i : 0;
         if (a.ckpt[0] == nullptr) {
 #pragma unroll
@@ -138,9 +141,22 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void grad_rows_kernel(GradRowsAr
             });
         }
         if constexpr (BIAS) {
-            if (add) {
+            if constexpr (HOLD) {
+                if (add) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) db[i][e] += v[0][e];
+                    for (int e = 0; e < 8; ++e) db[i][e] += v[0][e];
+                }
+            } else if (add) {
+                // the workgroup's own partial sums, in L2
+                const int c = (i * G + t) * 8;
+                float* own = a.part + (int64_t)blockIdx.x * N + c;
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const int count = N - c - 4 * half;
+                    v4f sum = {v[0][4 * half], v[0][4 * half + 1], v[0][4 * half + 2], v[0][4 * half + 3]};
+                    if (!first) sum = load4(own + 4 * half, count) + sum;
+                    if (count > 0) store4(own + 4 * half, QG_FP32, count, sum);
+                }
             }
         }
 #pragma unroll
@@ -161,14 +177,14 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void grad_rows_kernel(GradRowsAr
         }
     };
     // red: two in turn, since a wave may be one row ahead of the others' reads
-    auto finish = [&](int64_t row, bool live, Row& v, int turn) {
+    auto finish = [&](int64_t row, bool live, Row& v, int turn, bool first) {
         float held[HOLD ? ITER : 1][H][8];
         uint32_t top = 0u;
-#pragma unroll
+#pragma unroll TURNS
         for (int i = 0; i < ITER; ++i) {
             float (*f)[8] = held[HOLD ? i : 0];
             if constexpr (!HOLD) fetch_group(live ? row : a.M - 1, v, i);
-            factors(v, i, f, live);
+            factors(v, i, f, live, first);
 #pragma unroll
             for (int h = 0; h < H; ++h)
 #pragma unroll
@@ -181,7 +197,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void grad_rows_kernel(GradRowsAr
         const float most = __uint_as_float(top), up = most < 0x1p-90f ? 0x1p60f : 1.0f;   // STEPS / most stays finite
         const float inv = top >= INF_BITS || top == 0u ? 0.f : STEPS / (most * up);
         if (t == 0) a.row_scale[row] = top >= INF_BITS ? __uint_as_float(0x7fc00000u) : most / STEPS;
-#pragma unroll
+#pragma unroll TURNS
         for (int i = 0; i < ITER; ++i) {
             const int c = (i * G + t) * 8;
             if (c >= a.np) continue;
@@ -189,7 +205,7 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void grad_rows_kernel(GradRowsAr
             if constexpr (!HOLD) {
                 __builtin_amdgcn_sched_barrier(0);
                 fetch_group(row, v, i);
-                factors(v, i, f, false);
+                factors(v, i, f, false, false);
             }
 #pragma unroll
             for (int h = 0; h < H; ++h) {
@@ -223,17 +239,18 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void grad_rows_kernel(GradRowsAr
             }
         for (int turn = 0; row - group < M; row += step, turn ^= 1) {
             if (row + step < M) fetch(row + step, next);
-            finish(row, row < M, now, turn);
+            finish(row, row < M, now, turn, false);
             now = next;
         }
     } else {
+        const int64_t first = row;
         for (int turn = 0; row - group < M; row += step, turn ^= 1) {
             const bool live = row < M;
             Row now;
-            finish(row, live, now, turn);
+            finish(row, live, now, turn, row == first);
         }
     }
-    if constexpr (BIAS) {
+    if constexpr (BIAS && HOLD) {
         if constexpr (RPW > 1) {
             if (group > 0) {
 #pragma unroll
@@ -276,10 +293,12 @@ hipError_t by_width(const GradRowsArgs& a, hipStream_t s) {
         hipLaunchKernelGGL((grad_rows_kernel<T, G, ITER, PAIR, BIAS>), dim3(grid), dim3(G < 256 ? 256 : G), 0, s, a); \
         done = true;                                                                                                \
     }
+    // One group a lane as far as lanes go: more waves, fewer registers (8192 x 2816, gated 82 -> 75 us with the
+    // product, linear 69 -> 62, of 512 x 1 after 256 x 2; 4096 x 8192 gated 97 -> 88 of 1024 x 1 after 512 x 2).
     QG_ROWS(64, 1, 512)
     QG_ROWS(256, 1, 2048)
-    QG_ROWS(256, 2, 4096)
-    QG_ROWS(512, 2, 8192)
+    QG_ROWS(512, 1, 4096)
+    QG_ROWS(1024, 1, 8192)
     QG_ROWS(1024, 2, 16384)
     QG_ROWS(1024, 4, 32768)
     QG_ROWS(1024, 8, 65536)
@@ -298,8 +317,9 @@ hipError_t by_form(const GradRowsArgs& a, bool pair, hipStream_t s) {
 
 // Workgroups of the row kernel where each leaves partial sums of dbias.
 int grad_rows_parts(int64_t M, int64_t N) {
-    // (few rows: one a compute unit and its partial sums fewer; 515 x 2816: 5.8 MB of them with 512)
-    const int64_t rows = N <= 512 ? 4 : 1, groups = (M + rows - 1) / rows, most = N > 8192 || M <= 1024 * rows ? 256 : 512;
+    // One to a compute unit for few rows and for wide ones, whose partial sums are many bytes (4096 x 8192
+    // 73 us with 256, 77 with 512).
+    const int64_t rows = N <= 512 ? 4 : 1, groups = (M + rows - 1) / rows, most = N > 4096 || M <= 1024 * rows ? 256 : 512;
     return (int)(groups < most ? groups : most);
 }
 

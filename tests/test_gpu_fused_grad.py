@@ -78,6 +78,25 @@ def test_gated_grad(shape, b_trans):
         check(dx, want, off + 2.0 ** -22 * np.abs(want), d)
 
 
+@pytest.mark.parametrize("m,n", [(2600, 300), (700, 2000), (1300, 4001), (600, 8001), (600, 16003), (600, 17003), (530, 40001)])
+def test_bias_over_more_rows_than_workgroups(m, n):
+    """Each workgroup of the factors' pass adds up several rows, of every width it is built for."""
+    k, d = 16, torch.bfloat16
+    case(f"bias {m} {n}")
+    _, (w,), _, (sw,) = inputs(m, n, k, m)
+    codes, scale = saved(m, n, 5)
+    dy, dyd = upstream(m, n, 6, d)
+    dx, db = q.qgemm_a8w8_linear_grad(dy, gpu(w), gpu(sw), (gpu(codes[0]), gpu(scale[0])), "silu", b_trans=True, bias_grad=True)
+    z = ref.values(codes[0], scale[0])
+    p = dyd * ref.slope("silu", z)
+    check(db, p.sum(0), (np.abs(p) * ((m + 4) * 2.0 ** -24 + 2.0 ** -20) + curve(dyd, 1 + np.abs(z))).sum(0), torch.float32)
+    want, off = ref.grad([p], [sw], [w], True)
+    off = off + curve(dyd, np.abs(sw.astype(np.float64)) * (1 + np.abs(z))) @ np.abs(w.astype(np.float64))
+    check(dx, want, off + 2.0 ** -22 * np.abs(want), d)
+    again = q.qgemm_a8w8_linear_grad(dy, gpu(w), gpu(sw), (gpu(codes[0]), gpu(scale[0])), "silu", b_trans=True, bias_grad=True)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], db)
+
+
 @pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
 def test_against_differences(act):
     """d/dt of sum(dy * out(x + t v)) at t = 0, from values of the forward pass in 64 bits.
