@@ -175,7 +175,9 @@ hipError_t launch_tile(const FusedArgs& a, bool any, hipStream_t s) {
     const int64_t tiles = (int64_t)((a.e.M + TM - 1) / TM) * ((a.e.N + TN - 1) / TN);
     const int64_t grid = tiles + (FORM == FUSED_GRAD && a.dbias != nullptr ? (a.bias_n + 31) / 32 : 0);
     if (grid * NT >= (int64_t)1 << 32) return hipErrorInvalidValue;
-    if (any) hipLaunchKernelGGL((fused_direct_kernel<FORM, TM, TN, 2, true>), dim3((unsigned)grid), dim3(NT), 0, s, a);
+    // one step ahead where two would spill
+    constexpr int ANY_NB = FORM != FUSED_ONE && TM * TN == 64 * 32 ? 1 : 2;
+    if (any) hipLaunchKernelGGL((fused_direct_kernel<FORM, TM, TN, ANY_NB, true>), dim3((unsigned)grid), dim3(NT), 0, s, a);
     else hipLaunchKernelGGL((fused_direct_kernel<FORM, TM, TN, NB, false>), dim3((unsigned)grid), dim3(NT), 0, s, a);
     return hipGetLastError();
 }
