@@ -35,7 +35,10 @@ extern "C" {
 /* act(z), in fp32:
  *   NONE z;  RELU max(z, 0);  SILU z / (1 + exp(-z));
  *   GELU z (1 + erf(z / sqrt 2)) / 2;
- *   GELU_TANH z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+ *   GELU_TANH z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2
+ * The exponential and the reciprocal are the hardware's.  Off by at most, relative to the
+ * value: SILU (|z| + 4) 2^-23; GELU (z^2 + 5) 2^-23; GELU_TANH (|y| + 2) 2^-21, with
+ * y = sqrt(8 / pi) (z + 0.044715 z^3); magnitudes below 2^-119 may be given as 0. */
 typedef enum {
     QG_ACT_NONE = 0, QG_ACT_RELU = 1, QG_ACT_SILU = 2, QG_ACT_GELU = 3, QG_ACT_GELU_TANH = 4
 } qg_activation;

@@ -15,17 +15,27 @@ __device__ __forceinline__ float sigmoid(float z) {
     return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(z * -1.44269504f));
 }
 
-// The normal distribution's Phi(z) = (1 + erf(z / sqrt 2)) / 2 from density = exp(-z^2 / 2): with
-// x = |z| / sqrt 2 and t = 1 / (1 + 0.3275911 x), erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2), to 1.5e-7
-// (Abramowitz and Stegun 7.1.26); 13 instructions where erff takes about 40, which is
-// most of a checkpointed product's epilogue.
+// The normal distribution's Phi(z) = (1 + erf(z / sqrt 2)) / 2 from density = exp(-z^2 / 2).  With
+// a = |z|, t = 1 / (1 + 0.265 a) and w = a t, Phi(-a) = density t P(w): P is the polynomial of
+// degree 8 whose largest relative error over 0 .. 16 is least (2.0e-8, found by exchange of its
+// extrema).  Past 16 the density is 0.  w, unlike t, keeps its own significand next to zero, where P
+// is 1/2 less a multiple of w, so that Phi is off by 3 2^-24 at most there; and no sum of
+// like magnitudes cancels for z < 0, where Phi keeps (z^2 + 4) 2^-23 of itself, most of it the
+// density's exponent.  (1 + erf in fp32 keeps 2^-24 of 1 there: nothing at all from -5.5 on.)  A
+// formula of five terms, to 1.5e-7 of 1, saves six instructions: 4096 x 8192 x 2048 forward with a
+// checkpoint and back 245 us, 252 with this one; 300 x 5001 x 2048 10.4 and 10.8.
 __device__ __forceinline__ float normal_cdf(float z, float density) {
-    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.23164190f, __builtin_fabsf(z), 1.0f));
-    float q = __builtin_fmaf(t, 0.53070271f, -0.72657601f);
-    q = __builtin_fmaf(t, q, 0.71070687f);
-    q = __builtin_fmaf(t, q, -0.14224837f);
-    q = __builtin_fmaf(t, q, 0.12741480f);
-    q = q * t * density;   // erfc(x) / 2
+    const float a = __builtin_fminf(__builtin_fabsf(z), 16.0f);   // 16 for a NaN, which the density holds
+    const float t = __builtin_amdgcn_rcpf(__builtin_fmaf(0.265f, a, 1.0f)), w = a * t;
+    float q = __builtin_fmaf(w, 7.317133849937818e-07f, -9.171379133476876e-06f);
+    q = __builtin_fmaf(w, q, 2.353733179916162e-05f);
+    q = __builtin_fmaf(w, q, 1.497743214713410e-04f);
+    q = __builtin_fmaf(w, q, -3.358556423336267e-04f);
+    q = __builtin_fmaf(w, q, -8.980181999504566e-03f);
+    q = __builtin_fmaf(w, q, 7.367415726184845e-02f);
+    q = __builtin_fmaf(w, q, -2.664422392845154e-01f);
+    q = __builtin_fmaf(w, q, 0.5f);
+    q = q * t * density;   // Phi(-a)
     return z < 0.f ? q : 1.0f - q;
 }
 
