@@ -120,7 +120,8 @@ __device__ __forceinline__ uint32_t pack_bytes(uint32_t a, uint32_t b, uint32_t 
 }
 
 // From the bits of the largest magnitude: codes are rint((v * up) * inv).  A NaN or an
-// infinity makes inv 0, and its own product with that a NaN, whose low bits are 0.
+// infinity makes inv 0, and so do zeros alone: then every code is 0 (a NaN's product with 0
+// would keep the NaN's own low bits).
 struct Int8Form {
     float inv, scale, up = 1.0f;
     // 2^-100 .. 2^120; outside: zeros, 127 / most not finite or its reciprocal not normal, most not
@@ -144,7 +145,8 @@ struct Int8Form {
             c *= up;
             d *= up;
         }
-        return pack_bytes(nearest_bits(a * inv), nearest_bits(b * inv), nearest_bits(c * inv), nearest_bits(d * inv));
+        const uint32_t w = pack_bytes(nearest_bits(a * inv), nearest_bits(b * inv), nearest_bits(c * inv), nearest_bits(d * inv));
+        return inv == 0.f ? 0u : w;
     }
 };
 

@@ -193,7 +193,8 @@ __global__ __launch_bounds__(G < 256 ? 256 : G) void grad_rows_kernel(GradRowsAr
         }
         top = row_max<G>(top, red[turn]);
         if (!live) return;
-        // a NaN or an infinity makes inv 0, and its own product a NaN, whose low bits are 0
+        // a NaN or an infinity makes the row's scale NaN, and so every output of the row, whatever
+        // its planes then hold (int8 values like any)
         const float most = __uint_as_float(top), up = most < 0x1p-90f ? 0x1p60f : 1.0f;   // STEPS / most stays finite
         const float inv = top >= INF_BITS || top == 0u ? 0.f : STEPS / (most * up);
         if (t == 0) a.row_scale[row] = top >= INF_BITS ? __uint_as_float(0x7fc00000u) : most / STEPS;
