@@ -8,7 +8,10 @@
  * row-major matrices with a leading dimension in elements, every call
  * asynchronous on `stream`, arguments checked on the host before any launch,
  * the same status codes, and qgemm_last_kernel() names what was launched.  A call
- * whose outputs have no elements checks its sizes only and launches nothing.
+ * whose outputs have no rows (M = 0) or, of the products, no columns (N = 0) checks its
+ * sizes only and launches nothing (but M = 0 clears a dbias).  With rows, K = 0, for the
+ * gradients N = 0 too, and for int8_quantize and int8_dequantize n < 1, are
+ * QG_ERR_INVALID_ARGUMENT, whether anything would be written or not.
  * int8 sums wrap mod 2^32, as qgemm_a8w8's do.
  *
  * int8 form: the values t of a row, or of each block of 32 columns of it (the
