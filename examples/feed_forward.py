@@ -39,7 +39,10 @@ class FeedForward(torch.nn.Module):
             self.register_buffer(name + "_scale", scale)
 
     def forward(self, x, residual):
-        """(output, h): h = x + residual is the stream that the block adds to."""
+        """(output, h): h = x + residual is the stream that the block adds to.  x: bf16 or fp16,
+        which the gradients take; serve takes fp32 too."""
+        if x.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError(f"x has dtype {x.dtype}; training through the block takes torch.bfloat16 or torch.float16")
         return _Step.apply(x, residual, self.gain, self)
 
     def serve(self, x, residual):

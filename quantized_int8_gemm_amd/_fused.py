@@ -63,7 +63,8 @@ def qgemm_a8w8_linear(A, W, act_scale, weight_scale, bias=None, activation=None,
     residual: [M, N] of out_dtype; out may be the residual itself.  out_dtype:
     torch.float32, bfloat16 or float16.  With checkpoint=True returns (out, saved):
     saved = (codes int8 [M, N], scale fp32 [M, ceil(N / 32)]) holds z in int8 form by
-    blocks of 32 columns, for qgemm_a8w8_linear_grad."""
+    blocks of 32 columns, for qgemm_a8w8_linear_grad (which takes the upstream gradient in
+    bf16 or fp16, whatever out_dtype was)."""
     return _fused_binding.linear(A, W, act_scale, weight_scale, bias, activation, residual, out_dtype, b_trans, checkpoint, out)
 
 
@@ -77,7 +78,8 @@ def qgemm_a8w8_gated(A, W_gate, W_up, act_scale, gate_scale, up_scale, activatio
     scalar; activation, out_dtype: as qgemm_a8w8_linear.  With checkpoint=True
     returns (out, saved): saved = (codes int8 [2, M, N], scale fp32 [2, M,
     ceil(N / 32)]) holds g and u in int8 form by blocks of 32 columns, for
-    qgemm_a8w8_gated_grad."""
+    qgemm_a8w8_gated_grad (which takes the upstream gradient in bf16 or fp16, whatever
+    out_dtype was)."""
     return _fused_binding.gated(A, W_gate, W_up, act_scale, gate_scale, up_scale, activation, out_dtype, b_trans, checkpoint, out)
 
 
