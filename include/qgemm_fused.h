@@ -130,6 +130,7 @@ qg_status qgemm_a8w8_gated(int64_t M, int64_t N, int64_t K,
  *   dy: QG_BF16 or QG_FP16 [M,N]; dx: [M,K] of that type.
  *   checkpoint, checkpoint_scale: as the forward call left them.  For the linear
  *     form with QG_ACT_NONE both may be NULL.
+ *   activation: the forward call's, which the checkpoint does not hold.
  *   dbias: fp32 [N], or NULL.  Its sums are fp32 in a fixed order.
  * Results repeat bit for bit.  N > QG_A8W8_GRAD_MAX_COLUMNS is
  * QG_ERR_UNSUPPORTED.  M == 0 writes dbias = 0.

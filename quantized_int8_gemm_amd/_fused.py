@@ -7,6 +7,10 @@ As in the binding of the norm and MX calls, each function checks dtypes
 and calls the C entry point on torch's current stream, in an extension module
 (_fused_binding, csrc/fused_binding.cpp).  Where the module is missing, each call
 raises ImportError.
+
+As everywhere in this package, nothing is recorded for autograd: outputs do not require
+grad, whatever the inputs do, and a program calls the gradients itself, as in a
+torch.autograd.Function (examples/feed_forward.py).
 """
 import ctypes
 
@@ -89,7 +93,8 @@ def qgemm_a8w8_linear_grad(dy, W, weight_scale, checkpoint=None, activation=None
     dx[m, k] = sum_n (dy act'(z) weight_scale)[m, n] W[k, n], z as the checkpoint holds it.
 
     dy: bf16 or fp16 [M, N]; checkpoint: the forward call's saved pair (not needed
-    without an activation).  Returns dx [M, K] of dy's dtype, or with bias_grad=True
+    without an activation); activation: the forward call's, which the pair does not
+    hold (None gives the gradient of the product alone).  Returns dx [M, K] of dy's dtype, or with bias_grad=True
     (dx, dbias): dbias fp32 [N].  The residual's gradient is dy itself.  The factors
     are held in 16-bit fixed point per row, sums over n are exact; results repeat bit
     for bit."""
