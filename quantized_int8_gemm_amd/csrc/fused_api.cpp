@@ -96,7 +96,7 @@ double time_of(const Shape& s, int tile, int splits, bool pad) {
     auto tiles = [&](double bm, double bn) { return std::ceil(rows / bm) * std::ceil(cols / bn) * splits; };
     double t;
     switch (tile) {
-        case qg::FUSED_256x256: {   // the epilogues: 4096 x 8192 x 1024 with GELU 62 us, 56 with 128 x 128; gated 4096 x 14336 x 1024 184, 198
+        case qg::FUSED_256x256: {   // the epilogues: 4096 x 8192 x 1024 with GELU 72 us, 67 with 128 x 128; gated 4096 x 14336 x 1024 184, 198
             const double last = s.form == qg::FUSED_ONE ? 12.5 : s.form == qg::FUSED_PAIR ? 10 : 8;
             t = std::ceil(tiles(256, 256) / 256) * (per * 1.7 + last);
             break;
